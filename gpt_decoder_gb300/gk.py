@@ -19,7 +19,7 @@ _lib = ct.CDLL(LIB_PATH)
 # status codes and enums (include/gk.h)
 GK_OK, GK_ERR_ARG, GK_ERR_ALIGN, GK_ERR_UNSUPPORTED, GK_ERR_CUDA, GK_ERR_TIMEOUT, GK_ERR_OVERFLOW, GK_ERR_INDEX, \
     GK_ERR_WORKSPACE, GK_ERR_IO, GK_ERR_FORMAT = range(11)
-GK_F32, GK_BF16, GK_BF16X2 = 0, 1, 2
+GK_F32, GK_BF16, GK_BF16X2, GK_I8 = 0, 1, 2, 3
 GK_MATH_FP32, GK_MATH_3XTF32 = 0, 1
 GK_ACT_NONE, GK_ACT_GELU = 0, 1
 (GK_T_WTE, GK_T_WPE, GK_T_LN1_W, GK_T_LN1_B, GK_T_ATTN_W, GK_T_ATTN_B, GK_T_ATTNPROJ_W, GK_T_ATTNPROJ_B,
@@ -49,6 +49,11 @@ class gk_gpt_cfg(ct.Structure):
 
 class gk_sample_cfg(ct.Structure):
     _fields_ = [("top_k", I32), ("temperature", F32), ("seed", ct.c_uint64), ("counter", ct.c_uint64)]
+
+
+class gk_paged_kv(ct.Structure):
+    _fields_ = [("k", P), ("v", P), ("k_scale", P), ("v_scale", P), ("page_table", P), ("kv_len", P), ("n_pages", I64),
+                ("ld_table", I64), ("dtype", I32), ("Hkv", I32), ("page_size", I32), ("hs", I32), ("max_pages", I32)]
 
 
 _SIGS = {
@@ -101,6 +106,12 @@ _SIGS = {
     "gk_prefill": (I32, [P, P, P, P, I32, P]),
     "gk_decode_step": (I32, [P, P, P, P, P, P, ct.POINTER(gk_sample_cfg)]),
     "gk_sample": (I32, [P, P, P, I64, P, ct.POINTER(gk_sample_cfg)]),
+    "gk_paged_write": (I32, [P, ct.POINTER(gk_paged_kv), I32, P, I64, P, I64, P, I32, I64]),
+    "gk_paged_read": (I32, [P, ct.POINTER(gk_paged_kv), I32, P, I64, P, I64, P, I32, I64]),
+    "gk_paged_attn": (I32, [P, ct.POINTER(gk_paged_kv), I32, P, I64, P, I64, P, P, I32, I32, I64, I32, F32]),
+    "gk_quant_w4": (I32, [P, P, I64, I32, P, P, I32, I64, I64]),
+    "gk_matvec_w4": (I32, [P, I32, P, I64, P, P, I32, P, P, I64, P, I64, I32, I64, I64, I64]),
+    "gk_sample_rows": (I32, [P, I32, P, I64, I64, I32, P, P, P, P, P, P, P]),
     "gk_st_open": (I32, [ct.c_char_p, ct.POINTER(P)]),
     "gk_st_close": (None, [P]),
     "gk_st_count": (I32, [P]),
@@ -408,6 +419,70 @@ def gk_sgd_step(ctx, p, g, n, lr):
 def gk_sample(ctx, kv, logits, ld, next_ids, sample=None):
     return _check(ctx, _lib.gk_sample(ctx.handle, kv.handle, _p(logits), ld, _p(next_ids), _sample(sample)),
                   "gk_sample")
+
+
+# ---- serving: the paged cache, attention over it, 4-bit weights, filtered sampling
+class PagedKv:
+    """A paged cache (gk_paged_kv) over the caller's tensors: k, v contiguous [n_pages, Hkv, page_size, hs],
+    bfloat16 or int8 with float32 scales [n_pages, Hkv, page_size]; page_table int32 [B, max_pages] and kv_len
+    int32 [B] on the device. It keeps references to them, and their contents may change between calls."""
+
+    def __init__(self, k, v, k_scale, v_scale, page_table, kv_len):
+        n_pages, Hkv, page_size, hs = k.shape
+        if v.shape != k.shape or v.dtype != k.dtype or not (k.is_contiguous() and v.is_contiguous()):
+            raise ValueError("PagedKv: k and v must be contiguous, of one shape and type")
+        dtype = {"torch.bfloat16": GK_BF16, "torch.int8": GK_I8}.get(str(k.dtype))
+        if dtype is None or (dtype == GK_I8) != (k_scale is not None) or (dtype == GK_I8) != (v_scale is not None):
+            raise ValueError("PagedKv: bfloat16 pages, or int8 pages with scales")
+        for s in (k_scale, v_scale):
+            if s is not None and (s.shape != k.shape[:3] or not s.is_contiguous() or str(s.dtype) != "torch.float32"):
+                raise ValueError("PagedKv: scales must be contiguous float32 [n_pages, Hkv, page_size]")
+        for t in (page_table, kv_len):
+            if str(t.dtype) != "torch.int32" or t.stride(-1) != 1:
+                raise ValueError("PagedKv: page_table and kv_len are int32 with unit stride")
+        if page_table.dim() != 2 or kv_len.dim() != 1:
+            raise ValueError("PagedKv: page_table is [B, max_pages], kv_len [B]")
+        self.tensors = (k, v, k_scale, v_scale, page_table, kv_len)
+        self.B = min(page_table.shape[0], kv_len.shape[0])
+        self.struct = gk_paged_kv(_p(k), _p(v), _p(k_scale), _p(v_scale), _p(page_table), _p(kv_len), n_pages,
+                                  page_table.stride(0), dtype, Hkv, page_size, hs, page_table.shape[1])
+        self._as_parameter_ = ct.byref(self.struct)
+
+
+def _batch(cache, B, where):
+    if B > cache.B:
+        raise ValueError(f"{where}: batch {B} over a cache of {cache.B} sequences")
+    return cache._as_parameter_
+
+
+def gk_paged_write(ctx, cache, dtype, k, ldk, v, ldv, q_start, B, rows):
+    return _check(ctx, _lib.gk_paged_write(ctx.handle, _batch(cache, B, "gk_paged_write"), dtype, _p(k), ldk, _p(v),
+                                           ldv, _p(q_start), B, rows), "gk_paged_write")
+
+
+def gk_paged_read(ctx, cache, dtype, k, ldk, v, ldv, q_start, B, rows):
+    return _check(ctx, _lib.gk_paged_read(ctx.handle, _batch(cache, B, "gk_paged_read"), dtype, _p(k), ldk, _p(v),
+                                          ldv, _p(q_start), B, rows), "gk_paged_read")
+
+
+def gk_paged_attn(ctx, cache, dtype, q, ldq, y, ldy, lse, q_start, B, H, rows, max_q, scale):
+    return _check(ctx, _lib.gk_paged_attn(ctx.handle, _batch(cache, B, "gk_paged_attn"), dtype, _p(q), ldq, _p(y),
+                                          ldy, _p(lse), _p(q_start), B, H, rows, max_q, scale), "gk_paged_attn")
+
+
+def gk_quant_w4(ctx, W, ldw, transW, Wq, scales, group, K, M):
+    return _check(ctx, _lib.gk_quant_w4(ctx.handle, _p(W), ldw, int(transW), _p(Wq), _p(scales), group, K, M),
+                  "gk_quant_w4")
+
+
+def gk_matvec_w4(ctx, dtype, X, ldx, Wq, scales, group, bias, residual, ldr, Y, ldy, y_dtype, N, K, M):
+    return _check(ctx, _lib.gk_matvec_w4(ctx.handle, dtype, _p(X), ldx, _p(Wq), _p(scales), group, _p(bias),
+                                         _p(residual), ldr, _p(Y), ldy, y_dtype, N, K, M), "gk_matvec_w4")
+
+
+def gk_sample_rows(ctx, dtype, logits, ld, rows, V, u, temperature, top_k, top_p, min_p, next_ids, prob=None):
+    return _check(ctx, _lib.gk_sample_rows(ctx.handle, dtype, _p(logits), ld, rows, V, _p(u), _p(temperature),
+                                           _p(top_k), _p(top_p), _p(min_p), _p(next_ids), _p(prob)), "gk_sample_rows")
 
 
 # ---- safetensors files of float32 tensors (host code in libgk; arrays on the host or the GPU)

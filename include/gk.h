@@ -50,7 +50,7 @@ enum {
     GK_ERR_FORMAT = 10      /* a malformed file, or a dtype this build does not read */
 };
 
-enum { GK_F32 = 0, GK_BF16 = 1, GK_BF16X2 = 2 };
+enum { GK_F32 = 0, GK_BF16 = 1, GK_BF16X2 = 2, GK_I8 = 3 }; /* GK_I8: a paged cache's codes only */
 /* Arithmetic of the products with float32 operands (the faithful mode):
  *   GK_MATH_3XTF32 (default): each operand x is split into TF32 parts hi = tf32(x) and
  *     lo = tf32(x - hi) (about 22 significant bits together), and the product is
@@ -392,6 +392,124 @@ gk_status gk_generate_uncached(gk_ctx* ctx, const float* params, gk_kv* kv, int3
  * index s is the cache's selection count, which this advances by one. */
 gk_status gk_sample(gk_ctx* ctx, gk_kv* kv, const float* logits, int64_t ld, int32_t* next,
                     const gk_sample_cfg* s);
+
+/* ---------------------------------------------------------------- serving: the paged cache */
+
+/* A key / value cache in pages, for batches of sequences of unequal lengths ([LM4] "Generation
+ * with a KV cache": one key and value row per position; here in pages that sequences share a
+ * pool of). The caller owns every array; a call copies this host struct, and the device arrays
+ * it points at are read when the call's kernels run.
+ *   k, v       [n_pages][Hkv][page_size][hs], contiguous, 16-byte aligned: GK_BF16 values or
+ *              GK_I8 codes (dtype).
+ *   k_scale, v_scale  GK_I8: float32 [n_pages][Hkv][page_size], the value of one code step of
+ *              that token and head (16-byte aligned); NULL for GK_BF16.
+ *   page_table device int32 [B][max_pages] (row stride ld_table): token position p of sequence b
+ *              is row p % page_size of page page_table[b][p / page_size].
+ *   kv_len     device int32 [B]: tokens of each sequence, those of the current call included.
+ * page_size is 16, 32, 64, 128 or 256; hs a multiple of 16, 16 .. 128.
+ *
+ * The three gk_paged_* calls below take `rows` token rows of B sequences packed one after the
+ * other: sequence b has rows q_start[b] .. q_start[b+1]-1 (device int32 [B+1], ascending from 0;
+ * a sequence may have none), and row i of its n sits at position kv_len[b] - n + i: the rows are
+ * the sequence's last n tokens. A position below zero is padding (a padded batch's dead row has
+ * kv_len 0). Rows from q_start[B] on belong to no sequence: they are not read, and the outputs'
+ * rows there are left as they were. What cannot be true on the device is refused there: a
+ * position at or past max_pages * page_size, or a page id outside [0, n_pages), is never followed;
+ * it records GK_ERR_INDEX (gk_sync), a token there is not stored, reads back as zeros, and
+ * counts as not visible to attention. Pages that one call writes must not be shared by two of
+ * its sequences at the same position (the order of the two stores would be open).
+ * Every call needs the context's device to be current (GK_ERR_ARG). No call is affected by what
+ * the cache holds outside the positions that it names. */
+typedef struct {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    const int32_t* page_table;
+    const int32_t* kv_len;
+    int64_t n_pages;
+    int64_t ld_table;
+    int dtype, Hkv, page_size, hs, max_pages;
+} gk_paged_kv;
+
+/* Store token rows k, v (dtype GK_F32 or GK_BF16; head h of a row at columns h*hs ..; row strides
+ * ldk, ldv in elements, a multiple of 8; 16-byte aligned) at their positions. GK_BF16 caches
+ * round to nearest even. GK_I8 caches keep, per token and head, with amax = max |x|:
+ *   scale = amax / 127,  code = rint(x * (127 / amax))   (float32, ties to even),
+ * so a value is off by at most half a step (amax / 254). A vector with amax < 2^-100 is stored as
+ * zeros with scale 0; one that holds an infinity or a NaN is stored as zeros with scale NaN, so
+ * that it reads back as NaN. Rows at a negative position are not stored. */
+gk_status gk_paged_write(gk_ctx* ctx, const gk_paged_kv* cache, int dtype, const void* k, int64_t ldk,
+                         const void* v, int64_t ldv, const int32_t* q_start, int B, int64_t rows);
+
+/* The inverse: k, v (dtype GK_F32 or GK_BF16, layout as above) receive the cached tokens at the
+ * rows' positions: code * scale in float32, rounded once for GK_BF16. With n = kv_len a whole
+ * sequence is read. Rows at a negative position read as zeros. */
+gk_status gk_paged_read(gk_ctx* ctx, const gk_paged_kv* cache, int dtype, void* k, int64_t ldk, void* v,
+                        int64_t ldv, const int32_t* q_start, int B, int64_t rows);
+
+/* Attention of new tokens over the cache, which already holds them (gk_paged_write first): query
+ * row i at position p sees the cached positions 0 .. p of its sequence. Head h of q attends with
+ * key / value head h / (H / Hkv) (H a multiple of Hkv):
+ *   y[i, h] = sum_{j <= p} softmax_j(scale q[i, h] . k[j]) v[j].
+ *   dtype   GK_BF16 (GK_ERR_UNSUPPORTED otherwise): q and y, bf16 [rows, H*hs] with row strides ldq,
+ *           ldy (multiples of 8, 16-byte aligned). Scores, softmax and sums are float32.
+ *   lse     float32 [rows, H] or NULL: the natural log-sum-exp of the scaled scores.
+ *   max_q   at least every sequence's number of rows (host; it sizes the launch). A sequence with
+ *           more rows than max_q records GK_ERR_INDEX and its rows are left as they were.
+ *   scale   finite.
+ * A row that sees nothing (a negative position) gets y = 0 and lse = -inf. Keys and values that a
+ * row does not see never reach it, whatever they hold (infinities and NaN among it). Long
+ * sequences are split over the GPU and joined through the context's workspace: the more of it
+ * there is the more they split, and any size will do. */
+gk_status gk_paged_attn(gk_ctx* ctx, const gk_paged_kv* cache, int dtype, const void* q, int64_t ldq,
+                        void* y, int64_t ldy, float* lse, const int32_t* q_start, int B, int H,
+                        int64_t rows, int max_q, float scale);
+
+/* ------------------------------------------------------------- serving: 4-bit weights */
+
+/* 4-bit weights of a Linear: Wq uint8 [M, K/2], row m holding output m's K codes two to a byte
+ * (even k in the low half), scales bf16 [M, K/group]; code c of group k / group stands for
+ * (c - 8) * scale. group is 32, 64 or 128 and divides K. Wq 16-byte aligned, scales 2-byte.
+ * gk_quant_w4 makes them from float32 W, [K, M] (transW = 0, the layout of [LM4]'s Linear weights)
+ * or [M, K] (transW = 1), row stride ldw: per output and group scale = bf16(max |w| / 7) and
+ * code = 8 + rint(w / scale) held to 1 .. 15; a group of zeros gets scale 0 and code 8, and one
+ * that holds an infinity or a NaN scale NaN and code 8. */
+gk_status gk_quant_w4(gk_ctx* ctx, const float* W, int64_t ldw, int transW, uint8_t* Wq, uint16_t* scales,
+                      int group, int64_t K, int64_t M);
+
+/* Y = X W^T + bias + residual for a few rows: X [N, K], 1 <= N <= 32 (GK_ERR_UNSUPPORTED above:
+ * gk_matmul_fwd is for those), W [M, K] in 4 bits as above.
+ *   dtype     GK_BF16 (X, row stride ldx a multiple of 8, 16-byte aligned); else GK_ERR_UNSUPPORTED.
+ *   bias      float32 [M] or NULL.  residual  float32 [N, M] (stride ldr) or NULL; it may alias Y
+ *             when y_dtype is GK_F32 and ldr == ldy.
+ *   y_dtype   GK_F32 or GK_BF16 (stride ldy).
+ * The codes' products are exact in float32; sums and the scales are float32, and the result is
+ * rounded once. The sum's order is fixed: the same call gives the same bits. */
+gk_status gk_matvec_w4(gk_ctx* ctx, int dtype, const void* X, int64_t ldx, const uint8_t* Wq,
+                       const uint16_t* scales, int group, const float* bias, const float* residual,
+                       int64_t ldr, void* Y, int64_t ldy, int y_dtype, int64_t N, int64_t K, int64_t M);
+
+/* --------------------------------------------------------------- serving: sampling */
+
+/* Pick one token per row of logits [rows, V] (GK_F32 or GK_BF16, row stride ld) from given uniform
+ * numbers, every row with filters of its own ([LM4] "Temperature and top-k", and the nucleus and
+ * min-p filters beside it). Device arrays [rows], each NULL for "off":
+ *   u            uniform in [0, 1) (required).
+ *   temperature  T; T <= 0 or NaN is greedy (the lowest index of the largest logit, prob 1). NULL: 1.
+ *   top_k        keeps the logits >= the k-th largest (ties with it kept); <= 0 or >= V: off.
+ *   top_p        keeps the fewest largest logits whose weights reach the share p of what top_k
+ *                left (ties with the last kept); >= 1 or NaN: off; <= 0 keeps the largest alone.
+ *   min_p        keeps weights of at least min_p times the largest; <= 0 or NaN: off.
+ * With w_i = exp((l_i - max) / T) the pick is the first kept index, ascending, whose running sum of
+ * w exceeds u times the kept total (the last kept index with a weight if none does). The largest logit is always
+ * kept. Weights are held to about 2^-45 of the largest and summed as integers, so results do
+ * not depend on any order. A NaN logit is never picked and counts as -inf; if the largest is
+ * +inf, those share the whole weight. A row with no logit above -inf gets next = -1, prob = 0.
+ *   next  int32 [rows];  prob  float32 [rows] or NULL: the pick's share of the kept weights. */
+gk_status gk_sample_rows(gk_ctx* ctx, int dtype, const void* logits, int64_t ld, int64_t rows, int V,
+                         const float* u, const float* temperature, const int32_t* top_k,
+                         const float* top_p, const float* min_p, int32_t* next, float* prob);
 
 /* ---- Generic ops of the autograd engine and plain SGD ([LM1] "Build a language model in C#
  * from scratch (1)": Ops, the op table (Add with broadcast, Scale, Sum, Tanh), "Why += and not =",
