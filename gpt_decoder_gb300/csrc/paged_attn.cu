@@ -1,88 +1,492 @@
-// Attention of new tokens over the paged cache.
+// Attention of a few new tokens over the paged cache (decoding): the entry point, the kernel for
+// up to 64 query rows per key / value head, and the joining of split sequences.
 // [LM4] = "Build a language model in C# from scratch (4): running GPT-2 weights", "Generation with
 // a KV cache" (the new tokens' queries against every cached position, no mask but the order).
 //
-// One warp per (token row, head): the keys one after the other, each lane four elements of the
-// head, with a running maximum m and sum l of the softmax (o and l rescaled when m moves).
+// y_i = sum_j p_ij v_j with p_ij = 2^(s_ij - m_i) / l_i, s = scale log2(e) q k. One pass over the
+// keys with a running reference m (moved, and o and l rescaled, only when a score passes it by more than
+// 8, so weights stay below 2^8) and sum l.
+//
+// With few rows the bytes of the cache are what counts, so each is read once, straight into
+// registers in the order that the matrix instructions take, with no shared memory between: the
+// products are computed transposed, S^T = K Q^T and O^T = V^T P^T (mma.sync m16n8k16), with 16
+// keys (dims) as the rows and 8 query rows as the columns, so that one decoded token with up to 8
+// heads a key / value head wastes nothing. The elements that a thread holds of a K row are 16
+// contiguous bytes; Q is loaded in the same order, so the permutation of the summed index cancels.
+// Of V it holds 16 bytes of four keys, paired by byte permutes. (tcgen05 takes its operands from
+// shared memory in tiles of 128 rows: at these few rows it would compute 16 times what is needed
+// and every byte would make the trip through shared memory.)
+//   rows per key / value head: all H / Hkv heads of all n queries; row i is query i / G, head i % G.
+//   A warp takes 8 or 16 rows (NT = 1, 2) and every KG-th tile of 16 keys; up to 64 rows are 4
+//   warps of the block next to each other, which read the same keys (L1 serves three of them).
+// 8-bit codes become bf16 exactly (|code| < 2^7): (code & 0x7f | 0x4300) is 128 + the low bits, and
+// (code & 0x80 | 0x4300) is 128 or 256, so their difference is the code. The key's scale multiplies
+// the score, the value's scale the weight.
+// Weights are split into two bf16 parts (hi + lo: 16 significant bits), so the result carries no
+// rounding but the output's.
 #include <math.h>
 
-#include "paged.cuh"
+#include <algorithm>
+
+#include "paged_attn.cuh"
 
 namespace gk {
 namespace {
 
-constexpr int THREADS = 128;
+constexpr int WARPS = 4;
 
-struct AttnArgs {
-    Pages p;
-    const __nv_bfloat16* q;
-    __nv_bfloat16* y;
-    float* lse;
-    const int32_t* q_start;
-    int64_t ldq, ldy;
-    int B, H, rows, max_q;
-    float scale;
-    int* err;
-};
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
-template <bool Q8>
-__global__ void __launch_bounds__(THREADS) paged_attn_kernel(AttnArgs a) {
-    const int64_t w = (int64_t)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    const int r = (int)(w / a.H), h = (int)(w % a.H);
-    if (r >= a.rows) return;
+// D += A B, bf16 operands, float32 accumulators: A 16x16, B 16x8.
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Transpose an 8x8 matrix of 16-bit elements held one row per four lanes.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&t);
+}
+// The codes in bytes 0 and 2 of x as a pair of bf16.
+__device__ __forceinline__ uint32_t codes02(uint32_t x) {
+    const uint32_t a = (x & 0x007f007fu) | 0x43004300u, b = (x & 0x00800080u) | 0x43004300u;
+    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&d);
+}
+// Zero the infinities and NaN of a bf16 pair; true if there were any.
+__device__ __forceinline__ bool drop_odd(uint32_t& x) {
+    const bool lo = (x & 0x7f80u) == 0x7f80u, hi = (x & 0x7f800000u) == 0x7f800000u;
+    if (lo) x &= 0xffff0000u;
+    if (hi) x &= 0x0000ffffu;
+    return lo || hi;
+}
+
+// HSP: head size rounded up to 64 or 128 (the rest reads as zeros). NT: tiles of 8 rows per warp.
+// KG: warps that share the keys; WARPS / KG groups of rows.
+template <int HSP, bool Q8, int NT, int KG>
+__global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) {
+    constexpr int KC = Q8 ? HSP / 64 : HSP / 32;  // 16-byte pieces of a K row per thread
+    constexpr int VC = Q8 ? 1 : HSP / 64;         // and of a V row (8-bit, HSP = 64: 8 bytes)
+    constexpr int MT = HSP / 16;                  // tiles of 16 dims
+    constexpr int ROWS = NT * 8 * (WARPS / KG);
+    __shared__ float s_o[ROWS][HSP + 4];
+    __shared__ float2 s_ml[KG][ROWS];
+    __shared__ int s_odd;
+    wait_for_earlier_kernels();
+
+    const int b = blockIdx.y, hk = blockIdx.x / a.splits, split = blockIdx.x - hk * a.splits;
+    const int s0 = a.q_start[b], s1 = a.q_start[b + 1], n = s1 - s0;
+    if (n <= 0) return;
+    if (n > a.max_q || s0 < 0 || s1 > a.rows) {
+        if (threadIdx.x == 0) report(a.err, GK_ERR_INDEX);
+        return;
+    }
+    const int kv_all = max(a.p.kv_len[b], 0), kv = min(kv_all, a.p.capacity);
+    if (kv_all > a.p.capacity && threadIdx.x == 0) report(a.err, GK_ERR_INDEX);
+    const int first = blockIdx.z * ROWS, R = n * a.G, hs = a.p.hs;  // rows first .. of R are this block's
+    if (first >= R) return;
+    const int piece = a.split_keys(kv), k_begin = split * piece, k_end = min(kv, k_begin + piece);
+    if (split > 0 && k_begin >= kv) return;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int kg = warp % KG, row0 = (warp / KG) * NT * 8;
+    if (threadIdx.x == 0) s_odd = 0;
+
+    // Q in the order of the K registers; rows past R are zeros
+    uint32_t q[NT][HSP / 8];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int i = first + row0 + nt * 8 + g;
+        const __nv_bfloat16* src = a.q + (int64_t)(s0 + i / a.G) * a.ldq + (hk * a.G + i % a.G) * hs;
+#pragma unroll
+        for (int c = 0; c < HSP / 32; ++c) {
+            const int d = Q8 ? ((c >> 1) * 4 + t) * 16 + (c & 1) * 8 : (c * 4 + t) * 8;
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (i < R && d < hs) u = *reinterpret_cast<const uint4*>(src + d);
+            if (Q8) {
+                q[nt][4 * c] = __byte_perm(u.x, u.y, 0x5410);
+                q[nt][4 * c + 1] = __byte_perm(u.x, u.y, 0x7632);
+                q[nt][4 * c + 2] = __byte_perm(u.z, u.w, 0x5410);
+                q[nt][4 * c + 3] = __byte_perm(u.z, u.w, 0x7632);
+            } else {
+                q[nt][4 * c] = u.x, q[nt][4 * c + 1] = u.y, q[nt][4 * c + 2] = u.z, q[nt][4 * c + 3] = u.w;
+            }
+        }
+    }
+    // the last position that each of this thread's score columns sees (kv_all - n + query)
+    int last[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = first + row0 + nt * 8 + 2 * t + e;
+            last[nt][e] = i < R ? min(kv - 1, kv_all - n + i / a.G) : -1;
+        }
+    const int clear = kv_all - n;  // keys up to this position are seen by every row
+
+    float o[NT][MT][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
+        m[nt][0] = m[nt][1] = -INFINITY;
+        l[nt][0] = l[nt][1] = 0.f;
+    }
+
+    uint4 kr[2][KC], vr[4][VC];
+    float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};
+    const int tiles = (k_end - k_begin + 15) >> 4;
+    const int mine = tiles > kg ? (tiles - kg + KG - 1) / KG : 0;
+    const int esz = Q8 ? 1 : 2;
+    int ids = -1;
+    bool bad_page = false;
+    // the first row (token of this key / value head) of the tile's page part, or -1
+    auto tile_row = [&](int j) -> int64_t {
+        if ((j & 31) == 0) {  // 32 tiles' page ids at once, one per lane
+            const int pos = k_begin + (kg + KG * (j + lane)) * 16;
+            ids = -1;
+            if (j + lane < mine) {
+                ids = __ldg(a.p.table + b * a.p.ld_table + (pos >> a.p.page_log2));
+                if (ids < 0 || ids >= a.p.n_pages) {
+                    ids = -1;
+                    bad_page = true;
+                }
+            }
+        }
+        const int id = __shfl_sync(0xffffffffu, ids, j & 31);
+        const int pos = k_begin + (kg + KG * j) * 16;
+        return id < 0 ? -1 : (((int64_t)id * a.p.Hkv + hk) << a.p.page_log2) + (pos & ((1 << a.p.page_log2) - 1));
+    };
+    auto load_k = [&](int64_t row) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const char* src = static_cast<const char*>(a.p.k) + (row + h * 8 + g) * hs * esz + t * 16;
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+                kr[h][c] = make_uint4(0, 0, 0, 0);
+                if (row >= 0 && (c * 4 + t) * 16 < hs * esz) kr[h][c] = __ldcs(reinterpret_cast<const uint4*>(src + c * 64));
+            }
+            if (Q8) ks[h] = row >= 0 ? __ldcs(a.p.k_scale + row + h * 8 + g) : 0.f;
+        }
+    };
+    auto load_v = [&](int64_t row) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const char* src = static_cast<const char*>(a.p.v) + (row + (x >> 1) * 8 + 2 * t + (x & 1)) * hs * esz;
+#pragma unroll
+            for (int c = 0; c < VC; ++c) {
+                vr[x][c] = make_uint4(0, 0, 0, 0);
+                if (Q8 && HSP == 64) {
+                    if (row >= 0 && g * 8 < hs) {
+                        const uint2 u = __ldcs(reinterpret_cast<const uint2*>(src + g * 8));
+                        vr[x][c].x = u.x, vr[x][c].y = u.y;
+                    }
+                } else if (row >= 0 && (c * 8 + g) * 16 < hs * esz) {
+                    vr[x][c] = __ldcs(reinterpret_cast<const uint4*>(src + (c * 8 + g) * 16));
+                }
+            }
+        }
+        if (Q8)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) vs[h] = row >= 0 ? __ldcs(a.p.v_scale + row + h * 8 + g) : 0.f;
+    };
+
+    int64_t row = -1;
+    if (mine > 0) {
+        row = tile_row(0);
+        load_k(row);
+        load_v(row);
+    }
+    bool odd = false;
+    for (int j = 0; j < mine; ++j) {
+        const int pos = k_begin + (kg + KG * j) * 16;
+        // S^T = K Q^T: keys g, g + 8 by rows 2t, 2t + 1
+        float s[NT][4] = {};
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+            const uint32_t x[2][4] = {{kr[0][c].x, kr[0][c].y, kr[0][c].z, kr[0][c].w}, {kr[1][c].x, kr[1][c].y, kr[1][c].z, kr[1][c].w}};
+            if (Q8) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const uint32_t a0 = codes02(x[0][w]), a1 = codes02(x[1][w]), a2 = codes02(x[0][w] >> 8), a3 = codes02(x[1][w] >> 8);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma(s[nt], a0, a1, a2, a3, q[nt][8 * c + 2 * w], q[nt][8 * c + 2 * w + 1]);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma(s[nt], x[0][2 * e], x[1][2 * e], x[0][2 * e + 1], x[1][2 * e + 1], q[nt][4 * c + 2 * e], q[nt][4 * c + 2 * e + 1]);
+            }
+        }
+        float f[2] = {a.scale_log2, a.scale_log2}, vsc[2] = {vs[0], vs[1]};
+        if (Q8) f[0] *= ks[0], f[1] *= ks[1];
+        const int64_t now = row;
+        if (j + 1 < mine) {  // the next keys are on their way while this tile is finished
+            row = tile_row(j + 1);
+            load_k(row);
+        }
+        const bool part = pos + 15 > clear || pos + 16 > kv || now < 0;  // some key some row does not see
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[nt][e] *= f[e >> 1];
+                if (part && (pos + g + (e >> 1) * 8 > last[nt][e & 1] || now < 0)) s[nt][e] = -INFINITY;
+            }
+        bool move = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) move |= fmaxf(s[nt][e], s[nt][e + 2]) > m[nt][e] + 8.f;
+        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x = fmaxf(s[nt][e], s[nt][e + 2]);
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                    if (x > m[nt][e]) {
+                        const float c = ex2(m[nt][e] - x);  // 0 while the row was empty
+                        m[nt][e] = x;
+                        l[nt][e] *= c;
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) o[nt][i][e] *= c, o[nt][i][e + 2] *= c;
+                    }
+                }
+        }
+        uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float ref = m[nt][e & 1];
+                p[e] = ex2(s[nt][e] - (ref == -INFINITY ? 0.f : ref));
+                l[nt][e & 1] += p[e];
+                if (Q8) p[e] = part && s[nt][e] == -INFINITY ? 0.f : p[e] * vsc[e >> 1];
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t hi = pack(p[2 * h], p[2 * h + 1]);
+                const uint32_t lo = pack(p[2 * h] - __uint_as_float(hi << 16), p[2 * h + 1] - __uint_as_float(hi & 0xffff0000u));
+                ph[nt][h] = transpose8(hi);
+                pl[nt][h] = transpose8(lo);
+            }
+        }
+        if (!Q8 && part) {
+            // values of keys past the end are not the cache's: zeros. An infinity or NaN that only
+            // later rows see must not meet the earlier rows' zero weights: taken out here, and put
+            // back at the end for the rows that see it.
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const bool off = pos + (x >> 1) * 8 + 2 * t + (x & 1) >= kv;
+#pragma unroll
+                for (int c = 0; c < VC; ++c) {
+                    if (off) vr[x][c] = make_uint4(0, 0, 0, 0);
+                    odd |= drop_odd(vr[x][c].x) | drop_odd(vr[x][c].y) | drop_odd(vr[x][c].z) | drop_odd(vr[x][c].w);
+                }
+            }
+        }
+        // O^T += V^T P^T: dims by rows
+#pragma unroll
+        for (int c = 0; c < VC; ++c)
+#pragma unroll
+            for (int w = 0; w < (Q8 && HSP == 64 ? 2 : 4); ++w) {
+                uint32_t x[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[k] = w == 0 ? vr[k][c].x : w == 1 ? vr[k][c].y : w == 2 ? vr[k][c].z : vr[k][c].w;
+                if (Q8) {
+                    const uint32_t y0 = __byte_perm(x[0], x[1], 0x5410), y1 = __byte_perm(x[0], x[1], 0x7632);
+                    const uint32_t z0 = __byte_perm(x[2], x[3], 0x5410), z1 = __byte_perm(x[2], x[3], 0x7632);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t y = half ? y1 : y0, z = half ? z1 : z0;
+                        const uint32_t a0 = codes02(y), a1 = codes02(y >> 8), a2 = codes02(z), a3 = codes02(z >> 8);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma(o[nt][2 * w + half], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
+                            mma(o[nt][2 * w + half], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+                        }
+                    }
+                } else {
+                    const uint32_t a0 = __byte_perm(x[0], x[1], 0x5410), a1 = __byte_perm(x[0], x[1], 0x7632);
+                    const uint32_t a2 = __byte_perm(x[2], x[3], 0x5410), a3 = __byte_perm(x[2], x[3], 0x7632);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma(o[nt][4 * c + w], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
+                        mma(o[nt][4 * c + w], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+                    }
+                }
+            }
+        if (j + 1 < mine) load_v(row);
+    }
+    if (bad_page) report(a.err, GK_ERR_INDEX);
+
+    // join the warps that shared the keys: the largest reference of each row, then the scaled sums
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], d);
+            if (g == 0) s_ml[kg][row0 + nt * 8 + 2 * t + e] = make_float2(m[nt][e], l[nt][e]);
+        }
+    __syncthreads();
+    if (odd) s_odd = 1;
+    for (int turn = 0; turn < KG; ++turn) {  // in a fixed order
+        if (kg == turn) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = row0 + nt * 8 + 2 * t + e;
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int w = 0; w < KG; ++w) top = fmaxf(top, s_ml[w][r].x);
+                    const float c = m[nt][e] == -INFINITY ? (l[nt][e] == 0.f ? 0.f : 1.f) : ex2(m[nt][e] - top);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            // the dim of tile i's row g + 8 h, as V was dealt out
+                            const int d = Q8 ? (HSP == 64 ? g * 8 : g * 16) + 2 * i + h : (i >> 2) * 64 + g * 8 + 2 * (i & 3) + h;
+                            const float x = c == 0.f ? 0.f : o[nt][i][e + 2 * h] * c;
+                            s_o[r][d] = turn ? s_o[r][d] + x : x;
+                        }
+                }
+        }
+        __syncthreads();
+    }
+    // write: a piece's sum for the join, or the result
+    const int per = hs >> 3, odd_from = s_odd ? max(k_begin, clear + 1) : 0x7fffffff;
+    for (int x = threadIdx.x; x < min(R - first, ROWS) * per; x += WARPS * 32) {
+        const int r = x / per, d = (x - r * per) * 8;
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < KG; ++w) top = fmaxf(top, s_ml[w][r].x);
+#pragma unroll
+        for (int w = 0; w < KG; ++w) {
+            const float2 ml = s_ml[w][r];
+            sum += ml.x == -INFINITY ? ml.y : ml.y * ex2(ml.x - top);  // (an empty part's sum is 0, or NaN)
+        }
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = s_o[r][d + e];
+        const int query = (first + r) / a.G, h = hk * a.G + (first + r) % a.G;
+        for (int j = odd_from; j < k_end && j <= kv_all - n + query; ++j) {  // rare: see above
+            const int id = a.p.table[b * a.p.ld_table + (j >> a.p.page_log2)];
+            if (id < 0 || id >= a.p.n_pages) continue;
+            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.p.v) +
+                                       ((((int64_t)id * a.p.Hkv + hk) << a.p.page_log2) + (j & ((1 << a.p.page_log2) - 1))) * hs + d;
+            for (int e = 0; e < 8; ++e) {
+                const float y = __bfloat162float(src[e]);
+                if (!isfinite(y)) v[e] += y;
+            }
+        }
+        const int64_t out = (int64_t)(s0 + query) * a.H + h;
+        if (a.splits > 1) {
+            float* dst = a.part_o + (out * a.splits + split) * hs + d;
+            *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(dst + 4) = make_float4(v[4], v[5], v[6], v[7]);
+            if (d == 0) a.part_ml[out * a.splits + split] = make_float2(top, sum);
+        } else {
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            *reinterpret_cast<uint4*>(a.y + (int64_t)(s0 + query) * a.ldy + h * hs + d) =
+                make_uint4(pack(v[0] * inv, v[1] * inv), pack(v[2] * inv, v[3] * inv), pack(v[4] * inv, v[5] * inv), pack(v[6] * inv, v[7] * inv));
+            if (a.lse && d == 0) a.lse[out] = sum == 0.f ? -INFINITY : ((top == -INFINITY ? 0.f : top) + log2f(sum)) * 0.6931471805599453f;
+        }
+    }
+}
+
+// One block per (row, head): warp w adds pieces w, w + 4, ... with four dims a lane.
+__global__ void __launch_bounds__(WARPS * 32) attn_join_kernel(const AttnArgs a) {
+    __shared__ float4 s_o[WARPS][32];
+    __shared__ float s_l[WARPS];
+    wait_for_earlier_kernels();
+    const int r = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = find_sequence(a.q_start, a.B, r);
     if (b < 0) return;
     const int s0 = a.q_start[b], s1 = a.q_start[b + 1];
-    if (r < s0 || r >= s1) return;
-    if (s1 - s0 > a.max_q) {
-        report(a.err, GK_ERR_INDEX);
-        return;
-    }
-    const int hs = a.p.hs, d = lane * 4;
-    const bool has = d < hs;
-    int64_t last = (int64_t)a.p.kv_len[b] - s1 + r;
-    if (last >= a.p.capacity) {
-        report(a.err, GK_ERR_INDEX);
-        last = a.p.capacity - 1;
-    }
-    const int hk = h / (a.H / a.p.Hkv);
-    float qv[4] = {}, o[4] = {}, m = -INFINITY, l = 0.f;
-    if (has)
-        for (int i = 0; i < 4; ++i) qv[i] = __bfloat162float(a.q[r * a.ldq + h * hs + d + i]) * a.scale;
-    const int mask = (1 << a.p.page_log2) - 1;
-    for (int j = 0; j <= last; ++j) {
-        const int id = a.p.table[b * a.p.ld_table + (j >> a.p.page_log2)];
-        if (id < 0 || id >= a.p.n_pages) {
-            report(a.err, GK_ERR_INDEX);
-            continue;
+    if (s0 < 0 || r < s0 || r >= s1 || s1 - s0 > a.max_q || s1 > a.rows) return;
+    const int kv = min(max(a.p.kv_len[b], 0), a.p.capacity);
+    const int pieces = kv <= 0 ? 1 : (kv + a.split_keys(kv) - 1) / a.split_keys(kv);
+    const int64_t out = (int64_t)r * a.H + h;
+    const float2* ml = a.part_ml + out * a.splits;
+    const float4* po = reinterpret_cast<const float4*>(a.part_o + out * a.splits * a.p.hs);
+    const int per = a.p.hs >> 2;
+    float top = -INFINITY;
+    for (int s = lane; s < pieces; s += 32) top = fmaxf(top, ml[s].x);
+    top = warp_max(top);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+#pragma unroll 4
+    for (int s = warp; s < pieces; s += WARPS) {
+        const float2 x = ml[s];
+        const float4 v = lane < per ? po[s * per + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+        // a piece in which the row sees nothing has sum 0 (or NaN, which stays) and no reference
+        const float c = x.x == -INFINITY ? (x.y == 0.f ? 0.f : 1.f) : ex2(x.x - top);
+        if (c != 0.f) {
+            l += x.y * c;
+            o.x += v.x * c, o.y += v.y * c, o.z += v.z * c, o.w += v.w * c;
         }
-        const int64_t vec = ((int64_t)id * a.p.Hkv + hk << a.p.page_log2) + (j & mask), at = vec * hs + d;
-        float s = 0.f, vv[4] = {};
-        for (int i = 0; i < 4; ++i)
-            if (has) {
-                if (Q8) {
-                    s = fmaf(qv[i], (float)static_cast<const int8_t*>(a.p.k)[at + i], s);
-                    vv[i] = (float)static_cast<const int8_t*>(a.p.v)[at + i] * a.p.v_scale[vec];
-                } else {
-                    s = fmaf(qv[i], __bfloat162float(static_cast<const __nv_bfloat16*>(a.p.k)[at + i]), s);
-                    vv[i] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.p.v)[at + i]);
-                }
-            }
-        s = warp_sum(s);
-        if (Q8) s *= a.p.k_scale[vec];
-        const float mn = fmaxf(m, s), c = m == mn ? 1.f : expf(m - mn), e = s == -INFINITY && mn == s ? 0.f : expf(s - mn);
-        m = mn;
-        l = l * c + e;
-        for (int i = 0; i < 4; ++i) o[i] = o[i] * c + e * vv[i];
+    }
+    s_o[warp][lane] = o;
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    if (warp) return;
+    l = 0.f;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        const float4 v = s_o[w][lane];
+        l += s_l[w];
+        o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    if (has)
-        for (int i = 0; i < 4; ++i) a.y[r * a.ldy + h * hs + d + i] = __float2bfloat16_rn(o[i] * inv);
-    if (a.lse && lane == 0) a.lse[(int64_t)r * a.H + h] = l == 0.f ? -INFINITY : m + logf(l);
+    if (lane < per)
+        *reinterpret_cast<uint2*>(a.y + (int64_t)r * a.ldy + h * a.p.hs + lane * 4) = make_uint2(pack(o.x * inv, o.y * inv), pack(o.z * inv, o.w * inv));
+    if (a.lse && lane == 0) a.lse[out] = l == 0.f ? -INFINITY : ((top == -INFINITY ? 0.f : top) + log2f(l)) * 0.6931471805599453f;
+}
+
+template <int HSP, bool Q8>
+gk_status few(gk_ctx* ctx, const AttnArgs& a) {
+    const int64_t R = (int64_t)a.max_q * a.G;
+    const dim3 grid((unsigned)(a.p.Hkv * a.splits), (unsigned)a.B, (unsigned)cdiv(R, 64)), block(WARPS * 32);
+#define FEW(NT, KG) return launch_dependent(ctx, "paged_attn", attn_few_kernel<HSP, Q8, NT, KG>, grid, block, 0, a)
+    if (R <= 8) FEW(1, 4);
+    if (R <= 16) FEW(2, 4);
+    if (R <= 32) FEW(2, 2);
+    FEW(2, 1);
+#undef FEW
 }
 
 }  // namespace
+
+gk_status launch_attn_join(gk_ctx* ctx, const AttnArgs& a) {
+    return launch_dependent(ctx, "paged_attn_join", attn_join_kernel, dim3((unsigned)a.rows, (unsigned)a.H), dim3(WARPS * 32), 0, a);
+}
+
+gk_status launch_attn_few(gk_ctx* ctx, const AttnArgs& a) {
+    if (a.p.hs <= 64) return a.p.k_scale ? few<64, true>(ctx, a) : few<64, false>(ctx, a);
+    return a.p.k_scale ? few<128, true>(ctx, a) : few<128, false>(ctx, a);
+}
+
 }  // namespace gk
 
 using namespace gk;
@@ -94,7 +498,8 @@ extern "C" gk_status gk_paged_attn(gk_ctx* ctx, const gk_paged_kv* cache, int dt
     GK_TRY(check_pages(ctx, "gk_paged_attn", cache, q_start, B, rows, &a.p));
     GK_REQUIRE(ctx, q && y, GK_ERR_ARG, "gk_paged_attn: null pointer");
     GK_REQUIRE(ctx, dtype == GK_BF16, GK_ERR_UNSUPPORTED, "gk_paged_attn: dtype %d (GK_BF16 only)", dtype);
-    GK_REQUIRE(ctx, H >= 1 && H % a.p.Hkv == 0 && max_q >= 1 && isfinite(scale), GK_ERR_ARG, "gk_paged_attn: bad argument");
+    GK_REQUIRE(ctx, H >= 1 && H <= 65535 && H % a.p.Hkv == 0 && max_q >= 1 && isfinite(scale), GK_ERR_ARG,
+               "gk_paged_attn: bad argument");
     GK_REQUIRE(ctx, ldq >= (int64_t)H * a.p.hs && ldy >= (int64_t)H * a.p.hs, GK_ERR_ARG, "gk_paged_attn: row stride");
     GK_REQUIRE(ctx, aligned16(q) && aligned16(y) && ldq % 8 == 0 && ldy % 8 == 0, GK_ERR_ALIGN,
                "gk_paged_attn: rows must be 16-byte aligned with strides a multiple of 8");
@@ -107,12 +512,20 @@ extern "C" gk_status gk_paged_attn(gk_ctx* ctx, const gk_paged_kv* cache, int dt
     a.ldy = ldy;
     a.B = B;
     a.H = H;
+    a.G = H / a.p.Hkv;
     a.rows = (int)rows;
-    a.max_q = max_q;
-    a.scale = scale;
+    a.max_q = (int)std::min<int64_t>(max_q, rows);
+    a.scale_log2 = scale * 1.4426950408889634f;
     a.err = ctx->d_err;
-    const unsigned grid = (unsigned)cdiv(rows * H, THREADS / 32);
-    if (a.p.k_scale) paged_attn_kernel<true><<<grid, THREADS, 0, ctx->stream>>>(a);
-    else paged_attn_kernel<false><<<grid, THREADS, 0, ctx->stream>>>(a);
-    return launched(ctx, "paged_attn");
+    // pieces per sequence: enough for 16 blocks an SM in all (four are resident; the rest evens out
+    // sequences of unequal lengths), of 128 keys at least, 256 where the batch alone fills the GPU
+    const int64_t units = (int64_t)B * a.p.Hkv, per = rows * H * (a.p.hs * 4 + 8);
+    a.min_split = units >= ctx->num_sms ? 256 : 128;
+    int64_t splits = std::min<int64_t>(cdiv(16 * (int64_t)ctx->num_sms, units), cdiv(a.p.capacity, a.min_split));
+    splits = std::min<int64_t>(splits, std::min<int64_t>(256, (int64_t)(ctx->ws_bytes / per)));
+    a.splits = (int)std::max<int64_t>(1, splits);
+    a.part_o = static_cast<float*>(ctx->ws);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + rows * H * a.splits * a.p.hs);
+    GK_TRY(launch_attn_few(ctx, a));
+    return a.splits > 1 ? launch_attn_join(ctx, a) : GK_OK;
 }

@@ -1,0 +1,36 @@
+// Internal interface of the attention over the paged cache: the arguments its kernels share, and
+// the partial results of sequences split over the GPU.
+#pragma once
+
+#include "paged.cuh"
+
+namespace gk {
+
+struct AttnArgs {
+    Pages p;
+    const __nv_bfloat16* q;
+    __nv_bfloat16* y;
+    float* lse;  // may be null
+    const int32_t* q_start;
+    int64_t ldq, ldy;
+    int B, H, G, rows, max_q;  // G = H / Hkv heads share a key / value head
+    float scale_log2;          // scale * log2(e): scores are kept in powers of two
+    // a sequence of kv keys is cut into pieces of split_keys(kv) keys, at most `splits` of them;
+    // with splits > 1 piece s of row r, head h leaves its weighted sum of values (not divided) in
+    // part_o[(r * H + h) * splits + s][hs] and its reference and sum of weights in part_ml
+    int splits, min_split;
+    float* part_o;
+    float2* part_ml;
+    int* err;
+    __host__ __device__ int split_keys(int kv) const {
+        const int even = (kv + splits - 1) / splits;
+        return max(min_split, (even + 127) & ~127);
+    }
+};
+
+// Join the pieces: one block per (row, head).
+gk_status launch_attn_join(gk_ctx* ctx, const AttnArgs& a);
+// Sequences with at most 64 query rows per key / value head.
+gk_status launch_attn_few(gk_ctx* ctx, const AttnArgs& a);
+
+}  // namespace gk
