@@ -1,0 +1,50 @@
+// Launches of the serving kernels: as programmatic dependents of the kernel before them on the
+// stream, alone or in clusters, and the cluster's barrier and shared-memory reads.
+#pragma once
+
+#include "common.cuh"
+
+namespace gk {
+
+// Every thread of `kernel` begins with wait_for_earlier_kernels, so only the launch overlaps the
+// earlier kernel's end. cluster: blocks along x that form one cluster (1: none).
+template <typename... KArgs, typename... Args>
+gk_status launch_dependent(gk_ctx* ctx, const char* what, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                           int cluster, Args... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = ctx->stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(ctx, GK_ERR_CUDA, "%s: launch failed: %s", what, cudaGetErrorString(e));
+    }
+    return launched(ctx, what);
+}
+__device__ __forceinline__ void wait_for_earlier_kernels() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Every thread of every block of the cluster arrives, then waits (release / acquire).
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The word at this block's shared-memory address p, read from block `rank` of the cluster.
+__device__ __forceinline__ uint32_t load_cluster_u32(const void* p, int rank) {
+    uint32_t at, v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ float load_cluster(const float* p, int rank) { return __uint_as_float(load_cluster_u32(p, rank)); }
+
+}  // namespace gk

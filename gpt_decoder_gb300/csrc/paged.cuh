@@ -3,7 +3,7 @@
 // a KV cache" (one key and value row per position).
 #pragma once
 
-#include "common.cuh"
+#include "launch.cuh"
 
 namespace gk {
 
@@ -57,30 +57,6 @@ inline gk_status check_pages(gk_ctx* ctx, const char* what, const gk_paged_kv* c
     p->capacity = c->max_pages * c->page_size;
     return GK_OK;
 }
-
-// Launch as a programmatic dependent of the kernel before it on the stream: every thread of `kernel`
-// begins with wait_for_earlier_kernels, so only its launch overlaps that kernel's end.
-template <typename... KArgs, typename... Args>
-gk_status launch_dependent(gk_ctx* ctx, const char* what, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                           Args... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = ctx->stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        return fail(ctx, GK_ERR_CUDA, "%s: launch failed: %s", what, cudaGetErrorString(e));
-    }
-    return launched(ctx, what);
-}
-__device__ __forceinline__ void wait_for_earlier_kernels() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // The sequence that token row r belongs to, or -1, by the whole warp: each round compares 32 of
 // q_start's entries at once, so a batch of up to 31 takes one round trip and one of 1023 two.

@@ -468,7 +468,7 @@ template <int HSP, bool Q8>
 gk_status few(gk_ctx* ctx, const AttnArgs& a) {
     const int64_t R = (int64_t)a.max_q * a.G;
     const dim3 grid((unsigned)(a.p.Hkv * a.splits), (unsigned)a.B, (unsigned)cdiv(R, 64)), block(WARPS * 32);
-#define FEW(NT, KG) return launch_dependent(ctx, "paged_attn", attn_few_kernel<HSP, Q8, NT, KG>, grid, block, 0, a)
+#define FEW(NT, KG) return launch_dependent(ctx, "paged_attn", attn_few_kernel<HSP, Q8, NT, KG>, grid, block, 0, 1, a)
     if (R <= 8) FEW(1, 4);
     if (R <= 16) FEW(2, 4);
     if (R <= 32) FEW(2, 2);
@@ -479,7 +479,7 @@ gk_status few(gk_ctx* ctx, const AttnArgs& a) {
 }  // namespace
 
 gk_status launch_attn_join(gk_ctx* ctx, const AttnArgs& a) {
-    return launch_dependent(ctx, "paged_attn_join", attn_join_kernel, dim3((unsigned)a.rows, (unsigned)a.H), dim3(WARPS * 32), 0, a);
+    return launch_dependent(ctx, "paged_attn_join", attn_join_kernel, dim3((unsigned)a.rows, (unsigned)a.H), dim3(WARPS * 32), 0, 1, a);
 }
 
 gk_status launch_attn_few(gk_ctx* ctx, const AttnArgs& a) {
