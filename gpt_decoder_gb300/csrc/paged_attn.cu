@@ -94,8 +94,7 @@ __global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) 
     }
     const int kv_all = max(a.p.kv_len[b], 0), kv = min(kv_all, a.p.capacity);
     if (kv_all > a.p.capacity && threadIdx.x == 0) report(a.err, GK_ERR_INDEX);
-    const int first = blockIdx.z * ROWS, R = n * a.G, hs = a.p.hs;  // rows first .. of R are this block's
-    if (first >= R) return;
+    const int R = n * a.G, hs = a.p.hs;
     const int piece = a.split_keys(kv), k_begin = split * piece, k_end = min(kv, k_begin + piece);
     if (split > 0 && k_begin >= kv) return;
 
@@ -107,7 +106,7 @@ __global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) 
     uint32_t q[NT][HSP / 8];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const int i = first + row0 + nt * 8 + g;
+        const int i = row0 + nt * 8 + g;
         const __nv_bfloat16* src = a.q + (int64_t)(s0 + i / a.G) * a.ldq + (hk * a.G + i % a.G) * hs;
 #pragma unroll
         for (int c = 0; c < HSP / 32; ++c) {
@@ -130,7 +129,7 @@ __global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) 
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int i = first + row0 + nt * 8 + 2 * t + e;
+            const int i = row0 + nt * 8 + 2 * t + e;
             last[nt][e] = i < R ? min(kv - 1, kv_all - n + i / a.G) : -1;
         }
     const int clear = kv_all - n;  // keys up to this position are seen by every row
@@ -375,7 +374,7 @@ __global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) 
     }
     // write: a piece's sum for the join, or the result
     const int per = hs >> 3, odd_from = s_odd ? max(k_begin, clear + 1) : 0x7fffffff;
-    for (int x = threadIdx.x; x < min(R - first, ROWS) * per; x += WARPS * 32) {
+    for (int x = threadIdx.x; x < R * per; x += WARPS * 32) {
         const int r = x / per, d = (x - r * per) * 8;
         float top = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -388,7 +387,7 @@ __global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) 
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = s_o[r][d + e];
-        const int query = (first + r) / a.G, h = hk * a.G + (first + r) % a.G;
+        const int query = r / a.G, h = hk * a.G + r % a.G;
         for (int j = odd_from; j < k_end && j <= kv_all - n + query; ++j) {  // rare: see above
             const int id = a.p.table[b * a.p.ld_table + (j >> a.p.page_log2)];
             if (id < 0 || id >= a.p.n_pages) continue;
@@ -467,7 +466,7 @@ __global__ void __launch_bounds__(WARPS * 32) attn_join_kernel(const AttnArgs a)
 template <int HSP, bool Q8>
 gk_status few(gk_ctx* ctx, const AttnArgs& a) {
     const int64_t R = (int64_t)a.max_q * a.G;
-    const dim3 grid((unsigned)(a.p.Hkv * a.splits), (unsigned)a.B, (unsigned)cdiv(R, 64)), block(WARPS * 32);
+    const dim3 grid((unsigned)(a.p.Hkv * a.splits), (unsigned)a.B), block(WARPS * 32);
 #define FEW(NT, KG) return launch_dependent(ctx, "paged_attn", attn_few_kernel<HSP, Q8, NT, KG>, grid, block, 0, 1, a)
     if (R <= 8) FEW(1, 4);
     if (R <= 16) FEW(2, 4);
@@ -498,7 +497,7 @@ extern "C" gk_status gk_paged_attn(gk_ctx* ctx, const gk_paged_kv* cache, int dt
     GK_TRY(check_pages(ctx, "gk_paged_attn", cache, q_start, B, rows, &a.p));
     GK_REQUIRE(ctx, q && y, GK_ERR_ARG, "gk_paged_attn: null pointer");
     GK_REQUIRE(ctx, dtype == GK_BF16, GK_ERR_UNSUPPORTED, "gk_paged_attn: dtype %d (GK_BF16 only)", dtype);
-    GK_REQUIRE(ctx, H >= 1 && H <= 65535 && H % a.p.Hkv == 0 && max_q >= 1 && isfinite(scale), GK_ERR_ARG,
+    GK_REQUIRE(ctx, H >= 1 && H <= 65535 && H % a.p.Hkv == 0 && max_q >= 1 && scale > 0.f && isfinite(scale), GK_ERR_ARG,
                "gk_paged_attn: bad argument");
     GK_REQUIRE(ctx, ldq >= (int64_t)H * a.p.hs && ldy >= (int64_t)H * a.p.hs, GK_ERR_ARG, "gk_paged_attn: row stride");
     GK_REQUIRE(ctx, aligned16(q) && aligned16(y) && ldq % 8 == 0 && ldy % 8 == 0, GK_ERR_ALIGN,
@@ -517,15 +516,24 @@ extern "C" gk_status gk_paged_attn(gk_ctx* ctx, const gk_paged_kv* cache, int dt
     a.max_q = (int)std::min<int64_t>(max_q, rows);
     a.scale_log2 = scale * 1.4426950408889634f;
     a.err = ctx->d_err;
-    // pieces per sequence: enough for 16 blocks an SM in all (four are resident; the rest evens out
-    // sequences of unequal lengths), of 128 keys at least, 256 where the batch alone fills the GPU
-    const int64_t units = (int64_t)B * a.p.Hkv, per = rows * H * (a.p.hs * 4 + 8);
-    a.min_split = units >= ctx->num_sms ? 256 : 128;
-    int64_t splits = std::min<int64_t>(cdiv(16 * (int64_t)ctx->num_sms, units), cdiv(a.p.capacity, a.min_split));
+    const int64_t R = (int64_t)a.max_q * a.G, per = rows * H * (a.p.hs * 4 + 8);
+    const bool few = R <= 64;
+    const int64_t units = (int64_t)B * a.p.Hkv * (few ? 1 : cdiv(R, 256));
+    int64_t splits;
+    if (few) {
+        // enough pieces for 16 blocks an SM in all (four are resident; the rest evens out sequences of
+        // unequal lengths), of 128 keys at least, 256 where the batch alone fills the GPU
+        a.min_split = units >= ctx->num_sms ? 256 : 128;
+        splits = cdiv(16 * (int64_t)ctx->num_sms, units);
+    } else {
+        a.min_split = 512;
+        splits = cdiv(3 * (int64_t)ctx->num_sms, units);
+    }
+    splits = std::min<int64_t>(splits, cdiv(a.p.capacity, a.min_split));
     splits = std::min<int64_t>(splits, std::min<int64_t>(256, (int64_t)(ctx->ws_bytes / per)));
     a.splits = (int)std::max<int64_t>(1, splits);
     a.part_o = static_cast<float*>(ctx->ws);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + rows * H * a.splits * a.p.hs);
-    GK_TRY(launch_attn_few(ctx, a));
+    GK_TRY(few ? launch_attn_few(ctx, a) : launch_attn_tiles(ctx, a));
     return a.splits > 1 ? launch_attn_join(ctx, a) : GK_OK;
 }

@@ -32,5 +32,7 @@ struct AttnArgs {
 gk_status launch_attn_join(gk_ctx* ctx, const AttnArgs& a);
 // Sequences with at most 64 query rows per key / value head.
 gk_status launch_attn_few(gk_ctx* ctx, const AttnArgs& a);
+// Any number of rows, in tiles of 128 on the tensor cores (tcgen05).
+gk_status launch_attn_tiles(gk_ctx* ctx, const AttnArgs& a);
 
 }  // namespace gk

@@ -456,8 +456,9 @@ gk_status gk_paged_read(gk_ctx* ctx, const gk_paged_kv* cache, int dtype, void* 
  *           ldy (multiples of 8, 16-byte aligned). Scores, softmax and sums are float32.
  *   lse     float32 [rows, H] or NULL: the natural log-sum-exp of the scaled scores.
  *   max_q   at least every sequence's number of rows (host; it sizes the launch). A sequence with
- *           more rows than max_q records GK_ERR_INDEX and its rows are left as they were.
- *   scale   finite.
+ *           more rows than max_q, or with rows past `rows`, records GK_ERR_INDEX and its rows
+ *           are left as they were.
+ *   scale   positive and finite.
  * A row that sees nothing (a negative position) gets y = 0 and lse = -inf. Keys and values that a
  * row does not see never reach it, whatever they hold (infinities and NaN among it). Long
  * sequences are split over the GPU and joined through the context's workspace: the more of it

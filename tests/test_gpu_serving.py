@@ -602,6 +602,8 @@ def test_paged_calls_refuse(gkctx):
     refused(A, gk.gk_paged_attn, *att(H=4))  # rows of 4 heads do not fit the stride
     refused(A, gk.gk_paged_attn, *att(mq=0))
     refused(A, gk.gk_paged_attn, *att(s=float("nan")))
+    refused(A, gk.gk_paged_attn, *att(s=0.0))
+    refused(A, gk.gk_paged_attn, *att(s=float("inf")))
     refused(L, gk.gk_paged_attn, *att(ldq=68))
     refused(L, gk.gk_paged_attn, *att(o=y.data_ptr() + 2))
     s = d.h.struct
