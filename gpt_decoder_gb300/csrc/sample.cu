@@ -5,9 +5,10 @@
 // A cluster of blocks takes a row: each block reads its slice of the logits once, into shared
 // memory, and the rest happens on chip. Every filter is a threshold on the logit, so a row is
 //   the largest logit (a maximum over the cluster),
-//   top-k's threshold, then top-p's: histograms of the kept logits, by count or by weight, first over 1024
-//     steps of 1/22 in log2 of the weight, then over the 32-bit keys that order floats inside the
-//     step where the count or share is reached, 1024 parts at a time, down to one key,
+//   top-k's threshold, then top-p's: a histogram of the kept logits, by count or by weight, over 1024 steps of
+//     1/22 in log2 of the weight; then the logits of the step where the count or share is reached
+//     are compared with each other, or, if over 512, cut by histograms of the 32-bit keys that
+//     order floats, 1024 parts at a time, down to one key,
 //   the kept weights' running sum in index order, and the pick by the thread in whose run it falls.
 // Weights are integers, round(2^45 exp((l - max) / T)): sums are exact, and no order of adding
 // matters to the result. (Float64 runs at 1/64 of the float32 rate here, and float32 sums over a
@@ -24,7 +25,7 @@
 namespace gk {
 namespace {
 
-constexpr int THREADS = 512, BINS = 1024;
+constexpr int THREADS = 512, BINS = 1024, LIST = THREADS;
 constexpr uint64_t ONE = 1ull << 45;  // the largest weight: up to 2^18 tokens sum below 2^63
 
 // round(2^63 * 2^(-i / 32)) and round(2^63 * 2^(-j / 1024))
@@ -54,6 +55,9 @@ __device__ __forceinline__ uint32_t key_of(float x) {
     const uint32_t u = __float_as_uint(x + 0.f);
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
+__device__ __forceinline__ float value_of(uint32_t key) {
+    return __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
+}
 constexpr uint32_t KEY_NINF = 0x007fffffu;  // key of -inf: candidates are above it
 
 struct SampleArgs {
@@ -80,6 +84,10 @@ struct Shared {
     uint32_t red_c[THREADS / 32];
     uint32_t range[2][2];   // exchange: the largest and smallest key (two sets in turn)
     uint64_t sum;           // exchange: this block's kept weight
+    uint32_t n_list;        // exchange: this block's candidates
+    uint32_t list[LIST], all_k[LIST];  // their keys; the cluster's keys and weights
+    uint64_t all_w[LIST];
+    uint32_t chosen;
     int bin;                // the step where the wanted count or weight is reached, or -1
     uint64_t above;         // and what lies in the steps before it
 };
@@ -106,14 +114,19 @@ __device__ __forceinline__ uint64_t weight(const Shared& sh, const Scale& s, uin
     float low;
     const float z = log2_distance(s, l, &low);
     if (!(z < 47.f)) return 0;
-    const int64_t f = max(0ll, __float2ll_rn(z * 0x1p52f) + __float2ll_rn(low * 0x1p52f));
+    // z in units of 2^-52 by its bits, and the low part by a 32-bit conversion (units of 2^-46: 64-bit
+    // conversions run on the float64 pipe)
+    const uint32_t bits = __float_as_uint(z);
+    const int up = (int)(bits >> 23) - 98;
+    const uint64_t whole = (bits & 0x7fffffu) | 0x800000u;
+    const int64_t f = max((int64_t)0, (int64_t)(up >= 0 ? whole << up : up > -24 ? whole >> -up : 0) + ((int64_t)__float2int_rn(low * 0x1p46f) << 6));
     const int n = (int)(f >> 52);
     if (n >= 47) return 0;
     const uint64_t t = __umul64hi(sh.pow32[(f >> 47) & 31], sh.pow1024[(f >> 42) & 31]);  // 2^62 and below
     const uint64_t g = __umul64hi((uint64_t)f << 22, LN2);                                // units of 2^-74
     const float gf = (float)(uint32_t)(g >> 32) * 0x1p-42f;
     const float q = gf * gf * 0.5f * fmaf(gf * (-1.f / 3.f), fmaf(gf, -0.25f, 1.f), 1.f);
-    const uint64_t less = (g >> 10) - __float2ull_rn(q * 0x1p64f);  // 1 - e^-g in units of 2^-64
+    const uint64_t less = (g >> 10) - ((uint64_t)__float2uint_rn(q * 0x1p53f) << 11);  // 1 - e^-g in units of 2^-64
     const uint64_t w = t - __umul64hi(t, less);
     const int shift = 17 + n;
     return (w + (1ull << (shift - 1))) >> shift;
@@ -221,7 +234,7 @@ __global__ void __launch_bounds__(THREADS) sample_rows_kernel(const SampleArgs a
         row_barrier(cl);  // no block leaves while another reads its shared memory
         return;
     }
-    const float largest = __uint_as_float((top & 0x80000000u) ? top & 0x7fffffffu : ~top);
+    const float largest = value_of(top);
     const bool greedy = !(t > 0.f);
     Scale sc;
     const double c = 2.0 * 1.4426950408889634074 / (double)t;
@@ -237,7 +250,7 @@ __global__ void __launch_bounds__(THREADS) sample_rows_kernel(const SampleArgs a
     int turn = 0;
     // raise `low` to the largest key that keeps `want` tokens, or the share p of the weight, of those kept now
     auto select = [&](bool weigh, uint64_t want, float p) {
-        uint32_t k_hi = 0, shift = 0;  // the range of keys under the bins, once below the steps of weight
+        uint32_t k_hi = 0, k_lo = 0, shift = 0;  // the range of keys under the bins, once below the steps of weight
         int step = -1;
         uint64_t have = 0;
         auto step_of = [&](uint32_t key, float l) {
@@ -258,7 +271,7 @@ __global__ void __launch_bounds__(THREADS) sample_rows_kernel(const SampleArgs a
                 if (level == 0) {
                     b = step_of(key, l);
                 } else {
-                    if (key > k_hi || step_of(key, l) != step) continue;
+                    if (key > k_hi || key < k_lo) continue;  // (steps are ranges of keys)
                     const uint32_t d = (k_hi - key) >> shift;
                     if (d >= BINS) continue;
                     b = (int)d;
@@ -293,29 +306,57 @@ __global__ void __launch_bounds__(THREADS) sample_rows_kernel(const SampleArgs a
             if (level == 0) {
                 if (bin == BINS - 1) return;  // reached among weights of zero: all others stay
                 step = bin;
-                // the keys of this step, over the cluster
+                // the logits of this step, over the cluster: usually few enough that each is compared with
+                // all the others
                 uint32_t kmax = 0, kmin = 0xffffffffu;
+                uint32_t* ex = sh.range[turn & 1];
+                if (tid == 0) ex[0] = 0, ex[1] = 0xffffffffu, sh.n_list = 0, sh.chosen = 0;
+                __syncthreads();
                 for (int i = 0; i < mine; ++i) {
                     const uint32_t key = key_of(xr[i]);
-                    if (key >= low && step_of(key, xr[i]) == step) kmax = max(kmax, key), kmin = min(kmin, key);
+                    if (key < low || step_of(key, xr[i]) != step) continue;
+                    kmax = max(kmax, key), kmin = min(kmin, key);
+                    const uint32_t at = atomicAdd(&sh.n_list, 1u);
+                    if (at < LIST) sh.list[at] = key;
                 }
-                uint32_t* ex = sh.range[turn & 1];
-                __syncthreads();
-                if (tid == 0) ex[0] = 0, ex[1] = 0xffffffffu;
-                __syncthreads();
                 kmax = __reduce_max_sync(0xffffffffu, kmax);
                 kmin = __reduce_min_sync(0xffffffffu, kmin);
-                if (lane == 0) atomicMax(&ex[0], kmax), atomicMin(&ex[1], kmin);
+                if (lane == 0 && kmax) atomicMax(&ex[0], kmax), atomicMin(&ex[1], kmin);
                 row_barrier(cl);
                 k_hi = 0;
-                uint32_t k_lo = 0xffffffffu;
-                for (int q = 0; q < cl; ++q) k_hi = max(k_hi, peer_u32(&ex[0], q, cl)), k_lo = min(k_lo, peer_u32(&ex[1], q, cl));
-                const int bits = 32 - __clz((int)(k_hi - k_lo));
-                shift = bits > 10 ? (uint32_t)(bits - 10) : 0;
+                k_lo = 0xffffffffu;
+                uint32_t many = 0, at = tid;
+                int from = -1;
+                for (int q = 0; q < cl; ++q) {
+                    k_hi = max(k_hi, peer_u32(&ex[0], q, cl)), k_lo = min(k_lo, peer_u32(&ex[1], q, cl));
+                    const uint32_t m = peer_u32(&sh.n_list, q, cl);
+                    if (from < 0 && tid < many + m) from = q, at = tid - many;
+                    many += m;
+                }
                 if (k_hi == k_lo) {
                     low = k_hi;
                     return;
                 }
+                if (many <= LIST) {
+                    if (from >= 0) {
+                        const uint32_t key = peer_u32(&sh.list[at], from, cl);
+                        sh.all_k[tid] = key;
+                        sh.all_w[tid] = weigh ? weight(sh, sc, key, top, value_of(key)) : 1;
+                    }
+                    __syncthreads();
+                    if (from >= 0) {
+                        const uint32_t key = sh.all_k[tid];
+                        uint64_t sum = have;
+                        for (uint32_t i = 0; i < many; ++i)
+                            if (sh.all_k[i] >= key) sum += sh.all_w[i];
+                        if (sum >= want) atomicMax(&sh.chosen, key);
+                    }
+                    __syncthreads();
+                    low = sh.chosen;
+                    return;
+                }
+                const int bits = 32 - __clz((int)(k_hi - k_lo));
+                shift = bits > 10 ? (uint32_t)(bits - 10) : 0;
             } else {
                 k_hi -= (uint32_t)bin << shift;
                 if (shift == 0) {
@@ -403,9 +444,9 @@ extern "C" gk_status gk_sample_rows(gk_ctx* ctx, int dtype, const void* logits, 
                "gk_sample_rows: misaligned logits");
     if (rows == 0) return GK_OK;
     SampleArgs a{logits, ld, V, 1, 0, u, temperature, top_k, top_p, min_p, next, prob};
-    // blocks per row: as many as fill the GPU with three an SM, while each still has 8 elements a
-    // thread; and enough that a thread has at most 64 (133 KB of shared memory)
-    while (a.cluster < 8 && (V > a.cluster * (THREADS * 64) ||
+    // blocks per row: as many as fill the GPU, while each still has 8 elements a thread; and enough that a
+    // thread has at most 32 (98 KB of shared memory, two blocks an SM), or 64 for the largest rows
+    while (a.cluster < 8 && (V > a.cluster * (THREADS * 32) ||
                              (rows * a.cluster * 2 <= 4 * ctx->num_sms && V >= a.cluster * 2 * THREADS * 8)))
         a.cluster *= 2;
     while (((int64_t)a.cluster * THREADS << a.run_log2) < V) ++a.run_log2;
