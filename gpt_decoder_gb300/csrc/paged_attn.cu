@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) 
     constexpr int VC = Q8 ? 1 : HSP / 64;         // and of a V row (8-bit, HSP = 64: 8 bytes)
     constexpr int MT = HSP / 16;                  // tiles of 16 dims
     constexpr int ROWS = NT * 8 * (WARPS / KG);
-    __shared__ float s_o[ROWS][HSP + 4];
+    __shared__ float s_o[KG][ROWS][HSP + 4];
     __shared__ float2 s_ml[KG][ROWS];
     __shared__ int s_odd;
     wait_for_earlier_kernels();
@@ -145,65 +145,72 @@ __global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) 
         l[nt][0] = l[nt][1] = 0.f;
     }
 
+    // Every load is of a row that exists: a refused page's keys are read from page 0 and masked, and
+    // dims past hs from the row's last 16 bytes (Q is zero there, and such dims of the result are not
+    // stored). The offsets from a tile's first row are the thread's own, once.
+    const int esz = Q8 ? 1 : 2, row_bytes = hs * esz;
     uint4 kr[2][KC], vr[4][VC];
     float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};
+    int k_at[KC], v_at[VC];
+#pragma unroll
+    for (int c = 0; c < KC; ++c) k_at[c] = g * row_bytes + min((c * 4 + t) * 16, row_bytes - 16);
+#pragma unroll
+    for (int c = 0; c < VC; ++c)
+        v_at[c] = 2 * t * row_bytes + (Q8 && HSP == 64 ? min(g * 8, row_bytes - 8) : min((c * 8 + g) * 16, row_bytes - 16));
     const int tiles = (k_end - k_begin + 15) >> 4;
     const int mine = tiles > kg ? (tiles - kg + KG - 1) / KG : 0;
-    const int esz = Q8 ? 1 : 2;
-    int ids = -1;
+    int ids = 0;
     bool bad_page = false;
-    // the first row (token of this key / value head) of the tile's page part, or -1
+    unsigned refused = 0;  // of the 32 tiles looked up last
+    // the first row (token of this key / value head) of the tile's part of its page
     auto tile_row = [&](int j) -> int64_t {
         if ((j & 31) == 0) {  // 32 tiles' page ids at once, one per lane
             const int pos = k_begin + (kg + KG * (j + lane)) * 16;
-            ids = -1;
+            ids = 0;
+            bool bad = false;
             if (j + lane < mine) {
                 ids = __ldg(a.p.table + b * a.p.ld_table + (pos >> a.p.page_log2));
                 if (ids < 0 || ids >= a.p.n_pages) {
-                    ids = -1;
-                    bad_page = true;
+                    ids = 0;
+                    bad = true;
                 }
             }
+            bad_page |= bad;
+            refused = __ballot_sync(0xffffffffu, bad);
         }
         const int id = __shfl_sync(0xffffffffu, ids, j & 31);
         const int pos = k_begin + (kg + KG * j) * 16;
-        return id < 0 ? -1 : (((int64_t)id * a.p.Hkv + hk) << a.p.page_log2) + (pos & ((1 << a.p.page_log2) - 1));
+        return (((int64_t)id * a.p.Hkv + hk) << a.p.page_log2) + (pos & ((1 << a.p.page_log2) - 1));
     };
     auto load_k = [&](int64_t row) {
+        const char* base = static_cast<const char*>(a.p.k) + row * row_bytes;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const char* src = static_cast<const char*>(a.p.k) + (row + h * 8 + g) * hs * esz + t * 16;
 #pragma unroll
-            for (int c = 0; c < KC; ++c) {
-                kr[h][c] = make_uint4(0, 0, 0, 0);
-                if (row >= 0 && (c * 4 + t) * 16 < hs * esz) kr[h][c] = __ldcs(reinterpret_cast<const uint4*>(src + c * 64));
-            }
-            if (Q8) ks[h] = row >= 0 ? __ldcs(a.p.k_scale + row + h * 8 + g) : 0.f;
+            for (int c = 0; c < KC; ++c) kr[h][c] = __ldg(reinterpret_cast<const uint4*>(base + (k_at[c] + h * 8 * row_bytes)));
+            if (Q8) ks[h] = __ldg(a.p.k_scale + row + h * 8 + g);
         }
     };
     auto load_v = [&](int64_t row) {
+        const char* base = static_cast<const char*>(a.p.v) + row * row_bytes;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const char* src = static_cast<const char*>(a.p.v) + (row + (x >> 1) * 8 + 2 * t + (x & 1)) * hs * esz;
+        for (int x = 0; x < 4; ++x)
 #pragma unroll
             for (int c = 0; c < VC; ++c) {
-                vr[x][c] = make_uint4(0, 0, 0, 0);
+                const char* src = base + (v_at[c] + ((x >> 1) * 8 + (x & 1)) * row_bytes);
                 if (Q8 && HSP == 64) {
-                    if (row >= 0 && g * 8 < hs) {
-                        const uint2 u = __ldcs(reinterpret_cast<const uint2*>(src + g * 8));
-                        vr[x][c].x = u.x, vr[x][c].y = u.y;
-                    }
-                } else if (row >= 0 && (c * 8 + g) * 16 < hs * esz) {
-                    vr[x][c] = __ldcs(reinterpret_cast<const uint4*>(src + (c * 8 + g) * 16));
+                    const uint2 u = __ldg(reinterpret_cast<const uint2*>(src));
+                    vr[x][c] = make_uint4(u.x, u.y, 0, 0);
+                } else {
+                    vr[x][c] = __ldg(reinterpret_cast<const uint4*>(src));
                 }
             }
-        }
         if (Q8)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) vs[h] = row >= 0 ? __ldcs(a.p.v_scale + row + h * 8 + g) : 0.f;
+            for (int h = 0; h < 2; ++h) vs[h] = __ldg(a.p.v_scale + row + h * 8 + g);
     };
 
-    int64_t row = -1;
+    int64_t row = 0;
     if (mine > 0) {
         row = tile_row(0);
         load_k(row);
@@ -234,19 +241,23 @@ __global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) 
         }
         float f[2] = {a.scale_log2, a.scale_log2}, vsc[2] = {vs[0], vs[1]};
         if (Q8) f[0] *= ks[0], f[1] *= ks[1];
-        const int64_t now = row;
+        const bool off = refused >> (j & 31) & 1;  // on a refused page: not visible
         if (j + 1 < mine) {  // the next keys are on their way while this tile is finished
             row = tile_row(j + 1);
             load_k(row);
         }
-        const bool part = pos + 15 > clear || pos + 16 > kv || now < 0;  // some key some row does not see
+        const bool part = pos + 15 > clear || pos + 16 > kv || off;  // some key some row does not see
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s[nt][e] *= f[e >> 1];
-                if (part && (pos + g + (e >> 1) * 8 > last[nt][e & 1] || now < 0)) s[nt][e] = -INFINITY;
-            }
+            for (int e = 0; e < 4; ++e) s[nt][e] *= f[e >> 1];
+        if (part) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (off || pos + g + (e >> 1) * 8 > last[nt][e & 1]) s[nt][e] = -INFINITY;
+        }
         bool move = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -278,7 +289,12 @@ __global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) 
                 const float ref = m[nt][e & 1];
                 p[e] = ex2(s[nt][e] - (ref == -INFINITY ? 0.f : ref));
                 l[nt][e & 1] += p[e];
-                if (Q8) p[e] = part && s[nt][e] == -INFINITY ? 0.f : p[e] * vsc[e >> 1];
+                if (Q8) p[e] *= vsc[e >> 1];
+            }
+            if (Q8 && part) {  // an unseen key's scale may be anything
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (s[nt][e] == -INFINITY) p[e] = 0.f;
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -294,10 +310,10 @@ __global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) 
             // back at the end for the rows that see it.
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                const bool off = pos + (x >> 1) * 8 + 2 * t + (x & 1) >= kv;
+                const bool none = off || pos + (x >> 1) * 8 + 2 * t + (x & 1) >= kv;
 #pragma unroll
                 for (int c = 0; c < VC; ++c) {
-                    if (off) vr[x][c] = make_uint4(0, 0, 0, 0);
+                    if (none) vr[x][c] = make_uint4(0, 0, 0, 0);
                     odd |= drop_odd(vr[x][c].x) | drop_odd(vr[x][c].y) | drop_odd(vr[x][c].z) | drop_odd(vr[x][c].w);
                 }
             }
@@ -348,30 +364,25 @@ __global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) 
         }
     __syncthreads();
     if (odd) s_odd = 1;
-    for (int turn = 0; turn < KG; ++turn) {  // in a fixed order
-        if (kg == turn) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = row0 + nt * 8 + 2 * t + e;
-                    float top = -INFINITY;
+        for (int e = 0; e < 2; ++e) {
+            const int r = row0 + nt * 8 + 2 * t + e;
+            float top = -INFINITY;
 #pragma unroll
-                    for (int w = 0; w < KG; ++w) top = fmaxf(top, s_ml[w][r].x);
-                    const float c = m[nt][e] == -INFINITY ? (l[nt][e] == 0.f ? 0.f : 1.f) : ex2(m[nt][e] - top);
+            for (int w = 0; w < KG; ++w) top = fmaxf(top, s_ml[w][r].x);
+            const float c = m[nt][e] == -INFINITY ? (l[nt][e] == 0.f ? 0.f : 1.f) : ex2(m[nt][e] - top);
 #pragma unroll
-                    for (int i = 0; i < MT; ++i)
+            for (int i = 0; i < MT; ++i)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            // the dim of tile i's row g + 8 h, as V was dealt out
-                            const int d = Q8 ? (HSP == 64 ? g * 8 : g * 16) + 2 * i + h : (i >> 2) * 64 + g * 8 + 2 * (i & 3) + h;
-                            const float x = c == 0.f ? 0.f : o[nt][i][e + 2 * h] * c;
-                            s_o[r][d] = turn ? s_o[r][d] + x : x;
-                        }
+                for (int h = 0; h < 2; ++h) {
+                    // the dim of tile i's row g + 8 h, as V was dealt out
+                    const int d = Q8 ? (HSP == 64 ? g * 8 : g * 16) + 2 * i + h : (i >> 2) * 64 + g * 8 + 2 * (i & 3) + h;
+                    s_o[kg][r][d] = c == 0.f ? 0.f : o[nt][i][e + 2 * h] * c;
                 }
         }
-        __syncthreads();
-    }
+    __syncthreads();
     // write: a piece's sum for the join, or the result
     const int per = hs >> 3, odd_from = s_odd ? max(k_begin, clear + 1) : 0x7fffffff;
     for (int x = threadIdx.x; x < R * per; x += WARPS * 32) {
@@ -386,7 +397,11 @@ __global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) 
         }
         float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = s_o[r][d + e];
+        for (int e = 0; e < 8; ++e) {
+            v[e] = s_o[0][r][d + e];
+#pragma unroll
+            for (int w = 1; w < KG; ++w) v[e] += s_o[w][r][d + e];
+        }
         const int query = r / a.G, h = hk * a.G + r % a.G;
         for (int j = odd_from; j < k_end && j <= kv_all - n + query; ++j) {  // rare: see above
             const int id = a.p.table[b * a.p.ld_table + (j >> a.p.page_log2)];

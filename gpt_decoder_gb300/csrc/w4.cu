@@ -43,7 +43,7 @@ __global__ void quant_w4_kernel(const float* __restrict__ W, int64_t ldw, int tr
 // to be unpacked into shared memory first).
 //   A warp takes MT tiles of 16 outputs and, of each, U groups of K at a time: a lane loads
 // group / 32 words (8 codes each) of outputs g and g + 8 at once, so four lanes cover a group's
-// codes of a row and U of them are in flight. A word's codes become bf16 pairs by masks:
+// codes of a row; the next U groups are in flight while U are multiplied. A word's codes become bf16 pairs by masks:
 // (w >> 4 i) & 0x000f000f | 0x43004300 is 128 + code, exactly, and 136 taken off leaves code - 8. The pairs
 // are codes (i, i + 4); X's elements are paired the same way by byte permutes, once for all MT tiles.
 //   The products of a group are summed by the matrix instruction and then scaled in float32. The 8
@@ -96,8 +96,8 @@ __device__ __forceinline__ Words<LW> load_words(const uint8_t* p) {
 
 // LW: words of a group per lane (group / 32). NT: tiles of 8 rows. MT: tiles of 16 outputs per warp.
 template <int LW, int NT, int MT>
-__global__ void __launch_bounds__(W4_WARPS * 32) matvec_w4_kernel(const W4Args a) {
-    constexpr int G = 32 * LW, U = 8 / LW < 4 ? 4 : 8 / LW;
+__global__ void __launch_bounds__(W4_WARPS * 32, NT * MT == 8 ? 1 : 2) matvec_w4_kernel(const W4Args a) {
+    constexpr int G = 32 * LW, U = LW == 4 ? 2 : LW == 2 ? 4 : 8;
     __shared__ float part[W4_WARPS][NT * 8][MT * 16 + 1];
     wait_for_earlier_kernels();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -117,16 +117,18 @@ __global__ void __launch_bounds__(W4_WARPS * 32) matvec_w4_kernel(const W4Args a
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) xp[nt] = a.x + (int64_t)min(nt * 8 + g, a.N - 1) * a.ldx + t * 8 * LW;
     float sum[MT][NT][4] = {};
-    for (int g0 = (slice * W4_WARPS + warp) * U; g0 < groups; g0 += a.slices * W4_WARPS * U) {
+    struct Step {
         Words<LW> w[U][MT][2];
         float s[U][MT][2];
+    };
+    auto load = [&](Step& to, int g0) {  // groups past the last read the last one's, and are not used
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int gi = min(g0 + u, groups - 1);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) w[u][mt][h] = load_words<LW>(wp[mt][h] + (int64_t)gi * (G / 2));
+                for (int h = 0; h < 2; ++h) to.w[u][mt][h] = load_words<LW>(wp[mt][h] + (int64_t)gi * (G / 2));
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -134,39 +136,58 @@ __global__ void __launch_bounds__(W4_WARPS * 32) matvec_w4_kernel(const W4Args a
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) s[u][mt][h] = __bfloat162float(sp[mt][h][gi]);
+                for (int h = 0; h < 2; ++h) to.s[u][mt][h] = __bfloat162float(sp[mt][h][gi]);
         }
+    };
+    auto multiply = [&](const Step& now, int g0, int u) {
+        float acc[MT][NT][4] = {};
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (g0 + u >= groups) break;
-            float acc[MT][NT][4] = {};
+        for (int j = 0; j < LW; ++j) {
+            uint32_t b[NT][4];
 #pragma unroll
-            for (int j = 0; j < LW; ++j) {
-                uint32_t b[NT][4];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(xp[nt] + (g0 + u) * G + j * 8));
-                    b[nt][0] = __byte_perm(v.x, v.z, 0x5410), b[nt][1] = __byte_perm(v.x, v.z, 0x7632);
-                    b[nt][2] = __byte_perm(v.y, v.w, 0x5410), b[nt][3] = __byte_perm(v.y, v.w, 0x7632);
-                }
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    const uint32_t w0 = w[u][mt][0].w[j], w1 = w[u][mt][1].w[j];
-#pragma unroll
-                    for (int i = 0; i < 4; i += 2) {
-                        const uint32_t a0 = w4_pair(w0, i), a1 = w4_pair(w1, i), a2 = w4_pair(w0, i + 1), a3 = w4_pair(w1, i + 1);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) w4_mma(acc[mt][nt], a0, a1, a2, a3, b[nt][i], b[nt][i + 1]);
-                    }
-                }
+            for (int nt = 0; nt < NT; ++nt) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(xp[nt] + (g0 + u) * G + j * 8));
+                b[nt][0] = __byte_perm(v.x, v.z, 0x5410), b[nt][1] = __byte_perm(v.x, v.z, 0x7632);
+                b[nt][2] = __byte_perm(v.y, v.w, 0x5410), b[nt][3] = __byte_perm(v.y, v.w, 0x7632);
             }
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int mt = 0; mt < MT; ++mt) {
+                const uint32_t w0 = now.w[u][mt][0].w[j], w1 = now.w[u][mt][1].w[j];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int i = 0; i < 4; i += 2) {
+                    const uint32_t a0 = w4_pair(w0, i), a1 = w4_pair(w1, i), a2 = w4_pair(w0, i + 1), a3 = w4_pair(w1, i + 1);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) sum[mt][nt][e] = fmaf(acc[mt][nt][e], s[u][mt][e >> 1], sum[mt][nt][e]);
+                    for (int nt = 0; nt < NT; ++nt) w4_mma(acc[mt][nt], a0, a1, a2, a3, b[nt][i], b[nt][i + 1]);
+                }
+            }
         }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[mt][nt][e] = fmaf(acc[mt][nt][e], now.s[u][mt][e >> 1], sum[mt][nt][e]);
+    };
+    // the next step's codes are on their way while this step is multiplied
+    const int stride = a.slices * W4_WARPS * U;
+    int g0 = (slice * W4_WARPS + warp) * U;
+    Step step[2];
+    auto turn = [&](const Step& now, Step& next) {
+        if (g0 + stride < groups) load(next, g0 + stride);
+        if (g0 + U <= groups) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) multiply(now, g0, u);
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (g0 + u < groups) multiply(now, g0, u);
+        }
+        g0 += stride;
+    };
+    if (g0 < groups) load(step[0], g0);
+    while (g0 < groups) {
+        turn(step[0], step[1]);
+        if (g0 < groups) turn(step[1], step[0]);
     }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -207,7 +228,7 @@ __global__ void __launch_bounds__(W4_WARPS * 32) matvec_w4_kernel(const W4Args a
 template <int LW, int NT, int MT>
 gk_status run_w4(gk_ctx* ctx, W4Args& a) {
     const int64_t tiles = cdiv(a.M, MT * 16);
-    const int groups = a.K / (32 * LW), turns = (int)cdiv(groups, W4_WARPS * 4);
+    const int groups = a.K / (32 * LW), turns = (int)cdiv(groups, W4_WARPS * (LW == 4 ? 2 : LW == 2 ? 4 : 8));
     a.slices = 1;  // a cluster shares K while that adds blocks that have work and fit the GPU once
     while (a.slices < 8 && tiles * a.slices * 2 <= 2 * ctx->num_sms && a.slices * 2 <= turns) a.slices *= 2;
     return launch_dependent(ctx, "matvec_w4", matvec_w4_kernel<LW, NT, MT>, dim3((unsigned)(tiles * a.slices)),
