@@ -428,49 +428,38 @@ __global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) 
     }
 }
 
-// One block per (row, head): warp w adds pieces w, w + 4, ... with four dims a lane.
-__global__ void __launch_bounds__(WARPS * 32) attn_join_kernel(const AttnArgs a) {
-    __shared__ float4 s_o[WARPS][32];
-    __shared__ float s_l[WARPS];
+// A warp per (row, head), four dims a lane, eight pieces' loads in flight.
+constexpr int JOIN_WARPS = 8;
+__global__ void __launch_bounds__(JOIN_WARPS * 32) attn_join_kernel(const AttnArgs a) {
     wait_for_earlier_kernels();
-    const int r = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31;
+    const int64_t out = (int64_t)blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5);
+    const int r = (int)(out / a.H), h = (int)(out - (int64_t)r * a.H);
+    if (r >= a.rows) return;
     const int b = find_sequence(a.q_start, a.B, r);
     if (b < 0) return;
     const int s0 = a.q_start[b], s1 = a.q_start[b + 1];
     if (s0 < 0 || r < s0 || r >= s1 || s1 - s0 > a.max_q || s1 > a.rows) return;
     const int kv = min(max(a.p.kv_len[b], 0), a.p.capacity);
     const int pieces = kv <= 0 ? 1 : (kv + a.split_keys(kv) - 1) / a.split_keys(kv);
-    const int64_t out = (int64_t)r * a.H + h;
     const float2* ml = a.part_ml + out * a.splits;
-    const float4* po = reinterpret_cast<const float4*>(a.part_o + out * a.splits * a.p.hs);
     const int per = a.p.hs >> 2;
+    const float4* po = reinterpret_cast<const float4*>(a.part_o + out * a.splits * a.p.hs) + min(lane, per - 1);
     float top = -INFINITY;
     for (int s = lane; s < pieces; s += 32) top = fmaxf(top, ml[s].x);
     top = warp_max(top);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
-#pragma unroll 4
-    for (int s = warp; s < pieces; s += WARPS) {
+#pragma unroll 8
+    for (int s = 0; s < pieces; ++s) {
         const float2 x = ml[s];
-        const float4 v = lane < per ? po[s * per + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 v = po[s * per];
         // a piece in which the row sees nothing has sum 0 (or NaN, which stays) and no reference
         const float c = x.x == -INFINITY ? (x.y == 0.f ? 0.f : 1.f) : ex2(x.x - top);
         if (c != 0.f) {
             l += x.y * c;
             o.x += v.x * c, o.y += v.y * c, o.z += v.z * c, o.w += v.w * c;
         }
-    }
-    s_o[warp][lane] = o;
-    if (lane == 0) s_l[warp] = l;
-    __syncthreads();
-    if (warp) return;
-    l = 0.f;
-    o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-        const float4 v = s_o[w][lane];
-        l += s_l[w];
-        o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     if (lane < per)
@@ -493,7 +482,8 @@ gk_status few(gk_ctx* ctx, const AttnArgs& a) {
 }  // namespace
 
 gk_status launch_attn_join(gk_ctx* ctx, const AttnArgs& a) {
-    return launch_dependent(ctx, "paged_attn_join", attn_join_kernel, dim3((unsigned)a.rows, (unsigned)a.H), dim3(WARPS * 32), 0, 1, a);
+    return launch_dependent(ctx, "paged_attn_join", attn_join_kernel, dim3((unsigned)cdiv((int64_t)a.rows * a.H, JOIN_WARPS)),
+                            dim3(JOIN_WARPS * 32), 0, 1, a);
 }
 
 gk_status launch_attn_few(gk_ctx* ctx, const AttnArgs& a) {
@@ -534,6 +524,19 @@ extern "C" gk_status gk_paged_attn(gk_ctx* ctx, const gk_paged_kv* cache, int dt
     const int64_t R = (int64_t)a.max_q * a.G, per = rows * H * (a.p.hs * 4 + 8);
     const bool few = R <= 64;
     const int64_t units = (int64_t)B * a.p.Hkv * (few ? 1 : cdiv(R, 256));
+    char* ws = static_cast<char*>(ctx->ws);
+    size_t room = ctx->ws_bytes;
+    if (!few && a.p.k_scale && R >= 512) {
+        // codes to bf16 once, in the workspace, when at least two pairs of row tiles read them
+        const int64_t er = (int64_t)B * a.p.Hkv * cdiv(a.p.capacity, 128) * 128, bytes = er * a.p.hs * 2;
+        if (er < (1ll << 31) && (size_t)bytes <= room / 2) {
+            a.expanded_k = reinterpret_cast<__nv_bfloat16*>(ws);
+            a.expanded_v = reinterpret_cast<__nv_bfloat16*>(ws + bytes);
+            a.expanded_rows = er;
+            ws += 2 * bytes;
+            room -= 2 * (size_t)bytes;
+        }
+    }
     int64_t splits;
     if (few) {
         // enough pieces for 16 blocks an SM in all (four are resident; the rest evens out sequences of
@@ -545,9 +548,9 @@ extern "C" gk_status gk_paged_attn(gk_ctx* ctx, const gk_paged_kv* cache, int dt
         splits = cdiv(3 * (int64_t)ctx->num_sms, units);
     }
     splits = std::min<int64_t>(splits, cdiv(a.p.capacity, a.min_split));
-    splits = std::min<int64_t>(splits, std::min<int64_t>(256, (int64_t)(ctx->ws_bytes / per)));
+    splits = std::min<int64_t>(splits, std::min<int64_t>(256, (int64_t)(room / per)));
     a.splits = (int)std::max<int64_t>(1, splits);
-    a.part_o = static_cast<float*>(ctx->ws);
+    a.part_o = reinterpret_cast<float*>(ws);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + rows * H * a.splits * a.p.hs);
     GK_TRY(few ? launch_attn_few(ctx, a) : launch_attn_tiles(ctx, a));
     return a.splits > 1 ? launch_attn_join(ctx, a) : GK_OK;

@@ -21,6 +21,10 @@ struct AttnArgs {
     int splits, min_split;
     float* part_o;
     float2* part_ml;
+    // 8-bit codes laid out as bf16 for the tile kernel, or null
+    __nv_bfloat16* expanded_k;
+    __nv_bfloat16* expanded_v;
+    int64_t expanded_rows;
     int* err;
     __host__ __device__ int split_keys(int kv) const {
         const int even = (kv + splits - 1) / splits;

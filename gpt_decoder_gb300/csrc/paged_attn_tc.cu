@@ -11,10 +11,9 @@
 //               passes it by more than 8;
 //   O += P V    (N = head size, K = 128 keys), accumulated in tensor memory.
 // The two tiles take turns: while one group of four warps turns its S into P, the tensor core
-// computes the other's products. Warps 8-11 bring the keys: pages lie anywhere, so rows are
-// gathered, 16 bytes a thread, into the 128-byte-swizzled layouts that the MMAs read; bf16 pages
-// by cp.async (zero-filled past the end), 8-bit pages through registers, where the codes become bf16
-// (exactly). Codes carry no scale into the products: the key's scale multiplies the score and
+// computes the other's products. Warp 8 sends for the keys by TMA, a box per page (pages lie anywhere).
+// 8-bit codes become bf16 (exactly) first: in one pass into the workspace, if it has room and enough
+// tiles of rows will read them; else on the way, by warps 8-11. Codes carry no scale into the products: the key's scale multiplies the score and
 // the value's scale the weight, both from shared memory. Warp 12 issues the MMAs.
 // K and V have rings of their own (a K tile is free once both S are there, a V tile after both
 // products), of three tiles each for head sizes up to 64 and two for 128.
@@ -47,9 +46,6 @@ struct Layout {
 // Byte offset of the 16 bytes at chunk c (of 8) of row r in a 128-byte-swizzled half tile.
 __device__ __forceinline__ uint32_t swizzled(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
-}
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&t);
@@ -68,6 +64,48 @@ __device__ __forceinline__ bool drop_odd2(uint32_t& x) {  // infinities and NaN 
     return lo || hi;
 }
 
+// Two float32 operations an instruction: (x, y) = (x s + t, y s + t); (x, y) += (a, b); (x, y) *= (a, b).
+__device__ __forceinline__ void fma2(uint32_t& x, uint32_t& y, float s, float t) {
+    asm("{\n\t.reg .b64 v, a, b;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 a, {%2, %2};\n\tmov.b64 b, {%3, %3};\n\t"
+        "fma.rn.f32x2 v, v, a, b;\n\tmov.b64 {%0, %1}, v;\n\t}"
+        : "+r"(x), "+r"(y)
+        : "f"(s), "f"(t));
+}
+__device__ __forceinline__ void add2(uint32_t& x, uint32_t& y, float a, float b) {
+    asm("{\n\t.reg .b64 v, w;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 w, {%2, %3};\n\tadd.rn.f32x2 v, v, w;\n\tmov.b64 {%0, %1}, v;\n\t}"
+        : "+r"(x), "+r"(y)
+        : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void mul2(uint32_t& x, uint32_t& y, float a, float b) {
+    asm("{\n\t.reg .b64 v, w;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 w, {%2, %3};\n\tmul.rn.f32x2 v, v, w;\n\tmov.b64 {%0, %1}, v;\n\t}"
+        : "+r"(x), "+r"(y)
+        : "f"(a), "f"(b));
+}
+
+// Wait for a phase: polled at first (try_wait suspends the thread, and its wake-up takes longer than most
+// of the waits here), then bounded by the clock.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint64_t limit) {
+    const uint32_t at = saddr(bar);
+#pragma unroll 1
+    for (int i = 0; i < 4096; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(at), "r"(parity)
+            : "memory");
+        if (ok) return true;
+    }
+    return mbar_wait(bar, parity, nullptr, limit);
+}
+
+// Rows that a sequence takes per head once expanded: whole tiles of keys.
+__device__ __forceinline__ int expanded_rows(const Pages& p, int b) {
+    return (min(max(__ldg(p.kv_len + b), 0), p.capacity) + KT - 1) / KT * KT;
+}
+
 // What one block works on.
 struct Item {
     int b, hk, split, s0, n, R, row0;  // rows row0 .. row0 + 255 of R
@@ -77,8 +115,14 @@ struct Item {
     __device__ __forceinline__ int last(int row, int G) const { return min(kv - 1, kv_all - n + row / G); }
 };
 
-template <int HSP, bool Q8>
-__global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const AttnArgs a) {
+// Where the keys come from: bf16 pages, by TMA; 8-bit pages, unpacked by warps 8-11; or 8-bit codes
+// already laid out as bf16 in the workspace (expand_kernel), by TMA.
+enum { PAGES16, PAGES8, EXPANDED };
+
+template <int HSP, int FROM>
+__global__ void __launch_bounds__(THREADS, 1)
+    attn_tiles_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
+    constexpr bool Q8 = FROM != PAGES16;
     using L = Layout<HSP>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -88,14 +132,14 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const AttnArgs a
     float* s_ks = reinterpret_cast<float*>(smem + L::SCALES);  // [4][128]: scale of the scores per key
     float* s_vs = s_ks + 4 * KT;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BARS);
-    uint64_t* q_full = bars;         // [2] tile's rows are there (128 arrivals)
-    uint64_t* k_full = bars + 2;     // [3] (128)
+    uint64_t* q_full = bars;         // [2] tile's rows are there (one arrival per warp)
+    uint64_t* k_full = bars + 2;     // [3]
     uint64_t* k_empty = bars + 5;    // [3]
-    uint64_t* v_full = bars + 8;     // [3] (128)
+    uint64_t* v_full = bars + 8;     // [3]
     uint64_t* v_empty = bars + 11;   // [3]
-    uint64_t* c_full = bars + 14;    // [4] the tile's scales and refused pages are there (128)
+    uint64_t* c_full = bars + 14;    // [4] the tile's scales and refused pages are there
     uint64_t* bar_s = bars + 18;     // [2] S_g is there
-    uint64_t* bar_p = bars + 20;     // [2] P_g is there (128)
+    uint64_t* bar_p = bars + 20;     // [2] P_g is there (one arrival per warp)
     uint64_t* bar_o = bars + 22;     // [2] O_g is complete
     uint64_t* bar_drain = bars + 24;
     volatile uint32_t* s_bad = reinterpret_cast<volatile uint32_t*>(bars + 25);  // [4] 16-key groups on refused pages
@@ -141,18 +185,18 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const AttnArgs a
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_full[i], 128);
+            mbar_init(&q_full[i], 4);
             mbar_init(&bar_s[i], 1);
-            mbar_init(&bar_p[i], 128);
+            mbar_init(&bar_p[i], 4);
             mbar_init(&bar_o[i], 1);
         }
         for (int i = 0; i < 3; ++i) {
-            mbar_init(&k_full[i], 128);
+            mbar_init(&k_full[i], 1);
             mbar_init(&k_empty[i], 1);
-            mbar_init(&v_full[i], 128);
+            mbar_init(&v_full[i], 1);
             mbar_init(&v_empty[i], 1);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(&c_full[i], 128);
+        for (int i = 0; i < 4; ++i) mbar_init(&c_full[i], 1);
         mbar_init(bar_drain, 1);
         *s_odd = 0;
         for (int i = 0; i < 4; ++i) s_bad[i] = 0;
@@ -187,10 +231,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const AttnArgs a
                 __syncwarp();
                 issued = true;
             };
-            if (n_kv > 0) ok = __all_sync(0xffffffffu, mbar_wait(&k_full[0], 0, nullptr, WAIT_NS));
+            if (n_kv > 0) ok = __all_sync(0xffffffffu, wait_phase(&k_full[0], 0, WAIT_NS));
             for (int g = 0; g < 2 && ok; ++g)
                 if (it.tiles(g) > 0) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&q_full[g], 0, nullptr, WAIT_NS));
+                    ok = __all_sync(0xffffffffu, wait_phase(&q_full[g], 0, WAIT_NS));
                     if (!ok) break;
                     tc_fence_after();
                     scores(g, 0);
@@ -204,8 +248,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const AttnArgs a
                 bool have_v = false, have_k = false;
                 for (int g = 0; g < 2 && ok; ++g) {
                     if (j >= it.tiles(g)) continue;
-                    ok = __all_sync(0xffffffffu, mbar_wait(&bar_p[g], j & 1, nullptr, WAIT_NS));
-                    if (ok && !have_v) ok = __all_sync(0xffffffffu, mbar_wait(&v_full[stage], phase, nullptr, WAIT_NS));
+                    ok = __all_sync(0xffffffffu, wait_phase(&bar_p[g], j & 1, WAIT_NS));
+                    if (ok && !have_v) ok = __all_sync(0xffffffffu, wait_phase(&v_full[stage], phase, WAIT_NS));
                     if (!ok) break;
                     have_v = true;
                     tc_fence_after();
@@ -218,7 +262,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const AttnArgs a
                     }
                     __syncwarp();
                     if (j + 1 < it.tiles(g)) {
-                        if (!have_k) ok = __all_sync(0xffffffffu, mbar_wait(&k_full[sn], pn, nullptr, WAIT_NS));
+                        if (!have_k) ok = __all_sync(0xffffffffu, wait_phase(&k_full[sn], pn, WAIT_NS));
                         if (!ok) break;
                         have_k = true;
                         tc_fence_after();
@@ -238,7 +282,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const AttnArgs a
             if (issued) {
                 if (elect_one()) {
                     umma_commit(bar_drain);
-                    mbar_wait(bar_drain, 0, nullptr, ok ? WAIT_NS : WAIT_NS / 5);
+                    wait_phase(bar_drain, 0, ok ? WAIT_NS : WAIT_NS / 5);
                 }
                 __syncwarp();
             }
@@ -246,160 +290,168 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const AttnArgs a
         }
     } else if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-        const int p = tid - 256;
-        const int tpr = Q8 ? HSP / 16 : 8;  // threads a row (bf16: a 128-byte half of it)
+        const int row_bytes = FROM == PAGES8 ? hs : 2 * hs;
         const int clear = it.kv_all - it.n + it.row0 / a.G;  // every row sees the keys up to here
-        // this thread's rows of a unit are (p / tpr) + i * (128 / tpr)
-        constexpr int PASSES = Q8 ? HSP / 16 : 8;
-        uint4 buf[2][Q8 ? PASSES : 1];
         bool ok = true, bad_page = false, odd = false;
-        int ids = -1;  // lane i < 8: the page of keys 16 i .. of the tile, or -1
+        int ids = 0;  // lane i < 8: the page of keys 16 i .. of the tile
+        bool bad = false;
         auto look_up = [&](int j) {
             const int pos = it.k_begin + j * KT + (lane & 7) * 16;
-            ids = -1;
+            ids = 0;
+            bad = false;
             if (pos < it.k_end) {
                 ids = __ldg(a.p.table + it.b * a.p.ld_table + (pos >> a.p.page_log2));
                 if (ids < 0 || ids >= a.p.n_pages) {
-                    ids = -1;
-                    bad_page = true;
+                    ids = 0;
+                    bad = bad_page = true;
                 }
             }
         };
-        // the token row of key r of tile j, or -1 where there is none to read
-        auto token = [&](int j, int r) -> int64_t {
-            const int id = __shfl_sync(0xffffffffu, ids, r >> 4);
-            const int pos = it.k_begin + j * KT + r;
-            if (id < 0 || pos >= it.k_end) return -1;
+        // keys of a group of 16 lie together in a page: the first one's row
+        auto group_row = [&](int j, int grp) -> int64_t {
+            const int id = __shfl_sync(0xffffffffu, ids, grp);
+            const int pos = it.k_begin + j * KT + grp * 16;
             return (((int64_t)id * a.p.Hkv + it.hk) << a.p.page_log2) + (pos & ((1 << a.p.page_log2) - 1));
         };
-        auto load8 = [&](int j, const void* pages, uint4 (&to)[Q8 ? PASSES : 1]) {  // codes into registers
+        // the scales of tile j, four keys a lane, read one tile ahead; then they and the refused pages are
+        // left for the softmax
+        float4 ks_next = make_float4(0.f, 0.f, 0.f, 0.f), vs_next = ks_next;
+        auto load_scales = [&](int j) {
             if constexpr (Q8) {
-#pragma unroll
-                for (int i = 0; i < PASSES; ++i) {
-                    const int64_t row = token(j, p / tpr + i * (128 / tpr));
-                    const int d = (p % tpr) * 16;
-                    to[i] = make_uint4(0, 0, 0, 0);
-                    if (row >= 0 && d < hs) to[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const int8_t*>(pages) + row * hs + d));
+                const int64_t row = group_row(j, lane >> 2) + (lane & 3) * 4;
+                ks_next = vs_next = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (lane * 4 < it.k_end - (it.k_begin + j * KT)) {  // (a page's rows past the end exist)
+                    ks_next = __ldg(reinterpret_cast<const float4*>(a.p.k_scale + row));
+                    vs_next = __ldg(reinterpret_cast<const float4*>(a.p.v_scale + row));
                 }
             }
         };
-        auto put8 = [&](uint8_t* tile, const uint4 (&from)[Q8 ? PASSES : 1]) {
+        auto leave_scales = [&](int j, unsigned refused) {
             if constexpr (Q8) {
+                const float c = a.scale_log2;
+                reinterpret_cast<float4*>(s_ks + (j & 3) * KT)[lane] = make_float4(ks_next.x * c, ks_next.y * c, ks_next.z * c, ks_next.w * c);
+                reinterpret_cast<float4*>(s_vs + (j & 3) * KT)[lane] = vs_next;
+            }
+            if (lane == 0) s_bad[j & 3] = refused;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c_full[j & 3]);
+        };
+        if constexpr (FROM != PAGES8) {
+            // Warp 8 sends for the tiles: whole boxes of a page's rows (EXPANDED: the tile's 128 rows) by TMA.
+            // Tiles of V that hold keys some row must not see, or past the end, or on refused pages, it copies
+            // itself: what is not finite or not there becomes zeros (and is put back at the end for the rows
+            // that see it). EXPANDED tiles are finite, and zeros past the end.
+            const int box = FROM == EXPANDED ? KT : min(KT, 1 << a.p.page_log2);
+            int64_t base_row = 0;  // EXPANDED: this head's first row
+            if constexpr (FROM == EXPANDED) {
+                int64_t sum = 0;
+                for (int i = lane; i < it.b; i += 32) sum += expanded_rows(a.p, i);
+                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                base_row = sum * a.p.Hkv + (int64_t)it.hk * expanded_rows(a.p, it.b) + it.k_begin;
+            }
+            int in_flight_k = -1, in_flight_v = -1;
+            if (warp == 8 && n_kv > 0) {
+                look_up(0);
+                load_scales(0);
+            }
+            for (int j = 0; warp == 8 && j < n_kv; ++j) {
+                const uint32_t stage = j % L::STAGES, phase = (j / L::STAGES) & 1;
+                const unsigned refused = __ballot_sync(0xffffffffu, lane < 8 && bad);
+                const bool checked = FROM == PAGES16 && (refused || it.k_begin + j * KT + KT - 1 > min(clear, it.k_end - 1));
+                const int left = it.k_end - (it.k_begin + j * KT);  // keys r < left exist
+                const int row = (int)(FROM == EXPANDED ? base_row + (int64_t)j * KT : group_row(j, (lane & 7) * box >> 4));
+                ok = __all_sync(0xffffffffu, wait_phase(&k_empty[stage], phase ^ 1, WAIT_NS));
+                if (!ok) break;
+                leave_scales(j, refused);
+                auto send = [&](const CUtensorMap* map, uint8_t* tile, uint64_t* full) {
+                    if (lane == 0) mbar_expect_tx(full, L::TILE);
+                    __syncwarp();
+                    if (lane < KT / box)
+                        for (int h = 0; h < L::HALVES; ++h) tma_load_2d(map, full, tile + h * HALF + lane * box * 128, h * 64, row);
+                    __syncwarp();
+                };
+                send(&tm_k, sK + stage * L::TILE, &k_full[stage]);
+                in_flight_k = j;
+                ok = __all_sync(0xffffffffu, wait_phase(&v_empty[stage], phase ^ 1, WAIT_NS));
+                if (!ok) break;
+                if (!checked) {
+                    send(&tm_v, sV + stage * L::TILE, &v_full[stage]);
+                } else {
+                    uint8_t* tile = sV + stage * L::TILE;
+                    for (int grp = 0; grp < 8; ++grp) {
+                        const char* src = static_cast<const char*>(a.p.v) + group_row(j, grp) * row_bytes;
+                        const bool none = refused >> grp & 1;
 #pragma unroll
+                        for (int i = 0; i < 4 * L::HALVES; ++i) {
+                            const int r = i / L::HALVES * 4 + lane / 8, c = (i % L::HALVES) * 8 + lane % 8;
+                            uint4 x = make_uint4(0, 0, 0, 0);
+                            if (!none && grp * 16 + r < left && c * 8 < hs) x = __ldg(reinterpret_cast<const uint4*>(src + r * row_bytes + c * 16));
+                            odd |= drop_odd2(x.x) | drop_odd2(x.y) | drop_odd2(x.z) | drop_odd2(x.w);
+                            *reinterpret_cast<uint4*>(tile + (c >> 3) * HALF + swizzled(grp * 16 + r, c & 7)) = x;
+                        }
+                    }
+                    if (odd) *s_odd = 1;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&v_full[stage]);
+                }
+                in_flight_v = j;
+                if (j + 1 < n_kv) {
+                    look_up(j + 1);
+                    load_scales(j + 1);
+                }
+            }
+            if (!ok && warp == 8) {  // the copies in flight land before the block ends
+                for (int j = max(0, in_flight_k - L::STAGES + 1); j <= in_flight_k; ++j) wait_phase(&k_full[j % L::STAGES], (j / L::STAGES) & 1, WAIT_NS / 5);
+                for (int j = max(0, in_flight_v - L::STAGES + 1); j <= in_flight_v; ++j) wait_phase(&v_full[j % L::STAGES], (j / L::STAGES) & 1, WAIT_NS / 5);
+            }
+        } else {
+            // each warp brings whole tiles: warps 8 and 10 those of K in turn, 9 and 11 those of V
+            const bool is_v = warp & 1;
+            const char* pages = static_cast<const char*>(is_v ? a.p.v : a.p.k);
+            uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
+            int j = (warp - 8) >> 1;
+            if (j < n_kv) {
+                look_up(j);
+                if (!is_v) load_scales(j);
+            }
+            for (; j < n_kv; j += 2) {
+                const uint32_t stage = j % L::STAGES, phase = (j / L::STAGES) & 1;
+                const unsigned refused = __ballot_sync(0xffffffffu, lane < 8 && bad);
+                ok = __all_sync(0xffffffffu, wait_phase(&empty[stage], phase ^ 1, WAIT_NS));
+                if (!ok) break;
+                uint8_t* tile = (is_v ? sV : sK) + stage * L::TILE;
+                if (!is_v) leave_scales(j, refused);
+                // lane: 16 codes of a row, 128 / HSP * 4 rows a pass; loads run four passes ahead
+                constexpr int TPR = HSP / 16, RPP = 32 / TPR, PASSES = KT / RPP;
+                const int c = lane % TPR, half = c >> 2, r_in = lane / TPR;
+                const int at = min(c * 16, row_bytes - 16);  // (dims past hs: Q is zero there, and they are not stored)
+                uint4 x[4];
+                auto load = [&](int i) {
+                    const int r = i * RPP + r_in;
+                    const int64_t row = group_row(j, (i * RPP) >> 4) + (r & 15);
+                    return __ldg(reinterpret_cast<const uint4*>(pages + row * row_bytes + at));
+                };
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = load(i);
+#pragma unroll 4
                 for (int i = 0; i < PASSES; ++i) {
-                    const int r = p / tpr + i * (128 / tpr), c = p % tpr, half = c >> 2;
-                    const uint4 x = from[i];
-                    const uint4 lo = make_uint4(codes_pair(x.x, 0), codes_pair(x.x, 1), codes_pair(x.y, 0), codes_pair(x.y, 1));
-                    const uint4 hi = make_uint4(codes_pair(x.z, 0), codes_pair(x.z, 1), codes_pair(x.w, 0), codes_pair(x.w, 1));
+                    const uint4 now = x[i & 3];
+                    if (i + 4 < PASSES) x[i & 3] = load(i + 4);
+                    const int r = i * RPP + r_in;
+                    const uint4 lo = make_uint4(codes_pair(now.x, 0), codes_pair(now.x, 1), codes_pair(now.y, 0), codes_pair(now.y, 1));
+                    const uint4 hi = make_uint4(codes_pair(now.z, 0), codes_pair(now.z, 1), codes_pair(now.w, 0), codes_pair(now.w, 1));
                     // the two halves' threads store even and odd chunks in turn: no bank conflicts
                     *reinterpret_cast<uint4*>(tile + half * HALF + swizzled(r, 2 * (c & 3) + half)) = half ? hi : lo;
                     *reinterpret_cast<uint4*>(tile + half * HALF + swizzled(r, 2 * (c & 3) + (half ^ 1))) = half ? lo : hi;
                 }
-            }
-        };
-        auto copy16 = [&](int j, const void* pages, uint8_t* tile) {  // bf16 rows by cp.async
-            const uint32_t base = saddr(tile);
-#pragma unroll
-            for (int h = 0; h < L::HALVES; ++h)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int r = p / 8 + i * 16, c = p % 8, d = h * 64 + c * 8;
-                    const int64_t row = token(j, r);
-                    const bool real = row >= 0 && d < hs;
-                    cp_async16(base + h * HALF + swizzled(r, c), static_cast<const __nv_bfloat16*>(pages) + (real ? row * hs + d : 0), real);
-                }
-        };
-        auto copy16_checked = [&](int j, const void* pages, uint8_t* tile) {  // V where some row must not see an odd value
-            for (int h = 0; h < L::HALVES; ++h)
-#pragma unroll 4
-                for (int i = 0; i < 8; ++i) {
-                    const int r = p / 8 + i * 16, c = p % 8, d = h * 64 + c * 8;
-                    const int64_t row = token(j, r);
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (row >= 0 && d < hs) x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(pages) + row * hs + d));
-                    odd |= drop_odd2(x.x) | drop_odd2(x.y) | drop_odd2(x.z) | drop_odd2(x.w);
-                    *reinterpret_cast<uint4*>(tile + h * HALF + swizzled(r, c)) = x;
-                }
-        };
-        auto scales = [&](int j) {  // thread p: key p of the tile; and which groups of 16 lie on refused pages
-            const int64_t row = token(j, p);
-            if constexpr (Q8) {
-                s_ks[(j & 3) * KT + p] = row >= 0 ? a.p.k_scale[row] * a.scale_log2 : 0.f;
-                s_vs[(j & 3) * KT + p] = row >= 0 ? a.p.v_scale[row] : 0.f;
-            }
-            const unsigned bad = __ballot_sync(0xffffffffu, lane < 8 && ids < 0 && it.k_begin + j * KT + lane * 16 < it.k_end);
-            if (p == 0) s_bad[j & 3] = bad;
-            mbar_arrive(&c_full[j & 3]);
-        };
-        uint32_t stage = 0, phase = 0;
-        // bf16: a unit (K or V of a tile) is announced when the same kind's unit LAG tiles later has been
-        // issued. One tile less than the ring holds: that later unit waits only for products that
-        // come before those that need this one.
-        constexpr int LAG = L::STAGES - 1;
-        auto landed = [&](uint64_t* full) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(2 * LAG) : "memory");
-            fence_proxy_async_smem();
-            mbar_arrive(&full[stage + 1 == L::STAGES ? 0 : stage + 1]);
-        };
-        if (n_kv > 0) {
-            look_up(0);
-            load8(0, a.p.k, buf[0]);
-            load8(0, a.p.v, buf[1]);
-        }
-        for (int j = 0; j < n_kv && ok; ++j) {
-            ok = mbar_wait(&k_empty[stage], phase ^ 1, nullptr, WAIT_NS);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
-            const int id_now = ids;
-            if constexpr (Q8) {
-                put8(sK + stage * L::TILE, buf[0]);
-                scales(j);
-                if (j + 1 < n_kv) {
-                    look_up(j + 1);
-                    load8(j + 1, a.p.k, buf[0]);
+                if (j + 2 < n_kv) {
+                    look_up(j + 2);
+                    if (!is_v) load_scales(j + 2);
                 }
                 fence_proxy_async_smem();
-                mbar_arrive(&k_full[stage]);
-            } else {
-                copy16(j, a.p.k, sK + stage * L::TILE);
-                asm volatile("cp.async.commit_group;" ::: "memory");
-                scales(j);
-                if (j >= LAG) landed(k_full);
-            }
-            ok = mbar_wait(&v_empty[stage], phase ^ 1, nullptr, WAIT_NS);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
-            if constexpr (Q8) {
-                put8(sV + stage * L::TILE, buf[1]);
-                if (j + 1 < n_kv) load8(j + 1, a.p.v, buf[1]);
-                fence_proxy_async_smem();
-                mbar_arrive(&v_full[stage]);
-            } else {
-                ids = id_now;
-                if (it.k_begin + j * KT + KT - 1 > clear) {
-                    copy16_checked(j, a.p.v, sV + stage * L::TILE);
-                    if (odd) *s_odd = 1;
-                } else {
-                    copy16(j, a.p.v, sV + stage * L::TILE);
-                }
-                asm volatile("cp.async.commit_group;" ::: "memory");
-                if (j + 1 < n_kv) look_up(j + 1);
-                if (j >= LAG) landed(v_full);
-            }
-            if (++stage == L::STAGES) stage = 0, phase ^= 1;
-        }
-        if constexpr (!Q8) {
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            if (ok && n_kv > 0) {
-                fence_proxy_async_smem();
-                for (int i = max(0, n_kv - LAG); i < n_kv; ++i) {
-                    mbar_arrive(&k_full[i % L::STAGES]);
-                    mbar_arrive(&v_full[i % L::STAGES]);
-                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[stage]);
             }
         }
         if (bad_page) report(a.err, GK_ERR_INDEX);
@@ -421,14 +473,15 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const AttnArgs a
                 *reinterpret_cast<uint4*>(sQ + g * L::TILE + (c >> 3) * HALF + swizzled(rr, c & 7)) = x;
             }
             fence_proxy_async_smem();
-            mbar_arrive(&q_full[g]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full[g]);
         }
         const int last = mine ? min(it.last(row, a.G), it.k_end - 1) : -1;
         const float sl2 = a.scale_log2;
         float m_ref = -INFINITY, l = 0.f;
         for (int j = 0; j < my_kt; ++j) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&c_full[j & 3], (j >> 2) & 1, nullptr, WAIT_NS) &&
-                                             mbar_wait(&bar_s[g], j & 1, nullptr, WAIT_NS))) {
+            if (!__all_sync(0xffffffffu, wait_phase(&c_full[j & 3], (j >> 2) & 1, WAIT_NS) &&
+                                             wait_phase(&bar_s[g], j & 1, WAIT_NS))) {
                 failed = true;
                 break;
             }
@@ -439,23 +492,20 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const AttnArgs a
             tmem_wait_ld_only();
 #pragma unroll
             for (int c = 0; c < 4; ++c) reg_fence32(sv[c]);
-            const float4* ks4 = reinterpret_cast<const float4*>(s_ks + (j & 3) * KT);
-            const float4* vs4 = reinterpret_cast<const float4*>(s_vs + (j & 3) * KT);
+            const int lim = last - (it.k_begin + j * KT) + 1;  // keys i < lim are seen
+            const uint32_t bad = s_bad[j & 3];
+            const bool part = __any_sync(0xffffffffu, lim < KT) || bad;
             if constexpr (Q8) {
+                const float4* ks4 = reinterpret_cast<const float4*>(s_ks + (j & 3) * KT);
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float4 k4 = ks4[c * 8 + i];
-                        sv[c][4 * i] = __float_as_uint(__uint_as_float(sv[c][4 * i]) * k4.x);
-                        sv[c][4 * i + 1] = __float_as_uint(__uint_as_float(sv[c][4 * i + 1]) * k4.y);
-                        sv[c][4 * i + 2] = __float_as_uint(__uint_as_float(sv[c][4 * i + 2]) * k4.z);
-                        sv[c][4 * i + 3] = __float_as_uint(__uint_as_float(sv[c][4 * i + 3]) * k4.w);
+                        mul2(sv[c][4 * i], sv[c][4 * i + 1], k4.x, k4.y);
+                        mul2(sv[c][4 * i + 2], sv[c][4 * i + 3], k4.z, k4.w);
                     }
             }
-            const int lim = last - (it.k_begin + j * KT) + 1;  // keys i < lim are seen
-            const uint32_t bad = s_bad[j & 3];
-            const bool part = __any_sync(0xffffffffu, lim < KT) || bad;
             if (part) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
@@ -463,14 +513,14 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const AttnArgs a
                     for (int i = 0; i < 32; ++i)
                         if (c * 32 + i >= lim || (bad >> (c * 2 + (i >> 4)) & 1)) sv[c][i] = 0xff800000u;
             }
-            float mx[8];
+            float mx[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) mx[e] = __uint_as_float(sv[0][e]);
+            for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(sv[0][e]);
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
-                for (int i = 0; i < 32; ++i) mx[i & 7] = fmaxf(mx[i & 7], __uint_as_float(sv[c][i]));
-            const float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+                for (int i = 0; i < 16; ++i) mx[i & 3] = fmaxf(fmaxf(mx[i & 3], __uint_as_float(sv[c][2 * i])), __uint_as_float(sv[c][2 * i + 1]));
+            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             const float m_new = fmaxf(m_ref, Q8 ? mt : mt * sl2);
             float corr = 1.f;
             const bool rescale = m_new > m_ref + 8.f;
@@ -480,32 +530,43 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const AttnArgs a
                 m_ref = m_new;
             }
             const float ref = m_ref == -INFINITY ? 0.f : m_ref;  // (a row that has seen nothing yet)
-            float ps[4] = {0.f, 0.f, 0.f, 0.f};
+            uint32_t ps[4] = {0, 0, 0, 0};  // two pairs of running sums
+            const float4* vs4 = reinterpret_cast<const float4*>(s_vs + (j & 3) * KT);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 uint32_t pw[16];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
+                    uint32_t* w = &sv[c][4 * e];
+                    const float one = Q8 ? 1.f : sl2;
+                    fma2(w[0], w[1], one, -ref);
+                    fma2(w[2], w[3], one, -ref);
                     float p[4];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const float s = __uint_as_float(sv[c][4 * e + x]);
-                        p[x] = ex2_hw(Q8 ? s - ref : fmaf(s, sl2, -ref));
-                        ps[x] += p[x];
-                    }
+                    for (int x = 0; x < 4; ++x) p[x] = ex2_hw(__uint_as_float(w[x]));
+                    add2(ps[0], ps[1], p[0], p[1]);
+                    add2(ps[2], ps[3], p[2], p[3]);
                     if constexpr (Q8) {
                         const float4 v4 = vs4[c * 8 + e];
-                        const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+                        uint32_t y[4];
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)  // (an unseen key's scale may be anything)
-                            p[x] = part && sv[c][4 * e + x] == 0xff800000u ? 0.f : p[x] * v[x];
+                        for (int x = 0; x < 4; ++x) y[x] = __float_as_uint(p[x]);
+                        mul2(y[0], y[1], v4.x, v4.y);
+                        mul2(y[2], y[3], v4.z, v4.w);
+                        if (part) {  // an unseen key's scale may be anything
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                if (w[x] == 0xff800000u) y[x] = 0;
+                        }
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) p[x] = __uint_as_float(y[x]);
                     }
                     pw[2 * e] = pack2(p[0], p[1]);
                     pw[2 * e + 1] = pack2(p[2], p[3]);
                 }
                 tmem_st16(lane_addr + g * 128 + c * 16, pw);
             }
-            l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+            l += (__uint_as_float(ps[0]) + __uint_as_float(ps[1])) + (__uint_as_float(ps[2]) + __uint_as_float(ps[3]));
             if (j > 0 && __any_sync(0xffffffffu, rescale)) {
 #pragma unroll
                 for (int c = 0; c < HSP / 32; ++c) {
@@ -520,10 +581,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const AttnArgs a
             }
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(&bar_p[g]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_p[g]);
         }
         if (!failed && my_kt > 0) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&bar_o[g], 0, nullptr, WAIT_NS))) failed = true;
+            if (!__all_sync(0xffffffffu, wait_phase(&bar_o[g], 0, WAIT_NS))) failed = true;
             tc_fence_after();
         }
         if (!failed) {
@@ -584,23 +646,71 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tiles_kernel(const AttnArgs a
     }
 }
 
-template <int HSP, bool Q8>
-gk_status tiles(gk_ctx* ctx, const AttnArgs& a) {
-    if (cudaFuncSetAttribute(attn_tiles_kernel<HSP, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<HSP>::BYTES) !=
+// The codes of every sequence as bf16 rows, heads apart: sequence b's head h at row
+// (sum of expanded_rows before b) * Hkv + h * expanded_rows(b), zeros past its end and on refused pages.
+// One pass, a block per 64 positions of a head.
+__global__ void __launch_bounds__(256) expand_kernel(const AttnArgs a, __nv_bfloat16* k_out, __nv_bfloat16* v_out) {
+    wait_for_earlier_kernels();
+    const int b = blockIdx.z, hk = blockIdx.y, len = expanded_rows(a.p, b), p0 = blockIdx.x * 64;
+    if (p0 >= len) return;
+    const int lane = threadIdx.x & 31, kv = min(max(a.p.kv_len[b], 0), a.p.capacity), hs = a.p.hs;
+    int64_t base = 0;
+    for (int i = lane; i < b; i += 32) base += expanded_rows(a.p, i);
+    for (int o = 16; o > 0; o >>= 1) base += __shfl_xor_sync(0xffffffffu, base, o);
+    base = base * a.p.Hkv + (int64_t)hk * len;
+    const int per = hs >> 4;
+    for (int i = threadIdx.x; i < 64 * per; i += 256) {
+        const int pos = p0 + i / per, d = (i % per) * 16;
+        const int id = pos < kv ? __ldg(a.p.table + b * a.p.ld_table + (pos >> a.p.page_log2)) : -1;
+        uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+        if (id >= 0 && id < a.p.n_pages) {
+            const int64_t at = ((((int64_t)id * a.p.Hkv + hk) << a.p.page_log2) + (pos & ((1 << a.p.page_log2) - 1))) * hs + d;
+            x[0] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const int8_t*>(a.p.k) + at));
+            x[1] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const int8_t*>(a.p.v) + at));
+        }
+        const int64_t out = (base + pos) * hs + d;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            uint4* dst = reinterpret_cast<uint4*>((e ? v_out : k_out) + out);
+            dst[0] = make_uint4(codes_pair(x[e].x, 0), codes_pair(x[e].x, 1), codes_pair(x[e].y, 0), codes_pair(x[e].y, 1));
+            dst[1] = make_uint4(codes_pair(x[e].z, 0), codes_pair(x[e].z, 1), codes_pair(x[e].w, 0), codes_pair(x[e].w, 1));
+        }
+    }
+}
+
+template <int HSP, int FROM>
+gk_status tiles(gk_ctx* ctx, const AttnArgs& a, const __nv_bfloat16* k, const __nv_bfloat16* v, int64_t rows, int box) {
+    if (cudaFuncSetAttribute(attn_tiles_kernel<HSP, FROM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<HSP>::BYTES) !=
         cudaSuccess) {
         cudaGetLastError();
         return fail(ctx, GK_ERR_CUDA, "gk_paged_attn: shared memory");
     }
+    CUtensorMap mk{}, mv{};
+    if (FROM != PAGES8)
+        GK_REQUIRE(ctx, make_map(&mk, k, a.p.hs, rows, a.p.hs, box) && make_map(&mv, v, a.p.hs, rows, a.p.hs, box), GK_ERR_CUDA,
+                   "gk_paged_attn: tensor map");
     const int64_t pairs = cdiv((int64_t)a.max_q * a.G, 2 * QT);
-    return launch_dependent(ctx, "paged_attn_tiles", attn_tiles_kernel<HSP, Q8>,
-                            dim3((unsigned)(pairs * a.splits), (unsigned)a.p.Hkv, (unsigned)a.B), dim3(THREADS), Layout<HSP>::BYTES, 1, a);
+    return launch_dependent(ctx, "paged_attn_tiles", attn_tiles_kernel<HSP, FROM>,
+                            dim3((unsigned)(pairs * a.splits), (unsigned)a.p.Hkv, (unsigned)a.B), dim3(THREADS), Layout<HSP>::BYTES, 1, a,
+                            mk, mv);
 }
 
 }  // namespace
 
 gk_status launch_attn_tiles(gk_ctx* ctx, const AttnArgs& a) {
-    if (a.p.hs <= 64) return a.p.k_scale ? tiles<64, true>(ctx, a) : tiles<64, false>(ctx, a);
-    return a.p.k_scale ? tiles<128, true>(ctx, a) : tiles<128, false>(ctx, a);
+    const bool small = a.p.hs <= 64;
+    if (a.expanded_k) {
+        const int64_t rows = a.expanded_rows;
+        GK_TRY(launch_dependent(ctx, "paged_attn_expand", expand_kernel, dim3((unsigned)cdiv(a.p.capacity, 128) * 2, (unsigned)a.p.Hkv, (unsigned)a.B),
+                                dim3(256), 0, 1, a, a.expanded_k, a.expanded_v));
+        return small ? tiles<64, EXPANDED>(ctx, a, a.expanded_k, a.expanded_v, rows, KT)
+                     : tiles<128, EXPANDED>(ctx, a, a.expanded_k, a.expanded_v, rows, KT);
+    }
+    if (a.p.k_scale) return small ? tiles<64, PAGES8>(ctx, a, nullptr, nullptr, 0, 0) : tiles<128, PAGES8>(ctx, a, nullptr, nullptr, 0, 0);
+    const int64_t rows = (a.p.n_pages * a.p.Hkv) << a.p.page_log2;
+    const __nv_bfloat16 *k = static_cast<const __nv_bfloat16*>(a.p.k), *v = static_cast<const __nv_bfloat16*>(a.p.v);
+    const int box = std::min(KT, 1 << a.p.page_log2);
+    return small ? tiles<64, PAGES16>(ctx, a, k, v, rows, box) : tiles<128, PAGES16>(ctx, a, k, v, rows, box);
 }
 
 }  // namespace gk

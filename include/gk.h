@@ -406,7 +406,8 @@ gk_status gk_sample(gk_ctx* ctx, gk_kv* kv, const float* logits, int64_t ld, int
  *   page_table device int32 [B][max_pages] (row stride ld_table): token position p of sequence b
  *              is row p % page_size of page page_table[b][p / page_size].
  *   kv_len     device int32 [B]: tokens of each sequence, those of the current call included.
- * page_size is 16, 32, 64, 128 or 256; hs a multiple of 16, 16 .. 128.
+ * page_size is 16, 32, 64, 128 or 256; hs a multiple of 16, 16 .. 128; n_pages * Hkv * page_size and
+ * max_pages * page_size below 2^31 and 2^30.
  *
  * The three gk_paged_* calls below take `rows` token rows of B sequences packed one after the
  * other: sequence b has rows q_start[b] .. q_start[b+1]-1 (device int32 [B+1], ascending from 0;

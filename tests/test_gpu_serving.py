@@ -199,6 +199,8 @@ ATTN = [  # kv_len, n, H, Hkv, hs, page
     ([2600, 0, 900], [513, 3, 600], 2, 2, 64, 128),
     ([140] * 40, [2] * 40, 5, 5, 112, 16),
     ([20000, 4000], [2, 1], 16, 2, 128, 64),
+    ([6000, 3000], [300, 70], 2, 1, 64, 32),
+    ([5000, 700], [260, 600], 1, 1, 128, 16),
 ]
 
 
@@ -299,23 +301,24 @@ def test_attention_small_workspace_and_graph(gkctx):
 
     t = _t()
     rng = np.random.default_rng(600)
-    for n in (1, 70):
-        c = cache(rng, [6000, 2500], 2, 64, 64, True)
-        q = serving.bf16(rng.standard_normal((2 * n, 4, 64)))
+    for n, hs, q8 in ((1, 64, True), (70, 64, True), (70, 64, False), (300, 128, True), (300, 128, False)):
+        c = cache(rng, [6000, 2500], 2, hs, 64, q8)
+        q = serving.bf16(rng.standard_normal((2 * n, 4, hs)))
         ref = serving.paged_attn(c, q, starts([n, n]), 0.125)
+        w = 4 * hs
         for ws in (0, 1 << 16, 64 << 20):
             ctx = gk.Ctx(t.cuda.current_stream().cuda_stream, workspace_bytes=ws)
             check_attention(*attend(ctx, c, q, [n, n], 0.125), ref, ws)
             ctx.close()
         s = t.cuda.Stream()
         ctx = gk.Ctx(s, workspace_bytes=64 << 20)
-        d, y = Dev(c), t.zeros(2 * n, 256, dtype=t.bfloat16, device="cuda")
-        qd, qs = t.zeros(2 * n, 256, dtype=t.bfloat16, device="cuda"), dev(starts([n, n]))
+        d, y = Dev(c), t.zeros(2 * n, w, dtype=t.bfloat16, device="cuda")
+        qd, qs = t.zeros(2 * n, w, dtype=t.bfloat16, device="cuda"), dev(starts([n, n]))
         t.cuda.synchronize()
         g = t.cuda.CUDAGraph()
         with t.cuda.graph(g, stream=s):
-            gk.gk_paged_attn(ctx, d.h, gk.GK_BF16, qd, 256, y, 256, None, qs, 2, 4, 2 * n, n, 0.125)
-        qd.copy_(dev(q.reshape(2 * n, 256), t.bfloat16))
+            gk.gk_paged_attn(ctx, d.h, gk.GK_BF16, qd, w, y, w, None, qs, 2, 4, 2 * n, n, 0.125)
+        qd.copy_(dev(q.reshape(2 * n, w), t.bfloat16))
         for _ in range(2):
             y.zero_()
             g.replay()
