@@ -17,10 +17,11 @@
 // the value's scale the weight, both from shared memory. Warp 12 issues the MMAs.
 // K and V have rings of their own (a K tile is free once both S are there, a V tile after both
 // products), of three tiles each for head sizes up to 64 and two for 128.
-// Registers: 512 threads at 128; the softmax warpgroups take 176 each, the copying one 104, the
-// MMA warp's 48.
+// Registers: 512 threads at 128; the softmax warpgroups take 184 each, the copying one 96, the MMA warp's
+// 48 (where the copying one unpacks codes: 176, 104, 48).
 // All mbarrier waits are bounded (timeout -> GK_ERR_TIMEOUT in the error word).
 #include <algorithm>
+#include <type_traits>
 
 #include "paged_attn.cuh"
 #include "tcgen05.cuh"
@@ -118,6 +119,7 @@ struct Item {
 // Where the keys come from: bf16 pages, by TMA; 8-bit pages, unpacked by warps 8-11; or 8-bit codes
 // already laid out as bf16 in the workspace (expand_kernel), by TMA.
 enum { PAGES16, PAGES8, EXPANDED };
+constexpr uint32_t ODD_SCALES = 1u << 31;  // beside a tile's refused groups: some value's scale is not finite
 
 template <int HSP, int FROM>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -289,7 +291,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!ok) failed = true;
         }
     } else if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        if constexpr (FROM == PAGES8) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         const int row_bytes = FROM == PAGES8 ? hs : 2 * hs;
         const int clear = it.kv_all - it.n + it.row0 / a.G;  // every row sees the keys up to here
         bool ok = true, bad_page = false, odd = false;
@@ -332,6 +335,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 reinterpret_cast<float4*>(s_ks + (j & 3) * KT)[lane] = make_float4(ks_next.x * c, ks_next.y * c, ks_next.z * c, ks_next.w * c);
                 reinterpret_cast<float4*>(s_vs + (j & 3) * KT)[lane] = vs_next;
             }
+            const bool odd = !(isfinite(vs_next.x) && isfinite(vs_next.y) && isfinite(vs_next.z) && isfinite(vs_next.w));
+            if (Q8 && __any_sync(0xffffffffu, odd)) refused |= ODD_SCALES;
             if (lane == 0) s_bad[j & 3] = refused;
             __syncwarp();
             if (lane == 0) mbar_arrive(&c_full[j & 3]);
@@ -457,7 +462,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (bad_page) report(a.err, GK_ERR_INDEX);
         if (!ok) failed = true;
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        if constexpr (FROM == PAGES8) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         const int g = warp >> 2, rr = (warp & 3) * 32 + lane;
         const int row = it.row0 + g * QT + rr, my_kt = it.tiles(g);
         const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -494,7 +500,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int c = 0; c < 4; ++c) reg_fence32(sv[c]);
             const int lim = last - (it.k_begin + j * KT) + 1;  // keys i < lim are seen
             const uint32_t bad = s_bad[j & 3];
-            const bool part = __any_sync(0xffffffffu, lim < KT) || bad;
+            const bool part = __any_sync(0xffffffffu, lim < KT) || (bad & 0xff);
             if constexpr (Q8) {
                 const float4* ks4 = reinterpret_cast<const float4*>(s_ks + (j & 3) * KT);
 #pragma unroll
@@ -532,40 +538,41 @@ __global__ void __launch_bounds__(THREADS, 1)
             const float ref = m_ref == -INFINITY ? 0.f : m_ref;  // (a row that has seen nothing yet)
             uint32_t ps[4] = {0, 0, 0, 0};  // two pairs of running sums
             const float4* vs4 = reinterpret_cast<const float4*>(s_vs + (j & 3) * KT);
+            // weights of the row's 128 keys into tensor memory; `odd`: a value's scale is not finite, and keys that are
+            // not seen must be kept from it
+            auto weights = [&](auto odd) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t pw[16];
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t pw[16];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    uint32_t* w = &sv[c][4 * e];
-                    const float one = Q8 ? 1.f : sl2;
-                    fma2(w[0], w[1], one, -ref);
-                    fma2(w[2], w[3], one, -ref);
-                    float p[4];
+                    for (int e = 0; e < 8; ++e) {
+                        uint32_t* w = &sv[c][4 * e];
+                        const float one = Q8 ? 1.f : sl2;
+                        fma2(w[0], w[1], one, -ref);
+                        fma2(w[2], w[3], one, -ref);
+                        float p[4];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) p[x] = ex2_hw(__uint_as_float(w[x]));
-                    add2(ps[0], ps[1], p[0], p[1]);
-                    add2(ps[2], ps[3], p[2], p[3]);
-                    if constexpr (Q8) {
-                        const float4 v4 = vs4[c * 8 + e];
-                        uint32_t y[4];
+                        for (int x = 0; x < 4; ++x) p[x] = ex2_hw(__uint_as_float(w[x]));
+                        add2(ps[0], ps[1], p[0], p[1]);
+                        add2(ps[2], ps[3], p[2], p[3]);
+                        if constexpr (Q8) {
+                            const float4 v4 = vs4[c * 8 + e];
+                            uint32_t y[4];
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) y[x] = __float_as_uint(p[x]);
-                        mul2(y[0], y[1], v4.x, v4.y);
-                        mul2(y[2], y[3], v4.z, v4.w);
-                        if (part) {  // an unseen key's scale may be anything
+                            for (int x = 0; x < 4; ++x) y[x] = __float_as_uint(p[x]);
+                            mul2(y[0], y[1], v4.x, v4.y);
+                            mul2(y[2], y[3], v4.z, v4.w);
 #pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                if (w[x] == 0xff800000u) y[x] = 0;
+                            for (int x = 0; x < 4; ++x) p[x] = decltype(odd)::value && w[x] == 0xff800000u ? 0.f : __uint_as_float(y[x]);
                         }
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) p[x] = __uint_as_float(y[x]);
+                        pw[2 * e] = pack2(p[0], p[1]);
+                        pw[2 * e + 1] = pack2(p[2], p[3]);
                     }
-                    pw[2 * e] = pack2(p[0], p[1]);
-                    pw[2 * e + 1] = pack2(p[2], p[3]);
+                    tmem_st16(lane_addr + g * 128 + c * 16, pw);
                 }
-                tmem_st16(lane_addr + g * 128 + c * 16, pw);
-            }
+            };
+            if (Q8 && (bad & ODD_SCALES)) weights(std::true_type{});
+            else weights(std::false_type{});
             l += (__uint_as_float(ps[0]) + __uint_as_float(ps[1])) + (__uint_as_float(ps[2]) + __uint_as_float(ps[3]));
             if (j > 0 && __any_sync(0xffffffffu, rescale)) {
 #pragma unroll
