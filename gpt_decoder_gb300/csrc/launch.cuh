@@ -38,11 +38,12 @@ __device__ __forceinline__ void wait_for_earlier_kernels() { asm volatile("gridd
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The word at this block's shared-memory address p, read from block `rank` of the cluster.
+// The word at this block's shared-memory address p, read from block `rank` of the cluster. (No memory
+// clobber, so that several such reads are on their way at once: a barrier before them orders them.)
 __device__ __forceinline__ uint32_t load_cluster_u32(const void* p, int rank) {
     uint32_t at, v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at));
     return v;
 }
 __device__ __forceinline__ float load_cluster(const float* p, int rank) { return __uint_as_float(load_cluster_u32(p, rank)); }
