@@ -77,6 +77,7 @@ struct SampleArgs {
 
 struct Hist {
     uint32_t count[BINS], lo[BINS], hi[BINS];  // weights as 32 low bits and the rest
+    uint32_t part_lo[32], part_hi[32];         // sums of every 32 bins
 };
 
 struct Shared {
@@ -160,71 +161,62 @@ __device__ __forceinline__ uint64_t peers_sum(const uint32_t* p, int cluster) {
     return s;
 }
 
-// Exclusive prefix of v over the block's threads, and the block's total.
-__device__ __forceinline__ uint64_t block_prefix(Shared& sh, uint64_t v, uint64_t* total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint64_t incl = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
-    }
-    __syncthreads();
-    if (lane == 31) sh.red_w[warp] = incl;
-    __syncthreads();
-    uint64_t before = incl - v, all = 0;
-    for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) before += sh.red_w[w];
-        all += sh.red_w[w];
-    }
-    *total = all;
-    return before;
+// floor(x * all) for 0 <= x < 1 (exact down to x = 2^-40), and whether anything was cut off.
+__device__ __forceinline__ uint64_t part_of(float x, uint64_t all, bool* cut) {
+    const uint32_t b = __float_as_uint(x);
+    const int shift = (int)(b >> 23) - 86;  // x = mantissa * 2^(exponent - 150), in units of 2^-64
+    const uint64_t m = (b & 0x7fffffu) | 0x800000u;
+    const uint64_t fix = shift >= 0 ? m << shift : shift > -24 ? m >> -shift : 0;
+    *cut = fix * all != 0;
+    return __umul64hi(fix, all);
 }
-
 // A whole running sum exceeds u * all when it exceeds this; u >= 1 or NaN: the last kept.
-__device__ __forceinline__ uint64_t needed(float u, uint64_t all, bool greedy) {
-    const double ua = (double)u * (double)all;
-    return greedy ? 0 : ua < (double)all ? min((uint64_t)fmax(ua, 0.0), all - 1) : all - 1;
+__device__ __forceinline__ uint64_t needed(float u, uint64_t all) {
+    bool cut;
+    return u <= 0.f ? 0 : u < 1.f ? part_of(u, all, &cut) : all - 1;
 }
+// What the share p < 1 of a whole is reached with.
 __device__ __forceinline__ uint64_t share(float p, uint64_t all) {
-    return p > 0.f ? max((uint64_t)1, (uint64_t)ceil((double)p * (double)all)) : 1;
+    bool cut;
+    if (!(p > 0.f)) return 1;
+    const uint64_t w = part_of(p, all, &cut);
+    return max((uint64_t)1, w + (cut ? 1 : 0));
 }
 
-// The histogram as running sums, before the cluster's barrier.
-__device__ __forceinline__ void accumulate(Shared& sh, Hist& h, bool weigh) {
-    const int b = threadIdx.x * 2;
-    uint64_t v[2], all;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) v[e] = weigh ? ((uint64_t)h.hi[b + e] << 32) + h.lo[b + e] : h.count[b + e];
-    const uint64_t before = block_prefix(sh, v[0] + v[1], &all);
-    v[0] += before;
-    v[1] += v[0];
+// Sums of every 32 bins, a warp two of them, before the cluster's barrier.
+__device__ __forceinline__ void sum_parts(Hist& h, bool weigh) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        if (weigh) h.hi[b + e] = (uint32_t)(v[e] >> 32), h.lo[b + e] = (uint32_t)v[e];
-        else h.count[b + e] = (uint32_t)v[e];
+        const int part = warp * 2 + e, b = part * 32 + lane;
+        uint64_t v = weigh ? ((uint64_t)h.hi[b] << 32) + h.lo[b] : h.count[b];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane == 0) h.part_lo[part] = (uint32_t)v, h.part_hi[part] = (uint32_t)(v >> 32);
     }
+}
+__device__ __forceinline__ uint64_t warp_inclusive(uint64_t v) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t x = __shfl_up_sync(0xffffffffu, v, o);
+        if ((int)(threadIdx.x & 31) >= o) v += x;
+    }
+    return v;
 }
 
 // After it: the first bin (ascending: descending logits) at which the cluster's counts (or weights) reach
-// `want`, or the share p of them all (p >= 0), `have` before bin 0. One warp reads every 32nd sum of all the
-// blocks, then the 32 of the part where it is reached; the answers are left in sh.
+// `want`, or the share p of them all, `have` before bin 0. One warp adds the parts' sums of all the
+// blocks, then the 32 bins of the part where it is reached; the answers are left in sh.
 __device__ __forceinline__ void search(Shared& sh, const Hist& h, int cluster, bool weigh, uint64_t want, bool of_share, float p, uint64_t have) {
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
-        auto sums = [&](int b) {
-            return have + (weigh ? (peers_sum(&h.hi[b], cluster) << 32) + peers_sum(&h.lo[b], cluster) : peers_sum(&h.count[b], cluster));
-        };
-        uint64_t s = sums(lane * 32 + 31);
-        if (of_share) {
-            want = lane == 31 ? share(p, s) : 0;
-            want = __shfl_sync(0xffffffffu, want, 31);
-        }
+        uint64_t s = have + warp_inclusive((peers_sum(&h.part_hi[lane], cluster) << 32) + peers_sum(&h.part_lo[lane], cluster));
+        if (of_share) want = share(p, __shfl_sync(0xffffffffu, s, 31));
         const unsigned m = __ballot_sync(0xffffffffu, s >= want);
-        const int part = m ? __ffs(m) - 1 : 31;
+        const int part = m ? __ffs(m) - 1 : 31, b = part * 32 + lane;
         uint64_t before = __shfl_sync(0xffffffffu, s, max(part - 1, 0));
         if (part == 0) before = have;
-        s = sums(part * 32 + lane);
+        s = before + warp_inclusive(weigh ? (peers_sum(&h.hi[b], cluster) << 32) + peers_sum(&h.lo[b], cluster) : peers_sum(&h.count[b], cluster));
         const unsigned m2 = __ballot_sync(0xffffffffu, s >= want);
         const int at = m2 ? __ffs(m2) - 1 : 31;
         const uint64_t upto = __shfl_sync(0xffffffffu, s, at), above = __shfl_sync(0xffffffffu, s, max(at - 1, 0));
@@ -236,6 +228,19 @@ __device__ __forceinline__ void search(Shared& sh, const Hist& h, int cluster, b
         }
     }
     __syncthreads();
+}
+
+// Exclusive prefix of v over the block's threads, and the block's total.
+__device__ __forceinline__ uint64_t block_prefix(Shared& sh, uint64_t v, uint64_t* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint64_t incl = warp_inclusive(v);
+    __syncthreads();
+    if (lane == 31) sh.red_w[warp] = incl;
+    __syncthreads();
+    const uint64_t w = warp_inclusive(lane < THREADS / 32 ? sh.red_w[lane] : 0);
+    *total = __shfl_sync(0xffffffffu, w, 31);
+    const uint64_t before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+    return (warp ? before : 0) + incl - v;
 }
 
 template <typename T>
@@ -295,9 +300,9 @@ __global__ void __launch_bounds__(THREADS) sample_rows_kernel(const SampleArgs a
     most = __reduce_max_sync(0xffffffffu, most);
     if (lane == 0) sh.red_c[warp] = most;
     __syncthreads();
-    if (tid == 0) {
-        for (int w = 1; w < THREADS / 32; ++w) most = max(most, sh.red_c[w]);
-        sh.range[0][0] = most;
+    if (warp == 0) {
+        most = __reduce_max_sync(0xffffffffu, lane < THREADS / 32 ? sh.red_c[lane] : 0);
+        if (lane == 0) sh.range[0][0] = most;
     }
     row_barrier(cl);
     uint32_t top = 0, got[MAX_CLUSTER];
@@ -324,6 +329,18 @@ __global__ void __launch_bounds__(THREADS) sample_rows_kernel(const SampleArgs a
 
     // this warp's part of the slice, 32 neighbours a turn
     const int w0 = warp * 32 * run, turns = (max(0, min(32 * run, n - w0)) + 31) >> 5;
+    auto each = [&](auto&& f) {  // (index in the slice, logit; -inf past its end), four loads at a time
+        for (int i = 0; i < turns; i += 4) {
+            float l[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int e = w0 + (i + q) * 32 + lane;
+                l[q] = i + q < turns && e < n ? x[e] : -INFINITY;
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) f(w0 + (i + q) * 32 + lane, l[q]);
+        }
+    };
     uint32_t low = greedy ? top : KEY_NINF + 1;  // the threshold so far, as a key and as a logit
     float low_l = value_of(low);
     auto raise = [&](uint32_t key) {
@@ -331,12 +348,6 @@ __global__ void __launch_bounds__(THREADS) sample_rows_kernel(const SampleArgs a
         low_l = value_of(key);
     };
     const uint64_t least = sh.least;
-    // one thread's answer for all: what the sums have to reach
-    auto asked = [&](auto&& f) {
-        if (tid == 0) sh.asked = f();
-        __syncthreads();
-        return sh.asked;
-    };
     auto step_of = [&](float l) {
         const float z = distance(sc, l);
         return l == largest ? 0 : z < 46.5f ? (int)(z * 22.f) : BINS - 1;
@@ -353,18 +364,15 @@ __global__ void __launch_bounds__(THREADS) sample_rows_kernel(const SampleArgs a
         uint32_t* ex = sh.range[turn & 1];
         if (tid == 0) ex[0] = 0, ex[1] = 0xffffffffu, sh.n_list = 0, sh.chosen = 0;
         __syncthreads();
-        for (int i = 0; i < turns; ++i) {
-            const int e = w0 + i * 32 + lane;
-            if (e >= n) continue;
-            const float l = x[e];
-            if (!(l >= low_l)) continue;
+        each([&](int e, float l) {
+            if (!(l >= low_l)) return;
             const int step = step_of(l);
-            if (step < step_from || step > step_to) continue;
+            if (step < step_from || step > step_to) return;
             const uint32_t key = key_of(l);
             kmax = max(kmax, key), kmin = min(kmin, key);
             const uint32_t at = atomicAdd(&sh.n_list, 1u);
             if (at < LIST) sh.list_k[at] = key, sh.list_i[at] = base + e;
-        }
+        });
         kmax = __reduce_max_sync(0xffffffffu, kmax);
         kmin = __reduce_min_sync(0xffffffffu, kmin);
         if (lane == 0 && kmax) atomicMax(&ex[0], kmax), atomicMin(&ex[1], kmin);
@@ -415,16 +423,14 @@ __global__ void __launch_bounds__(THREADS) sample_rows_kernel(const SampleArgs a
     auto histogram = [&](bool weigh, uint64_t want) {
         Hist& h = sh.hist[turn++ & 1];
         clear(h);
-        for (int i = 0; i < turns; ++i) {
-            const int e = w0 + i * 32 + lane;
-            const float l = e < n ? x[e] : -INFINITY;
-            if (!(l >= low_l)) continue;
+        each([&](int, float l) {
+            if (!(l >= low_l)) return;
             const int b = step_of(l);
             if (!weigh) atomicAdd(&h.count[b], 1u);
             else if (b < BINS - 1) add_weight(h, b, weight(sh, sc, l));
-        }
+        });
         __syncthreads();
-        accumulate(sh, h, weigh);
+        sum_parts(h, weigh);
         row_barrier(cl);
         search(sh, h, cl, weigh, want, weigh, top_p, 0);
         return sh.asked;
@@ -448,7 +454,7 @@ __global__ void __launch_bounds__(THREADS) sample_rows_kernel(const SampleArgs a
                 else atomicAdd(&h.count[b], 1u);
             }
             __syncthreads();
-            accumulate(sh, h, weigh);
+            sum_parts(h, weigh);
             row_barrier(cl);
             search(sh, h, cl, weigh, want, false, 0.f, have);
             const int bin = sh.bin;
@@ -490,7 +496,7 @@ __global__ void __launch_bounds__(THREADS) sample_rows_kernel(const SampleArgs a
                         if (by_k) {
                             uint64_t all = tid < many && sh.all_k[tid] >= low ? sh.all_w[tid] : 0;
                             block_prefix(sh, all, &all);
-                            want = asked([&] { return share(top_p, all); });
+                            want = share(top_p, all);
                         }
                         decide(many, true, 0, want);
                     }
@@ -500,7 +506,7 @@ __global__ void __launch_bounds__(THREADS) sample_rows_kernel(const SampleArgs a
                     if (tid < many) sh.all_w[tid] = own;
                     uint64_t all = own;
                     block_prefix(sh, all, &all);  // (and every all_w is written)
-                    const uint64_t need = asked([&] { return needed(u, all, false); });
+                    const uint64_t need = needed(u, all);
                     if (own) {
                         const int32_t index = sh.all_i[tid];
                         uint64_t before = 0;
@@ -559,11 +565,10 @@ __global__ void __launch_bounds__(THREADS) sample_rows_kernel(const SampleArgs a
     uint64_t own = 0;
     uint32_t* packed = sh.packed[warp];
     int held = 0;
-    for (int i = 0; i < turns; ++i) {
-        const int e = w0 + i * 32 + lane;
-        const float l = e < n ? x[e] : -INFINITY;
+    each([&](int, float l) {
         const bool in = l >= low_l && (l == largest || sc.flat || (!sc.peak && distance(sc, l) <= z_max + 0.5f));
         const unsigned m = __ballot_sync(0xffffffffu, in);
+        if (m == 0) return;
         if (in) packed[held + __popc(m & ((1u << lane) - 1))] = __float_as_uint(l);
         held += __popc(m);
         __syncwarp();
@@ -575,14 +580,15 @@ __global__ void __launch_bounds__(THREADS) sample_rows_kernel(const SampleArgs a
             if (lane < held) packed[lane] = next;
             __syncwarp();
         }
-    }
+    });
     if (lane < held) own += kept(__uint_as_float(packed[lane]));
     for (int o = 16; o > 0; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
     __syncthreads();
     if (lane == 0) sh.red_w[warp] = own;
     __syncthreads();
-    uint64_t here = 0;
-    for (int w = 0; w < THREADS / 32; ++w) here += sh.red_w[w];
+    uint64_t here = lane < THREADS / 32 ? sh.red_w[lane] : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) here += __shfl_xor_sync(0xffffffffu, here, o);
     if (tid == 0) sh.sum = here;
     row_barrier(cl);
     uint64_t all = here, before = 0;
@@ -599,7 +605,7 @@ __global__ void __launch_bounds__(THREADS) sample_rows_kernel(const SampleArgs a
         }
         row_barrier(cl);  // no block leaves while another reads its shared memory
     }
-    const uint64_t need = asked([&] { return needed(u, all, greedy); });
+    const uint64_t need = greedy ? 0 : needed(u, all);
     if (here == 0 || need < before || need >= before + here) return;  // another block's
     int part = 0;  // the warp in whose part it falls: its elements are dealt to the whole block
     while (part < THREADS / 32 - 1 && before + sh.red_w[part] <= need) before += sh.red_w[part++];
