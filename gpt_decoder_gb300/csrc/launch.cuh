@@ -34,6 +34,19 @@ gk_status launch_dependent(gk_ctx* ctx, const char* what, void (*kernel)(KArgs..
 }
 __device__ __forceinline__ void wait_for_earlier_kernels() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// (a & b) | c in one instruction. Only one operand of it can be a constant in the code: kernels that unpack
+// codes take their masks as arguments (CodeMasks), which stay in registers.
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+struct CodeMasks {
+    uint32_t bf16_128 = 0x43004300u;  // 128 as a pair of bf16: seven low bits added to it are exact
+    uint32_t low7 = 0x007f007fu, sign = 0x00800080u;   // 8-bit codes
+    uint32_t low4 = 0x000f000fu, bf16_136 = 0x43084308u;  // 4-bit codes
+};
+
 // Every thread of every block of the cluster arrives, then waits (release / acquire).
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");

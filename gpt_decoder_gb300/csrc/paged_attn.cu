@@ -59,8 +59,8 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&t);
 }
 // The codes in bytes 0 and 2 of x as a pair of bf16.
-__device__ __forceinline__ uint32_t codes02(uint32_t x) {
-    const uint32_t a = (x & 0x007f007fu) | 0x43004300u, b = (x & 0x00800080u) | 0x43004300u;
+__device__ __forceinline__ uint32_t codes02(const CodeMasks& k, uint32_t x) {
+    const uint32_t a = and_or(x, k.low7, k.bf16_128), b = and_or(x, k.sign, k.bf16_128);
     const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
     return *reinterpret_cast<const uint32_t*>(&d);
 }
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) 
             if (Q8) {
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
-                    const uint32_t a0 = codes02(x[0][w]), a1 = codes02(x[1][w]), a2 = codes02(x[0][w] >> 8), a3 = codes02(x[1][w] >> 8);
+                    const uint32_t a0 = codes02(a.masks, x[0][w]), a1 = codes02(a.masks, x[1][w]), a2 = codes02(a.masks, x[0][w] >> 8), a3 = codes02(a.masks, x[1][w] >> 8);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) mma(s[nt], a0, a1, a2, a3, q[nt][8 * c + 2 * w], q[nt][8 * c + 2 * w + 1]);
                 }
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) 
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const uint32_t y = half ? y1 : y0, z = half ? z1 : z0;
-                        const uint32_t a0 = codes02(y), a1 = codes02(y >> 8), a2 = codes02(z), a3 = codes02(z >> 8);
+                        const uint32_t a0 = codes02(a.masks, y), a1 = codes02(a.masks, y >> 8), a2 = codes02(a.masks, z), a3 = codes02(a.masks, z >> 8);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             mma(o[nt][2 * w + half], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);

@@ -26,6 +26,7 @@ struct AttnArgs {
     __nv_bfloat16* expanded_v;
     int64_t expanded_rows;
     int* err;
+    CodeMasks masks;
     __host__ __device__ int split_keys(int kv) const {
         const int even = (kv + splits - 1) / splits;
         return max(min_split, (even + 127) & ~127);

@@ -52,9 +52,9 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&t);
 }
 // Codes 0 and 1 (or 2 and 3) of a word as a pair of bf16: 128 + the low seven bits, less 128 or 256.
-__device__ __forceinline__ uint32_t codes_pair(uint32_t w, int second) {
+__device__ __forceinline__ uint32_t codes_pair(const CodeMasks& k, uint32_t w, int second) {
     const uint32_t x = __byte_perm(w, 0, second ? 0x4342 : 0x4140);
-    const uint32_t a = (x & 0x007f007fu) | 0x43004300u, b = (x & 0x00800080u) | 0x43004300u;
+    const uint32_t a = and_or(x, k.low7, k.bf16_128), b = and_or(x, k.sign, k.bf16_128);
     const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
     return *reinterpret_cast<const uint32_t*>(&d);
 }
@@ -444,8 +444,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const uint4 now = x[i & 3];
                     if (i + 4 < PASSES) x[i & 3] = load(i + 4);
                     const int r = i * RPP + r_in;
-                    const uint4 lo = make_uint4(codes_pair(now.x, 0), codes_pair(now.x, 1), codes_pair(now.y, 0), codes_pair(now.y, 1));
-                    const uint4 hi = make_uint4(codes_pair(now.z, 0), codes_pair(now.z, 1), codes_pair(now.w, 0), codes_pair(now.w, 1));
+                    const uint4 lo = make_uint4(codes_pair(a.masks, now.x, 0), codes_pair(a.masks, now.x, 1), codes_pair(a.masks, now.y, 0), codes_pair(a.masks, now.y, 1));
+                    const uint4 hi = make_uint4(codes_pair(a.masks, now.z, 0), codes_pair(a.masks, now.z, 1), codes_pair(a.masks, now.w, 0), codes_pair(a.masks, now.w, 1));
                     // the two halves' threads store even and odd chunks in turn: no bank conflicts
                     *reinterpret_cast<uint4*>(tile + half * HALF + swizzled(r, 2 * (c & 3) + half)) = half ? hi : lo;
                     *reinterpret_cast<uint4*>(tile + half * HALF + swizzled(r, 2 * (c & 3) + (half ^ 1))) = half ? lo : hi;
@@ -679,8 +679,8 @@ __global__ void __launch_bounds__(256) expand_kernel(const AttnArgs a, __nv_bflo
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             uint4* dst = reinterpret_cast<uint4*>((e ? v_out : k_out) + out);
-            dst[0] = make_uint4(codes_pair(x[e].x, 0), codes_pair(x[e].x, 1), codes_pair(x[e].y, 0), codes_pair(x[e].y, 1));
-            dst[1] = make_uint4(codes_pair(x[e].z, 0), codes_pair(x[e].z, 1), codes_pair(x[e].w, 0), codes_pair(x[e].w, 1));
+            dst[0] = make_uint4(codes_pair(a.masks, x[e].x, 0), codes_pair(a.masks, x[e].x, 1), codes_pair(a.masks, x[e].y, 0), codes_pair(a.masks, x[e].y, 1));
+            dst[1] = make_uint4(codes_pair(a.masks, x[e].z, 0), codes_pair(a.masks, x[e].z, 1), codes_pair(a.masks, x[e].w, 0), codes_pair(a.masks, x[e].w, 1));
         }
     }
 }

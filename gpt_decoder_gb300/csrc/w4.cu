@@ -3,6 +3,8 @@
 // into our classes" (a Linear's weight is [in, out]; here each output's K codes lie together).
 #include <math.h>
 
+#include <algorithm>
+
 #include "launch.cuh"
 
 namespace gk {
@@ -37,18 +39,20 @@ __global__ void quant_w4_kernel(const float* __restrict__ W, int64_t ldw, int tr
     scales[m * G + g] = sb;
 }
 
-// Y = X W^T for a few rows, bound by the weights' bytes: every code is read once, straight into the
-// registers that the matrix instruction takes (mma.sync m16n8k16: 16 outputs by 8 rows of X; with
-// tcgen05's tiles of 128 rows most of the product would be of nothing, and the codes would have
-// to be unpacked into shared memory first).
-//   A warp takes MT tiles of 16 outputs and, of each, U groups of K at a time: a lane loads
-// group / 32 words (8 codes each) of outputs g and g + 8 at once, so four lanes cover a group's
-// codes of a row; the next U groups are in flight while U are multiplied. A word's codes become bf16 pairs by masks:
-// (w >> 4 i) & 0x000f000f | 0x43004300 is 128 + code, exactly, and 136 taken off leaves code - 8. The pairs
-// are codes (i, i + 4); X's elements are paired the same way by byte permutes, once for all MT tiles.
+// Y = X W^T for a few rows, bound by the weights' bytes: every code is read once and multiplied on
+// mma.sync m16n8k16 (16 outputs by 8 rows of X; with tcgen05's tiles of 128 rows most of the product
+// would be of nothing).
+//   A warp takes MT tiles of 16 outputs and of K every 8th piece of 256 (128 bytes of a row): whole lines
+// by cp.async into a ring of its own in shared memory, SLOTS - 1 pieces ahead, running on from one tile of
+// outputs to the block's next, so that a warp waits for nobody but the memory. The ring's
+// 16-byte chunks are swizzled by the row, so that the words of 8 rows come from 32 different banks.
+//   A word's codes become bf16 pairs by masks: (w >> 4 i) & 0x000f000f | 0x43004300 is 128 + code, exactly,
+// and 136 taken off leaves code - 8. The pairs are codes (i, i + 4); X's elements are paired the same
+// way by byte permutes, once for all MT tiles. The four lanes of a row hold neighbouring words, so X is
+// read 64 bytes a row at a time (from L1).
 //   The products of a group are summed by the matrix instruction and then scaled in float32. The 8
-// warps of a block share the K groups, the blocks of a cluster share them again when there are few
-// outputs; sums are joined in shared memory in a fixed order.
+// warps of a block share K, the blocks of a cluster share it again when there are few outputs; sums
+// are joined in shared memory in a fixed order.
 constexpr int W4_WARPS = 8;
 
 struct W4Args {
@@ -60,6 +64,7 @@ struct W4Args {
     void* y;
     int64_t ldx, ldr, ldy;
     int N, K, M, y_f32, slices;  // slices: blocks (one cluster) that share a tile's K
+    CodeMasks masks;
 };
 
 __device__ __forceinline__ void w4_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -69,170 +74,201 @@ __device__ __forceinline__ void w4_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // Codes i and i + 4 of a word, as bf16 (code - 8).
-__device__ __forceinline__ uint32_t w4_pair(uint32_t w, int i) {
-    const uint32_t a = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u, b = 0x43084308u;
-    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+__device__ __forceinline__ uint32_t w4_pair(const CodeMasks& k, uint32_t w, int i) {
+    const uint32_t a = and_or(w >> (4 * i), k.low4, k.bf16_128);
+    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&k.bf16_136));
     return *reinterpret_cast<const uint32_t*>(&d);
 }
 
-template <int LW>
-struct Words {
-    uint32_t w[LW];
-};
-template <int LW>
-__device__ __forceinline__ Words<LW> load_words(const uint8_t* p) {
-    Words<LW> r;
-    if constexpr (LW == 4) {
-        const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
-        r.w[0] = u.x, r.w[1] = u.y, r.w[2] = u.z, r.w[3] = u.w;
-    } else if constexpr (LW == 2) {
-        const uint2 u = __ldcs(reinterpret_cast<const uint2*>(p));
-        r.w[0] = u.x, r.w[1] = u.y;
-    } else {
-        r.w[0] = __ldcs(reinterpret_cast<const uint32_t*>(p));
-    }
-    return r;
-}
+constexpr int PIECE = 256;  // codes of a row that a warp takes at a time
 
-// LW: words of a group per lane (group / 32). NT: tiles of 8 rows. MT: tiles of 16 outputs per warp.
+template <int NT, int MT>
+struct W4Shared {
+    static constexpr int SLOTS = NT == 4 ? 4 : 3;
+    static constexpr int SLOT = MT * 16 * (PIECE / 2), RING = W4_WARPS * SLOTS * SLOT;
+    static constexpr int ROW = MT * 16 + 1;
+    static constexpr int BYTES = RING + W4_WARPS * NT * 8 * ROW * 4;
+};
+
+// LW: words (8 codes) of a group per lane: group / 32. NT: tiles of 8 rows. MT: tiles of 16 outputs per warp.
 template <int LW, int NT, int MT>
-__global__ void __launch_bounds__(W4_WARPS * 32, NT * MT == 8 ? 1 : 2) matvec_w4_kernel(const W4Args a) {
-    constexpr int G = 32 * LW, U = LW == 4 ? 2 : LW == 2 ? 4 : 8;
-    __shared__ float part[W4_WARPS][NT * 8][MT * 16 + 1];
+__global__ void __launch_bounds__(W4_WARPS * 32, NT == 4 ? 1 : 2) matvec_w4_kernel(const W4Args a) {
+    using S = W4Shared<NT, MT>;
+    constexpr int GPP = 8 / LW;  // groups of a piece
+    extern __shared__ __align__(128) uint8_t w4_smem[];
+    float(*part)[NT * 8][S::ROW] = reinterpret_cast<float(*)[NT * 8][S::ROW]>(w4_smem + S::RING);
     wait_for_earlier_kernels();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int tile = blockIdx.x / a.slices, slice = blockIdx.x - tile * a.slices;
-    const int m0 = tile * MT * 16, groups = a.K / G;
-    const uint8_t* wp[MT][2];
-    const __nv_bfloat16* sp[MT][2];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {  // outputs past M read the last one's weights and are not stored
-            const int64_t m = min(m0 + mt * 16 + h * 8 + g, a.M - 1);
-            wp[mt][h] = a.w + m * (a.K / 2) + t * 4 * LW;
-            sp[mt][h] = a.scales + m * groups;
-        }
+    const int slice = blockIdx.x % a.slices, groups = a.K / (32 * LW), row_bytes = a.K / 2;
+    const int tiles = (a.M + MT * 16 - 1) / (MT * 16), hop = gridDim.x / a.slices;
+    const int pieces = (a.K + PIECE - 1) / PIECE, stride = a.slices * W4_WARPS, first = slice * W4_WARPS + warp;
+    uint8_t* ring = w4_smem + warp * S::SLOTS * S::SLOT;
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
     const __nv_bfloat16* xp[NT];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) xp[nt] = a.x + (int64_t)min(nt * 8 + g, a.N - 1) * a.ldx + t * 8 * LW;
-    float sum[MT][NT][4] = {};
-    struct Step {
-        Words<LW> w[U][MT][2];
-        float s[U][MT][2];
-    };
-    auto load = [&](Step& to, int g0) {  // groups past the last read the last one's, and are not used
+    for (int nt = 0; nt < NT; ++nt) xp[nt] = a.x + (int64_t)min(nt * 8 + g, a.N - 1) * a.ldx + t * 8;
+
+    // send for piece p of a tile's rows; outputs past M read the last one's, bytes past a row's end are zeros
+    auto send = [&](int slot, int tile, int p) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int gi = min(g0 + u, groups - 1);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) to.w[u][mt][h] = load_words<LW>(wp[mt][h] + (int64_t)gi * (G / 2));
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int gi = min(g0 + u, groups - 1);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) to.s[u][mt][h] = __bfloat162float(sp[mt][h][gi]);
+        for (int i = 0; i < MT * 4; ++i) {
+            const int r = i * 4 + (lane >> 3), c = lane & 7, at = p * (PIECE / 2) + c * 16;
+            const uint8_t* src = a.w + (int64_t)min(tile * MT * 16 + r, a.M - 1) * row_bytes + (at < row_bytes ? at : 0);
+            asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(
+                             ring_at + slot * S::SLOT + r * 128 + ((c ^ (r & 7)) << 4)),
+                         "l"(src), "r"(at < row_bytes ? 16 : 0)
+                         : "memory");
         }
     };
-    auto multiply = [&](const Step& now, int g0, int u) {
-        float acc[MT][NT][4] = {};
+    // the piece's scales, read one piece ahead
+    struct Scales {
+        __nv_bfloat16 s[MT][2][GPP];
+    };
+    const bool vector = groups % GPP == 0 && (reinterpret_cast<uintptr_t>(a.scales) & (2 * GPP - 1)) == 0;
+    auto load_scales = [&](Scales& to, int tile, int p) {
 #pragma unroll
-        for (int j = 0; j < LW; ++j) {
-            uint32_t b[NT][4];
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(xp[nt] + (g0 + u) * G + j * 8));
-                b[nt][0] = __byte_perm(v.x, v.z, 0x5410), b[nt][1] = __byte_perm(v.x, v.z, 0x7632);
-                b[nt][2] = __byte_perm(v.y, v.w, 0x5410), b[nt][3] = __byte_perm(v.y, v.w, 0x7632);
-            }
+            for (int h = 0; h < 2; ++h) {
+                const __nv_bfloat16* sp = a.scales + (int64_t)min(tile * MT * 16 + mt * 16 + h * 8 + g, a.M - 1) * groups + p * GPP;
+                if (vector) {
+                    if constexpr (GPP == 2) *reinterpret_cast<uint32_t*>(to.s[mt][h]) = __ldg(reinterpret_cast<const uint32_t*>(sp));
+                    else if constexpr (GPP == 4) *reinterpret_cast<uint2*>(to.s[mt][h]) = __ldg(reinterpret_cast<const uint2*>(sp));
+                    else *reinterpret_cast<uint4*>(to.s[mt][h]) = __ldg(reinterpret_cast<const uint4*>(sp));
+                } else {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                const uint32_t w0 = now.w[u][mt][0].w[j], w1 = now.w[u][mt][1].w[j];
-#pragma unroll
-                for (int i = 0; i < 4; i += 2) {
-                    const uint32_t a0 = w4_pair(w0, i), a1 = w4_pair(w1, i), a2 = w4_pair(w0, i + 1), a3 = w4_pair(w1, i + 1);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) w4_mma(acc[mt][nt], a0, a1, a2, a3, b[nt][i], b[nt][i + 1]);
+                    for (int u = 0; u < GPP; ++u) to.s[mt][h][u] = sp[min(u, groups - 1 - p * GPP)];
                 }
             }
+    };
+    // the next piece of this warp's walk over (tile, piece)
+    auto step_on = [&](int& tile, int& p) {
+        p += stride;
+        if (p >= pieces) p = first, tile += hop;
+    };
+    int tile = blockIdx.x / a.slices, sent_tile = tile, sent_p = first;  // sent: the next piece to send for
+    const bool works = first < pieces;
+    int slot = 0, sent_slot = 0;
+#pragma unroll
+    for (int i = 0; i < S::SLOTS - 1; ++i) {
+        if (works && sent_tile < tiles) {
+            send(sent_slot, sent_tile, sent_p);
+            step_on(sent_tile, sent_p);
         }
+        sent_slot = sent_slot + 1 == S::SLOTS ? 0 : sent_slot + 1;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    Scales sc;
+    if (works && tile < tiles) load_scales(sc, tile, first);
+    for (; tile < tiles; tile += hop) {
+        float sum[MT][NT][4] = {};
+        for (int p = first; p < pieces; p += stride) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(S::SLOTS - 2) : "memory");
+            __syncwarp();  // every lane's part of the piece is there, and the slot sent for next has been read
+            if (sent_tile < tiles) {
+                send(sent_slot, sent_tile, sent_p);
+                step_on(sent_tile, sent_p);
+            }
+            sent_slot = sent_slot + 1 == S::SLOTS ? 0 : sent_slot + 1;
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            const Scales now = sc;
+            {
+                int tn = tile, pn = p;
+                step_on(tn, pn);
+                if (tn < tiles) load_scales(sc, tn, pn);
+            }
+            const uint8_t* rows = ring + slot * S::SLOT + t * 4;
+            slot = slot + 1 == S::SLOTS ? 0 : slot + 1;
+#pragma unroll
+            for (int u = 0; u < GPP; ++u) {
+                if (p * GPP + u >= groups) break;
+                float acc[MT][NT][4] = {};
+#pragma unroll
+                for (int j = 0; j < LW; ++j) {
+                    const int q = u * LW + j;
+                    uint32_t b[NT][4];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const uint4 v = __ldg(reinterpret_cast<const uint4*>(xp[nt] + p * PIECE + q * 32));
+                        b[nt][0] = __byte_perm(v.x, v.z, 0x5410), b[nt][1] = __byte_perm(v.x, v.z, 0x7632);
+                        b[nt][2] = __byte_perm(v.y, v.w, 0x5410), b[nt][3] = __byte_perm(v.y, v.w, 0x7632);
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        const uint32_t w0 = *reinterpret_cast<const uint32_t*>(rows + (mt * 16 + g) * 128 + ((q ^ g) << 4));
+                        const uint32_t w1 = *reinterpret_cast<const uint32_t*>(rows + (mt * 16 + 8 + g) * 128 + ((q ^ g) << 4));
+#pragma unroll
+                        for (int i = 0; i < 4; i += 2) {
+                            const uint32_t a0 = w4_pair(a.masks, w0, i), a1 = w4_pair(a.masks, w1, i), a2 = w4_pair(a.masks, w0, i + 1), a3 = w4_pair(a.masks, w1, i + 1);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) w4_mma(acc[mt][nt], a0, a1, a2, a3, b[nt][i], b[nt][i + 1]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sum[mt][nt][e] = fmaf(acc[mt][nt][e], __bfloat162float(now.s[mt][e >> 1][u]), sum[mt][nt][e]);
+            }
+        }
+        __syncthreads();  // the tile before has been written
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sum[mt][nt][e] = fmaf(acc[mt][nt][e], now.s[u][mt][e >> 1], sum[mt][nt][e]);
-    };
-    // the next step's codes are on their way while this step is multiplied
-    const int stride = a.slices * W4_WARPS * U;
-    int g0 = (slice * W4_WARPS + warp) * U;
-    Step step[2];
-    auto turn = [&](const Step& now, Step& next) {
-        if (g0 + stride < groups) load(next, g0 + stride);
-        if (g0 + U <= groups) {
+                for (int e = 0; e < 4; ++e) part[warp][nt * 8 + 2 * t + (e & 1)][mt * 16 + g + (e >> 1) * 8] = sum[mt][nt][e];
+        __syncthreads();
+        constexpr int OUT = NT * 8 * MT * 16;
+        const int m0 = tile * MT * 16;
+        if (a.slices > 1) {  // this block's sum, for the cluster
+            for (int i = threadIdx.x; i < OUT; i += W4_WARPS * 32) {
+                const int n = i / (MT * 16), m = i - n * (MT * 16);
+                float v = 0.f;
 #pragma unroll
-            for (int u = 0; u < U; ++u) multiply(now, g0, u);
-        } else {
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (g0 + u < groups) multiply(now, g0, u);
+                for (int w = 0; w < W4_WARPS; ++w) v += part[w][n][m];
+                part[0][n][m] = v;
+            }
+            __syncwarp();
+            cluster_barrier();
         }
-        g0 += stride;
-    };
-    if (g0 < groups) load(step[0], g0);
-    while (g0 < groups) {
-        turn(step[0], step[1]);
-        if (g0 < groups) turn(step[1], step[0]);
-    }
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) part[warp][nt * 8 + 2 * t + (e & 1)][mt * 16 + g + (e >> 1) * 8] = sum[mt][nt][e];
-    __syncthreads();
-    constexpr int OUT = NT * 8 * MT * 16;
-    if (a.slices > 1) {  // this block's sum, for the cluster
-        for (int i = threadIdx.x; i < OUT; i += W4_WARPS * 32) {
+        for (int i = slice * (W4_WARPS * 32) + threadIdx.x; i < min(OUT, a.N * MT * 16); i += a.slices * W4_WARPS * 32) {
             const int n = i / (MT * 16), m = i - n * (MT * 16);
             float v = 0.f;
+            if (a.slices > 1) {
+                for (int r = 0; r < a.slices; ++r) v += load_cluster(&part[0][n][m], r);
+            } else {
 #pragma unroll
-            for (int w = 0; w < W4_WARPS; ++w) v += part[w][n][m];
-            part[0][n][m] = v;
+                for (int w = 0; w < W4_WARPS; ++w) v += part[w][n][m];
+            }
+            if (m0 + m >= a.M) continue;
+            if (a.bias) v += a.bias[m0 + m];
+            if (a.residual) v += a.residual[n * a.ldr + m0 + m];
+            if (a.y_f32) static_cast<float*>(a.y)[n * a.ldy + m0 + m] = v;
+            else static_cast<__nv_bfloat16*>(a.y)[n * a.ldy + m0 + m] = __float2bfloat16_rn(v);
         }
-        cluster_barrier();
-    }
-    for (int i = slice * (W4_WARPS * 32) + threadIdx.x; i < OUT; i += a.slices * W4_WARPS * 32) {
-        const int n = i / (MT * 16), m = i - n * (MT * 16);
-        float v = 0.f;
-        if (a.slices > 1) {
-            for (int r = 0; r < a.slices; ++r) v += load_cluster(&part[0][n][m], r);
-        } else {
-#pragma unroll
-            for (int w = 0; w < W4_WARPS; ++w) v += part[w][n][m];
+        if (a.slices > 1) {  // no block goes on while another reads its sums
+            __syncwarp();
+            cluster_barrier();
         }
-        if (n >= a.N || m0 + m >= a.M) continue;
-        if (a.bias) v += a.bias[m0 + m];
-        if (a.residual) v += a.residual[n * a.ldr + m0 + m];
-        if (a.y_f32) static_cast<float*>(a.y)[n * a.ldy + m0 + m] = v;
-        else static_cast<__nv_bfloat16*>(a.y)[n * a.ldy + m0 + m] = __float2bfloat16_rn(v);
     }
-    if (a.slices > 1) cluster_barrier();  // no block leaves while another reads its sums
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 template <int LW, int NT, int MT>
 gk_status run_w4(gk_ctx* ctx, W4Args& a) {
-    const int64_t tiles = cdiv(a.M, MT * 16);
-    const int groups = a.K / (32 * LW), turns = (int)cdiv(groups, W4_WARPS * (LW == 4 ? 2 : LW == 2 ? 4 : 8));
+    constexpr int BYTES = W4Shared<NT, MT>::BYTES;
+    if (cudaFuncSetAttribute(matvec_w4_kernel<LW, NT, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES) != cudaSuccess) {
+        cudaGetLastError();
+        return fail(ctx, GK_ERR_CUDA, "gk_matvec_w4: shared memory");
+    }
+    const int64_t tiles = cdiv(a.M, MT * 16), turns = cdiv(a.K, PIECE * W4_WARPS), wave = (NT == 4 ? 1 : 2) * ctx->num_sms;
     a.slices = 1;  // a cluster shares K while that adds blocks that have work and fit the GPU once
-    while (a.slices < 8 && tiles * a.slices * 2 <= 2 * ctx->num_sms && a.slices * 2 <= turns) a.slices *= 2;
-    return launch_dependent(ctx, "matvec_w4", matvec_w4_kernel<LW, NT, MT>, dim3((unsigned)(tiles * a.slices)),
-                            dim3(W4_WARPS * 32), 0, a.slices, a);
+    while (a.slices < 8 && tiles * a.slices * 2 <= wave && a.slices * 2 <= turns) a.slices *= 2;
+    return launch_dependent(ctx, "matvec_w4", matvec_w4_kernel<LW, NT, MT>, dim3((unsigned)(std::min(tiles, wave) * a.slices)),
+                            dim3(W4_WARPS * 32), BYTES, a.slices, a);
 }
 
 // Two tiles of outputs per warp halve the reads of X (from L1) once there are enough tiles for
@@ -295,7 +331,7 @@ gk_status gk_matvec_w4(gk_ctx* ctx, int dtype, const void* X, int64_t ldx, const
     GK_REQUIRE(ctx, aligned16(X) && ldx % 8 == 0, GK_ERR_ALIGN, "gk_matvec_w4: X must be 16-byte aligned, ldx a multiple of 8");
     if (N == 0) return GK_OK;
     W4Args a{static_cast<const __nv_bfloat16*>(X), Wq, reinterpret_cast<const __nv_bfloat16*>(scales), bias, residual, Y,
-             ldx, ldr, ldy, (int)N, (int)K, (int)M, y_dtype == GK_F32, 1};
+             ldx, ldr, ldy, (int)N, (int)K, (int)M, y_dtype == GK_F32, 1, {}};
     return group == 128 ? run_w4_rows<4>(ctx, a) : group == 64 ? run_w4_rows<2>(ctx, a) : run_w4_rows<1>(ctx, a);
 }
 
