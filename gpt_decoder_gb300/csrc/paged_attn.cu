@@ -545,7 +545,7 @@ extern "C" gk_status gk_paged_attn(gk_ctx* ctx, const gk_paged_kv* cache, int dt
         splits = cdiv(16 * (int64_t)ctx->num_sms, units);
     } else {
         a.min_split = 512;
-        splits = cdiv(3 * (int64_t)ctx->num_sms, units);
+        splits = cdiv((int64_t)ctx->num_sms, units);  // one wave: more blocks cost more to join than they even out
     }
     splits = std::min<int64_t>(splits, cdiv(a.p.capacity, a.min_split));
     splits = std::min<int64_t>(splits, std::min<int64_t>(256, (int64_t)(room / per)));

@@ -10,6 +10,8 @@
 //               memory; the reference m moves (and O is rescaled there) only when the row's maximum
 //               passes it by more than 8;
 //   O += P V    (N = head size, K = 128 keys), accumulated in tensor memory.
+// Head sizes up to 64 leave room there for P beside S: the next S is computed as soon as the scores of
+// this one have been read, under the softmax. With 128 P lies over S, and the next S waits for P V.
 // The two tiles take turns: while one group of four warps turns its S into P, the tensor core
 // computes the other's products. Warp 8 sends for the keys by TMA, a box per page (pages lie anywhere).
 // 8-bit codes become bf16 (exactly) first: in one pass into the workspace, if it has room and enough
@@ -126,6 +128,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     attn_tiles_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
     constexpr bool Q8 = FROM != PAGES16;
     using L = Layout<HSP>;
+    constexpr bool EARLY = HSP == 64;  // the next S before P V
+    constexpr uint32_t P_AT = EARLY ? 384 : 0, P_STEP = EARLY ? 64 : 128;  // tensor memory columns of P_g
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sQ = smem;           // [2 tiles][halves]
@@ -147,14 +151,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     volatile uint32_t* s_bad = reinterpret_cast<volatile uint32_t*>(bars + 25);  // [4] 16-key groups on refused pages
     volatile int* s_odd = reinterpret_cast<volatile int*>(bars + 27);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 28);
+    uint64_t* s_free = bars + 29;    // [2] early S: S_g has been read (one arrival per warp)
+    uint64_t* bar_pv = bars + 31;    // [2] early S: P_g V is complete
     wait_for_earlier_kernels();
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     Item it;
     {
         const int pairs = gridDim.x / a.splits;
-        const int pair = pairs - 1 - blockIdx.x / a.splits;  // the last rows see the most keys: first
-        it.split = blockIdx.x % a.splits;
+        // the last rows see the most keys: first; and pairs that read the same keys next to each other
+        const int pair = pairs - 1 - blockIdx.x % pairs;
+        it.split = blockIdx.x / pairs;
         it.b = blockIdx.z;
         it.hk = blockIdx.y;
         it.s0 = a.q_start[it.b];
@@ -191,6 +198,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(&bar_s[i], 1);
             mbar_init(&bar_p[i], 4);
             mbar_init(&bar_o[i], 1);
+            mbar_init(&s_free[i], 4);
+            mbar_init(&bar_pv[i], 1);
         }
         for (int i = 0; i < 3; ++i) {
             mbar_init(&k_full[i], 1);
@@ -248,6 +257,21 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int j = 0; ok && j < n_kv; ++j) {
                 const uint32_t sn = stage + 1 == L::STAGES ? 0 : stage + 1, pn = sn ? phase : phase ^ 1;
                 bool have_v = false, have_k = false;
+                if constexpr (EARLY) {
+                    for (int g = 0; g < 2 && ok; ++g) {
+                        if (j + 1 >= it.tiles(g)) continue;
+                        ok = __all_sync(0xffffffffu, wait_phase(&s_free[g], j & 1, WAIT_NS) && (have_k || wait_phase(&k_full[sn], pn, WAIT_NS)));
+                        if (!ok) break;
+                        have_k = true;
+                        tc_fence_after();
+                        scores(g, sn);
+                    }
+                    if (!ok) break;
+                    if (j + 1 < n_kv) {
+                        if (elect_one()) umma_commit(&k_empty[sn]);
+                        __syncwarp();
+                    }
+                }
                 for (int g = 0; g < 2 && ok; ++g) {
                     if (j >= it.tiles(g)) continue;
                     ok = __all_sync(0xffffffffu, wait_phase(&bar_p[g], j & 1, WAIT_NS));
@@ -258,12 +282,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < KT / 16; ++kk)
-                            umma_bf16_ts(tmem + 256 + g * HSP, tmem + g * 128 + kk * 8, desc_add(v_d, stage * L::TILE + kk * 2048),
+                            umma_bf16_ts(tmem + 256 + g * HSP, tmem + P_AT + g * P_STEP + kk * 8, desc_add(v_d, stage * L::TILE + kk * 2048),
                                          id_o, (j > 0 || kk > 0) ? 1u : 0u);
+                        if (EARLY) umma_commit(&bar_pv[g]);
                         if (j == it.tiles(g) - 1) umma_commit(&bar_o[g]);
                     }
                     __syncwarp();
-                    if (j + 1 < it.tiles(g)) {
+                    if (!EARLY && j + 1 < it.tiles(g)) {
                         if (!have_k) ok = __all_sync(0xffffffffu, wait_phase(&k_full[sn], pn, WAIT_NS));
                         if (!ok) break;
                         have_k = true;
@@ -274,7 +299,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!ok) break;
                 if (elect_one()) {  // these tiles are free once the products issued so far are complete
                     umma_commit(&v_empty[stage]);
-                    if (j + 1 < n_kv) umma_commit(&k_empty[sn]);
+                    if (!EARLY && j + 1 < n_kv) umma_commit(&k_empty[sn]);
                 }
                 __syncwarp();
                 stage = sn;
@@ -423,7 +448,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (; j < n_kv; j += 2) {
                 const uint32_t stage = j % L::STAGES, phase = (j / L::STAGES) & 1;
                 const unsigned refused = __ballot_sync(0xffffffffu, lane < 8 && bad);
-                ok = __all_sync(0xffffffffu, wait_phase(&empty[stage], phase ^ 1, WAIT_NS));
+                // (K too waits for the V tile that far back: its scales' places have been read then)
+                ok = __all_sync(0xffffffffu, wait_phase(&empty[stage], phase ^ 1, WAIT_NS) && (is_v || wait_phase(&v_empty[stage], phase ^ 1, WAIT_NS)));
                 if (!ok) break;
                 uint8_t* tile = (is_v ? sV : sK) + stage * L::TILE;
                 if (!is_v) leave_scales(j, refused);
@@ -498,6 +524,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             tmem_wait_ld_only();
 #pragma unroll
             for (int c = 0; c < 4; ++c) reg_fence32(sv[c]);
+            if constexpr (EARLY) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_free[g]);
+            }
             const int lim = last - (it.k_begin + j * KT) + 1;  // keys i < lim are seen
             const uint32_t bad = s_bad[j & 3];
             const bool part = __any_sync(0xffffffffu, lim < KT) || (bad & 0xff);
@@ -535,6 +566,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                 l *= corr;
                 m_ref = m_new;
             }
+            if constexpr (EARLY) {  // P and O are free once the products before are complete
+                if (j > 0 && !__all_sync(0xffffffffu, wait_phase(&bar_pv[g], (j - 1) & 1, WAIT_NS))) {
+                    failed = true;
+                    break;
+                }
+                tc_fence_after();
+            }
             const float ref = m_ref == -INFINITY ? 0.f : m_ref;  // (a row that has seen nothing yet)
             uint32_t ps[4] = {0, 0, 0, 0};  // two pairs of running sums
             const float4* vs4 = reinterpret_cast<const float4*>(s_vs + (j & 3) * KT);
@@ -568,7 +606,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         pw[2 * e] = pack2(p[0], p[1]);
                         pw[2 * e + 1] = pack2(p[2], p[3]);
                     }
-                    tmem_st16(lane_addr + g * 128 + c * 16, pw);
+                    tmem_st16(lane_addr + P_AT + g * P_STEP + c * 16, pw);
                 }
             };
             if (Q8 && (bad & ODD_SCALES)) weights(std::true_type{});
