@@ -85,23 +85,36 @@ __device__ __forceinline__ void mul2(uint32_t& x, uint32_t& y, float a, float b)
         : "f"(a), "f"(b));
 }
 
+__device__ __forceinline__ uint32_t test_phase(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(saddr(bar)), "r"(parity)
+        : "memory");
+    return ok;
+}
 // Wait for a phase: polled at first (try_wait suspends the thread, and its wake-up takes longer than most
 // of the waits here), then bounded by the clock.
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint64_t limit) {
-    const uint32_t at = saddr(bar);
+#pragma unroll 1
+    for (int i = 0; i < 4096; ++i)
+        if (test_phase(bar, parity)) return true;
+    return mbar_wait(bar, parity, nullptr, limit);
+}
+// Several at once: even a test of a completed phase takes hundreds of cycles behind the softmax warps' traffic
+// with the tensor memory, so the tests are sent together. (b and c only where asked.)
+__device__ __forceinline__ bool wait_phases(uint64_t* a, uint32_t pa, bool has_b, uint64_t* b, uint32_t pb, bool has_c, uint64_t* c,
+                                            uint32_t pc, uint64_t limit) {
 #pragma unroll 1
     for (int i = 0; i < 4096; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(at), "r"(parity)
-            : "memory");
-        if (ok) return true;
+        const uint32_t x = test_phase(a, pa), y = test_phase(has_b ? b : a, has_b ? pb : pa);
+        const uint32_t z = test_phase(has_c ? c : a, has_c ? pc : pa);
+        if (x & y & z) return true;
     }
-    return mbar_wait(bar, parity, nullptr, limit);
+    return mbar_wait(a, pa, nullptr, limit) && (!has_b || mbar_wait(b, pb, nullptr, limit)) && (!has_c || mbar_wait(c, pc, nullptr, limit));
 }
 
 // Rows that a sequence takes per head once expanded: whole tiles of keys.
@@ -256,28 +269,27 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             for (int j = 0; ok && j < n_kv; ++j) {
                 const uint32_t sn = stage + 1 == L::STAGES ? 0 : stage + 1, pn = sn ? phase : phase ^ 1;
-                bool have_v = false, have_k = false;
+                const bool next_a = j + 1 < it.t0, next_b = j + 1 < it.t1;
                 if constexpr (EARLY) {
-                    for (int g = 0; g < 2 && ok; ++g) {
-                        if (j + 1 >= it.tiles(g)) continue;
-                        ok = __all_sync(0xffffffffu, wait_phase(&s_free[g], j & 1, WAIT_NS) && (have_k || wait_phase(&k_full[sn], pn, WAIT_NS)));
+                    if (next_a || next_b) {
+                        ok = __all_sync(0xffffffffu, wait_phases(&k_full[sn], pn, next_a, &s_free[0], j & 1, next_b, &s_free[1], j & 1,
+                                                                 WAIT_NS));
                         if (!ok) break;
-                        have_k = true;
                         tc_fence_after();
-                        scores(g, sn);
-                    }
-                    if (!ok) break;
-                    if (j + 1 < n_kv) {
+                        if (next_a) scores(0, sn);
+                        if (next_b) scores(1, sn);
                         if (elect_one()) umma_commit(&k_empty[sn]);
                         __syncwarp();
                     }
                 }
+                bool first = true;
                 for (int g = 0; g < 2 && ok; ++g) {
                     if (j >= it.tiles(g)) continue;
-                    ok = __all_sync(0xffffffffu, wait_phase(&bar_p[g], j & 1, WAIT_NS));
-                    if (ok && !have_v) ok = __all_sync(0xffffffffu, wait_phase(&v_full[stage], phase, WAIT_NS));
+                    // the first group's wait takes V, and the next K, with it
+                    ok = __all_sync(0xffffffffu, wait_phases(&bar_p[g], j & 1, first, &v_full[stage], phase,
+                                                             !EARLY && first && j + 1 < n_kv, &k_full[sn], pn, WAIT_NS));
                     if (!ok) break;
-                    have_v = true;
+                    first = false;
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
@@ -288,13 +300,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (j == it.tiles(g) - 1) umma_commit(&bar_o[g]);
                     }
                     __syncwarp();
-                    if (!EARLY && j + 1 < it.tiles(g)) {
-                        if (!have_k) ok = __all_sync(0xffffffffu, wait_phase(&k_full[sn], pn, WAIT_NS));
-                        if (!ok) break;
-                        have_k = true;
-                        tc_fence_after();
-                        scores(g, sn);
-                    }
+                    if (!EARLY && j + 1 < it.tiles(g)) scores(g, sn);
                 }
                 if (!ok) break;
                 if (elect_one()) {  // these tiles are free once the products issued so far are complete
@@ -512,8 +518,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float sl2 = a.scale_log2;
         float m_ref = -INFINITY, l = 0.f;
         for (int j = 0; j < my_kt; ++j) {
-            if (!__all_sync(0xffffffffu, wait_phase(&c_full[j & 3], (j >> 2) & 1, WAIT_NS) &&
-                                             wait_phase(&bar_s[g], j & 1, WAIT_NS))) {
+            if (!__all_sync(0xffffffffu, wait_phases(&bar_s[g], j & 1, true, &c_full[j & 3], (j >> 2) & 1, false, nullptr, 0, WAIT_NS))) {
                 failed = true;
                 break;
             }
