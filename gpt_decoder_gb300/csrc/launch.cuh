@@ -2,9 +2,26 @@
 // stream, alone or in clusters, and the cluster's barrier and shared-memory reads.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace gk {
+
+// Let `Kernel` have up to `bytes` (always the same) of dynamic shared memory on the context's device. The
+// setting lasts, so it is made once a device (it takes the host about as long as a launch).
+template <auto Kernel>
+gk_status allow_shared(gk_ctx* ctx, const char* what, size_t bytes) {
+    static std::atomic<uint64_t> done{0};
+    const uint64_t bit = ctx->device < 64 ? 1ull << ctx->device : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return GK_OK;
+    if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) {
+        cudaGetLastError();
+        return fail(ctx, GK_ERR_CUDA, "%s: shared memory", what);
+    }
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return GK_OK;
+}
 
 // Every thread of `kernel` begins with wait_for_earlier_kernels, so only the launch overlaps the
 // earlier kernel's end. cluster: blocks along x that form one cluster (1: none).

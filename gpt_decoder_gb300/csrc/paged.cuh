@@ -17,7 +17,7 @@ struct Pages {
     const int32_t* kv_len;
     int64_t n_pages, ld_table;
     int Hkv, hs, page_log2;
-    int capacity;  // positions the table has room for: max_pages * page_size (below 2^31)
+    int capacity;  // positions the table has room for: max_pages * page_size (below 2^30)
 };
 
 // Refuse what no kernel could run on; fill `p`.
@@ -39,7 +39,7 @@ inline gk_status check_pages(gk_ctx* ctx, const char* what, const gk_paged_kv* c
                "%s: page size %d (16, 32, 64, 128 or 256)", what, c->page_size);
     GK_REQUIRE(ctx, c->hs >= 16 && c->hs <= 128 && c->hs % 16 == 0, GK_ERR_UNSUPPORTED,
                "%s: head size %d (a multiple of 16 up to 128)", what, c->hs);
-    GK_REQUIRE(ctx, c->Hkv <= 65535 && (int64_t)c->max_pages * c->page_size < (1ll << 30) && 
+    GK_REQUIRE(ctx, c->Hkv <= 65535 && (int64_t)c->max_pages * c->page_size < (1ll << 30) &&
                c->n_pages < (1ll << 31) / c->Hkv / c->page_size,
                GK_ERR_UNSUPPORTED, "%s: cache too large", what);
     GK_REQUIRE(ctx, aligned16(c->k) && aligned16(c->v) && aligned16(c->k_scale) && aligned16(c->v_scale), GK_ERR_ALIGN,

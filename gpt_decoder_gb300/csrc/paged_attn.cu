@@ -507,6 +507,8 @@ extern "C" gk_status gk_paged_attn(gk_ctx* ctx, const gk_paged_kv* cache, int dt
     GK_REQUIRE(ctx, ldq >= (int64_t)H * a.p.hs && ldy >= (int64_t)H * a.p.hs, GK_ERR_ARG, "gk_paged_attn: row stride");
     GK_REQUIRE(ctx, aligned16(q) && aligned16(y) && ldq % 8 == 0 && ldy % 8 == 0, GK_ERR_ALIGN,
                "gk_paged_attn: rows must be 16-byte aligned with strides a multiple of 8");
+    GK_REQUIRE(ctx, std::min<int64_t>(max_q, rows) * (H / a.p.Hkv) < (1ll << 30), GK_ERR_UNSUPPORTED,
+               "gk_paged_attn: %d rows of %d heads a key / value head", max_q, H / a.p.Hkv);
     if (rows == 0) return GK_OK;
     a.q = static_cast<const __nv_bfloat16*>(q);
     a.y = static_cast<__nv_bfloat16*>(y);

@@ -730,11 +730,7 @@ __global__ void __launch_bounds__(256) expand_kernel(const AttnArgs a, __nv_bflo
 
 template <int HSP, int FROM>
 gk_status tiles(gk_ctx* ctx, const AttnArgs& a, const __nv_bfloat16* k, const __nv_bfloat16* v, int64_t rows, int box) {
-    if (cudaFuncSetAttribute(attn_tiles_kernel<HSP, FROM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<HSP>::BYTES) !=
-        cudaSuccess) {
-        cudaGetLastError();
-        return fail(ctx, GK_ERR_CUDA, "gk_paged_attn: shared memory");
-    }
+    GK_TRY((allow_shared<attn_tiles_kernel<HSP, FROM>>(ctx, "gk_paged_attn", Layout<HSP>::BYTES)));
     CUtensorMap mk{}, mv{};
     if (FROM != PAGES8)
         GK_REQUIRE(ctx, make_map(&mk, k, a.p.hs, rows, a.p.hs, box) && make_map(&mv, v, a.p.hs, rows, a.p.hs, box), GK_ERR_CUDA,

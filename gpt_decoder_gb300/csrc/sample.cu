@@ -28,7 +28,7 @@
 namespace gk {
 namespace {
 
-constexpr int THREADS = 512, BINS = 1024, LIST = THREADS, POWERS = 512;
+constexpr int THREADS = 512, BINS = 1024, LIST = THREADS, POWERS = 512, MAX_V = 1 << 18;
 constexpr uint64_t ONE = 1ull << 45;  // the largest weight: up to 2^18 tokens sum below 2^63
 
 // round(2^63 * 2^(-i / 32)) and round(2^63 * 2^(-j / 1024))
@@ -643,7 +643,7 @@ extern "C" gk_status gk_sample_rows(gk_ctx* ctx, int dtype, const void* logits, 
     GK_REQUIRE(ctx, dtype == GK_F32 || dtype == GK_BF16, GK_ERR_ARG, "gk_sample_rows: dtype %d", dtype);
     GK_REQUIRE(ctx, logits && u && next && V >= 1 && ld >= V && rows >= 0 && rows < (1ll << 28), GK_ERR_ARG,
                "gk_sample_rows: bad argument");
-    GK_REQUIRE(ctx, V <= 1 << 18, GK_ERR_UNSUPPORTED, "gk_sample_rows: vocabulary of %d (up to 262144)", V);
+    GK_REQUIRE(ctx, V <= MAX_V, GK_ERR_UNSUPPORTED, "gk_sample_rows: vocabulary of %d (up to 262144)", V);
     GK_REQUIRE(ctx, reinterpret_cast<uintptr_t>(logits) % (dtype == GK_F32 ? 4 : 2) == 0, GK_ERR_ALIGN,
                "gk_sample_rows: misaligned logits");
     if (rows == 0) return GK_OK;
@@ -655,10 +655,9 @@ extern "C" gk_status gk_sample_rows(gk_ctx* ctx, int dtype, const void* logits, 
         a.cluster *= 2;
     while (((int64_t)a.cluster * THREADS << a.run_log2) < V) ++a.run_log2;
     const size_t smem = sizeof(Shared) + ((size_t)THREADS << a.run_log2) * sizeof(float);
-    auto kernel = dtype == GK_F32 ? sample_rows_kernel<float> : sample_rows_kernel<__nv_bfloat16>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
-        cudaGetLastError();
-        return fail(ctx, GK_ERR_CUDA, "gk_sample_rows: shared memory");
-    }
-    return launch_dependent(ctx, "sample_rows", kernel, dim3((unsigned)(rows * a.cluster)), dim3(THREADS), smem, a.cluster, a);
+    constexpr size_t most = sizeof(Shared) + (MAX_V / MAX_CLUSTER) * sizeof(float);
+    const bool f32 = dtype == GK_F32;
+    GK_TRY(f32 ? allow_shared<sample_rows_kernel<float>>(ctx, "gk_sample_rows", most)
+               : allow_shared<sample_rows_kernel<__nv_bfloat16>>(ctx, "gk_sample_rows", most));
+    return launch_dependent(ctx, "sample_rows", f32 ? sample_rows_kernel<float> : sample_rows_kernel<__nv_bfloat16>, dim3((unsigned)(rows * a.cluster)), dim3(THREADS), smem, a.cluster, a);
 }

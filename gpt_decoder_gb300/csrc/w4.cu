@@ -260,10 +260,7 @@ __global__ void __launch_bounds__(W4_WARPS * 32, NT == 4 ? 1 : 2) matvec_w4_kern
 template <int LW, int NT, int MT>
 gk_status run_w4(gk_ctx* ctx, W4Args& a) {
     constexpr int BYTES = W4Shared<NT, MT>::BYTES;
-    if (cudaFuncSetAttribute(matvec_w4_kernel<LW, NT, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES) != cudaSuccess) {
-        cudaGetLastError();
-        return fail(ctx, GK_ERR_CUDA, "gk_matvec_w4: shared memory");
-    }
+    GK_TRY((allow_shared<matvec_w4_kernel<LW, NT, MT>>(ctx, "gk_matvec_w4", BYTES)));
     const int64_t tiles = cdiv(a.M, MT * 16), turns = cdiv(a.K, PIECE * W4_WARPS), wave = (NT == 4 ? 1 : 2) * ctx->num_sms;
     a.slices = 1;  // a cluster shares K while that adds blocks that have work and fit the GPU once
     while (a.slices < 8 && tiles * a.slices * 2 <= wave && a.slices * 2 <= turns) a.slices *= 2;
@@ -293,7 +290,7 @@ gk_status check_w4(gk_ctx* ctx, const char* what, const void* Wq, const void* sc
     GK_REQUIRE(ctx, group == 32 || group == 64 || group == 128, GK_ERR_UNSUPPORTED, "%s: group %d (32, 64 or 128)", what,
                group);
     GK_REQUIRE(ctx, K >= 1 && M >= 1 && K % group == 0, GK_ERR_ARG, "%s: K must be a positive multiple of the group", what);
-    GK_REQUIRE(ctx, K < (1ll << 24) && M < (1ll << 31), GK_ERR_UNSUPPORTED, "%s: sizes too large", what);
+    GK_REQUIRE(ctx, K < (1ll << 24) && M < (1ll << 30), GK_ERR_UNSUPPORTED, "%s: sizes too large", what);
     GK_REQUIRE(ctx, aligned16(Wq) && (reinterpret_cast<uintptr_t>(scales) & 1) == 0, GK_ERR_ALIGN, "%s: misaligned weights",
                what);
     return GK_OK;

@@ -442,6 +442,8 @@ class PagedKv:
                 raise ValueError("PagedKv: page_table and kv_len are int32 with unit stride")
         if page_table.dim() != 2 or kv_len.dim() != 1:
             raise ValueError("PagedKv: page_table is [B, max_pages], kv_len [B]")
+        if len({t.device for t in (k, v, k_scale, v_scale, page_table, kv_len) if t is not None}) != 1:
+            raise ValueError("PagedKv: tensors on different devices")
         self.tensors = (k, v, k_scale, v_scale, page_table, kv_len)
         self.B = min(page_table.shape[0], kv_len.shape[0])
         self.struct = gk_paged_kv(_p(k), _p(v), _p(k_scale), _p(v_scale), _p(page_table), _p(kv_len), n_pages,

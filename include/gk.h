@@ -461,9 +461,12 @@ gk_status gk_paged_read(gk_ctx* ctx, const gk_paged_kv* cache, int dtype, void* 
  *           are left as they were.
  *   scale   positive and finite.
  * A row that sees nothing (a negative position) gets y = 0 and lse = -inf. Keys and values that a
- * row does not see never reach it, whatever they hold (infinities and NaN among it). Long
+ * row does not see never reach it, whatever they hold (infinities and NaN among it). y must not
+ * overlap q, and max_q * H / Hkv stays below 2^30 (GK_ERR_UNSUPPORTED). Long
  * sequences are split over the GPU and joined through the context's workspace: the more of it
- * there is the more they split, and any size will do. */
+ * there is the more they split, and any size will do. (Calls of one context are ordered on its stream;
+ * graphs captured from one context share its workspace, so replay them one after the other, or
+ * capture each from a context of its own.) */
 gk_status gk_paged_attn(gk_ctx* ctx, const gk_paged_kv* cache, int dtype, const void* q, int64_t ldq,
                         void* y, int64_t ldy, float* lse, const int32_t* q_start, int B, int H,
                         int64_t rows, int max_q, float scale);
@@ -472,7 +475,8 @@ gk_status gk_paged_attn(gk_ctx* ctx, const gk_paged_kv* cache, int dtype, const 
 
 /* 4-bit weights of a Linear: Wq uint8 [M, K/2], row m holding output m's K codes two to a byte
  * (even k in the low half), scales bf16 [M, K/group]; code c of group k / group stands for
- * (c - 8) * scale. group is 32, 64 or 128 and divides K. Wq 16-byte aligned, scales 2-byte.
+ * (c - 8) * scale. group is 32, 64 or 128 and divides K; K below 2^24, M below 2^30. Wq 16-byte
+ * aligned, scales 2-byte.
  * gk_quant_w4 makes them from float32 W, [K, M] (transW = 0, the layout of [LM4]'s Linear weights)
  * or [M, K] (transW = 1), row stride ldw: per output and group scale = bf16(max |w| / 7) and
  * code = 8 + rint(w / scale) held to 1 .. 15; a group of zeros gets scale 0 and code 8, and one
@@ -486,7 +490,7 @@ gk_status gk_quant_w4(gk_ctx* ctx, const float* W, int64_t ldw, int transW, uint
  *   bias      float32 [M] or NULL.  residual  float32 [N, M] (stride ldr) or NULL; it may alias Y
  *             when y_dtype is GK_F32 and ldr == ldy.
  *   y_dtype   GK_F32 or GK_BF16 (stride ldy).
- * The codes' products are exact in float32; sums and the scales are float32, and the result is
+ * Y overlaps nothing else that is read. The codes' products are exact in float32; sums and the scales are float32, and the result is
  * rounded once. The sum's order is fixed: the same call gives the same bits. */
 gk_status gk_matvec_w4(gk_ctx* ctx, int dtype, const void* X, int64_t ldx, const uint8_t* Wq,
                        const uint16_t* scales, int group, const float* bias, const float* residual,

@@ -646,3 +646,121 @@ def test_w4_and_sampling_refuse(gkctx):
         refused(status, gk.gk_sample_rows, *sr(**bad))
     gk.gk_sample_rows(*sr(rows=0))
     gk.gk_sync(gkctx)
+
+
+def test_serving_calls_refuse_sizes_past_their_indices(gkctx):
+    from gpt_decoder_gb300 import gk
+
+    t = _t()
+    c = cache(np.random.default_rng(2), [20], 2, 32, 16, False)
+    d, y, qs = Dev(c), t.zeros(4, 128, dtype=t.bfloat16, device="cuda"), dev(starts([4]))
+    refused(gk.GK_ERR_UNSUPPORTED, gk.gk_paged_attn, gkctx, d.h, gk.GK_BF16, y, 128, y, 128, None, qs, 1, 4, 1 << 30, 1 << 30, 1.0)
+    w, s = t.zeros(8, 32, dtype=t.uint8, device="cuda"), t.zeros(8, 2, dtype=t.bfloat16, device="cuda")
+    M = 1 << 30
+    refused(gk.GK_ERR_UNSUPPORTED, gk.gk_matvec_w4, gkctx, gk.GK_BF16, y, 128, w, s, 32, None, None, 0, y, M, gk.GK_F32, 2, 64, M)
+    gk.gk_sync(gkctx)
+
+
+@pytest.mark.parametrize("n", [1, 40, 200])
+def test_attention_of_sequences_that_share_pages(gkctx, n):
+    """A common prefix kept once: two tables name the same pages (nothing is written meanwhile)."""
+    rng = np.random.default_rng(700 + n)
+    for q8 in (False, True):
+        c = cache(rng, [1000, 1000, 700], 2, 64, 32, q8)
+        c.table[1, :20] = c.table[0, :20]
+        c.table[2, :c.table.shape[1]] = c.table[0]
+        q = serving.bf16(rng.standard_normal((3 * n, 4, 64)))
+        ref = serving.paged_attn(c, q, starts([n] * 3), 0.125)
+        check_attention(*attend(gkctx, c, q, [n] * 3, 0.125), ref, (n, q8))
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_cache_offsets_past_32_bits(gkctx, q8):
+    """Pages whose first element lies past 2^32 elements of the cache: write, read back and attention."""
+    from gpt_decoder_gb300 import gk
+
+    t = _t()
+    rng = np.random.default_rng(800)
+    Hkv, hs, page, n_pages = 8, 128, 128, 33000
+    assert (n_pages - 200) * Hkv * hs * page > 1 << 32
+    c = cache(rng, [1500, 333], Hkv, hs, page, q8)
+    d = Dev(c)
+
+    def big(x):  # the last pages are the small cache's
+        if x is None:
+            return None
+        y = t.empty(n_pages, *x.shape[1:], dtype=x.dtype, device="cuda")
+        y[n_pages - c.n_pages:].copy_(x)
+        return y
+
+    k, v, ks, vs = (big(x) for x in (d.k, d.v, d.ks, d.vs))
+    h = gk.PagedKv(k, v, ks, vs, d.table + (n_pages - c.n_pages), d.kv_len)
+    w = Hkv * hs
+    for n in (1, 300):
+        q = serving.bf16(rng.standard_normal((2 * n, Hkv, hs)))
+        ref = serving.paged_attn(c, q, starts([n, n]), 0.088)
+        y = t.zeros(2 * n, w, dtype=t.bfloat16, device="cuda")
+        lse = t.zeros(2 * n, Hkv, device="cuda")
+        qd, qs = dev(q.reshape(2 * n, w), t.bfloat16), dev(starts([n, n]))
+        gk.gk_paged_attn(gkctx, h, gk.GK_BF16, qd, w, y, w, lse, qs, 2, Hkv, 2 * n, n, 0.088)
+        gk.gk_sync(gkctx)
+        check_attention(y.float().cpu().numpy().reshape(ref[0].shape), lse.cpu().numpy(), ref, n)
+    # write and read at the same places as in the small cache: the same bits
+    new = t.from_numpy(rng.standard_normal((2, 200, w)).astype(np.float32)).cuda()
+    qs = dev(starts([100, 100]))
+    out = []
+    for cache_h in (h, d.h):
+        gk.gk_paged_write(gkctx, cache_h, gk.GK_F32, new[0], w, new[1], w, qs, 2, 200)
+        o = t.zeros(2, 200, w, device="cuda")
+        gk.gk_paged_read(gkctx, cache_h, gk.GK_F32, o[0], w, o[1], w, qs, 2, 200)
+        gk.gk_sync(gkctx)
+        out.append(o)
+    assert t.equal(out[0], out[1])
+    assert float((out[0] - new).abs().max()) < 0.05  # half a step of values below 6, or bf16's rounding of them
+
+
+def test_two_contexts_at_once(gkctx):
+    """Calls of two contexts on two streams run together, each with a workspace of its own: the bits of one alone."""
+    from gpt_decoder_gb300 import gk
+
+    t = _t()
+    rng = np.random.default_rng(900)
+    jobs = []
+    for n, hs, q8 in ((300, 128, True), (260, 64, False), (1, 64, True), (1, 128, False)):
+        c = cache(rng, [3000, 900], 2, hs, 64, q8)
+        q = dev(rng.standard_normal((2 * n, 8 * hs)), t.bfloat16)
+        jobs.append((Dev(c), q, dev(starts([n, n])), n, 8 * hs))
+    W = dev(rng.standard_normal((512, 1000)).astype(np.float32))
+    wq, sc = t.zeros(1000, 256, dtype=t.uint8, device="cuda"), t.zeros(1000, 16, dtype=t.bfloat16, device="cuda")
+    gk.gk_quant_w4(gkctx, W, 1000, 0, wq, sc, 32, 512, 1000)
+    x, u = dev(rng.standard_normal((5, 512)), t.bfloat16), dev(rng.random(5).astype(np.float32))
+    p = dev(np.full(5, 0.9, np.float32))
+    gk.gk_sync(gkctx)
+
+    def outputs():
+        return [t.zeros(q.shape, dtype=t.bfloat16, device="cuda") for _, q, _, _, _ in jobs] + [
+            t.zeros(5, 1000, device="cuda"), t.zeros(5, dtype=t.int32, device="cuda")]
+
+    def run(ctx, out):
+        for (d, q, qs, n, w), y in zip(jobs, out):
+            gk.gk_paged_attn(ctx, d.h, gk.GK_BF16, q, w, y, w, None, qs, 2, 8, 2 * n, n, 0.1)
+        gk.gk_matvec_w4(ctx, gk.GK_BF16, x, 512, wq, sc, 32, None, None, 0, out[-2], 1000, gk.GK_F32, 5, 512, 1000)
+        gk.gk_sample_rows(ctx, gk.GK_F32, out[-2], 1000, 5, 1000, u, None, None, p, None, out[-1])
+
+    want = outputs()
+    t.cuda.synchronize()
+    run(gkctx, want)
+    gk.gk_sync(gkctx)
+    ctxs = [gk.Ctx(t.cuda.Stream(), workspace_bytes=64 << 20) for _ in range(2)]
+    got = [[outputs() for _ in range(10)] for _ in ctxs]
+    t.cuda.synchronize()
+    for i in range(10):
+        for ctx, o in zip(ctxs, got):
+            run(ctx, o[i])
+    for ctx in ctxs:
+        gk.gk_sync(ctx)
+        ctx.close()
+    for o in got:
+        for each in o:
+            for a, b in zip(each, want):
+                assert t.equal(a, b)

@@ -161,6 +161,18 @@ def test_binding_refuses_mismatched_cache_tensors():
         gk._batch(c, 3, "gk_paged_read")
 
 
+def test_binding_refuses_cache_tensors_on_different_devices():
+    import torch
+
+    from gpt_decoder_gb300 import gk
+
+    k = torch.zeros(3, 2, 16, 32, dtype=torch.bfloat16)
+    t, n = torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    gk.PagedKv(k, k.clone(), None, None, t, n)
+    with pytest.raises(ValueError):
+        gk.PagedKv(k, k.clone(), None, None, t.to("meta"), n)
+
+
 def test_calls_without_a_context_are_refused():
     import ctypes as ct
 
