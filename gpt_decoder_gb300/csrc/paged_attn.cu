@@ -1,5 +1,5 @@
-// Attention of a few new tokens over the paged cache (decoding): the entry point, the kernel for
-// up to 64 query rows per key / value head, and the joining of split sequences.
+// Attention of a few new tokens over the paged cache (decoding): the entry point, the kernel for few rows (
+// up to 64 query rows per key / value head, 32 of bf16 pages), and the joining of split sequences.
 // [LM4] = "Build a language model in C# from scratch (4): running GPT-2 weights", "Generation with
 // a KV cache" (the new tokens' queries against every cached position, no mask but the order).
 //
@@ -17,8 +17,8 @@
 // shared memory in tiles of 128 rows: at these few rows it would compute 16 times what is needed
 // and every byte would make the trip through shared memory.)
 //   rows per key / value head: all H / Hkv heads of all n queries; row i is query i / G, head i % G.
-//   A warp takes 8 or 16 rows (NT = 1, 2) and every KG-th tile of 16 keys; up to 64 rows are 4
-//   warps of the block next to each other, which read the same keys (L1 serves three of them).
+//   A warp takes 8 or 16 rows (NT = 1, 2) and every KG-th tile of 16 keys; more rows are 2 or 4
+//   warps of the block next to each other, which read the same keys (L1 serves all but one of them).
 // 8-bit codes become bf16 exactly (|code| < 2^7): (code & 0x7f | 0x4300) is 128 + the low bits, and
 // (code & 0x80 | 0x4300) is 128 or 256, so their difference is the code. The key's scale multiplies
 // the score, the value's scale the weight.
@@ -428,39 +428,60 @@ __global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) 
     }
 }
 
-// A warp per (row, head), four dims a lane, eight pieces' loads in flight.
+// A warp per (row, head) and up to eight pieces, four dims a lane, its pieces' loads in flight together;
+// with more pieces 2, 4 or 8 warps of the block share them and add their sums in shared memory.
 constexpr int JOIN_WARPS = 8;
+__host__ __device__ constexpr int join_log2(int splits) { return splits <= 8 ? 0 : splits <= 16 ? 1 : splits <= 32 ? 2 : 3; }
 __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_join_kernel(const AttnArgs a) {
+    __shared__ float4 s_o[JOIN_WARPS][32];
+    __shared__ float s_l[JOIN_WARPS];
     wait_for_earlier_kernels();
-    const int lane = threadIdx.x & 31;
-    const int64_t out = (int64_t)blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lg = join_log2(a.splits), share = 1 << lg, sub = warp & (share - 1);
+    const int64_t out = (int64_t)blockIdx.x * (JOIN_WARPS >> lg) + (warp >> lg);
     const int r = (int)(out / a.H), h = (int)(out - (int64_t)r * a.H);
-    if (r >= a.rows) return;
-    const int b = find_sequence(a.q_start, a.B, r);
-    if (b < 0) return;
-    const int s0 = a.q_start[b], s1 = a.q_start[b + 1];
-    if (s0 < 0 || r < s0 || r >= s1 || s1 - s0 > a.max_q || s1 > a.rows) return;
-    const int kv = min(max(a.p.kv_len[b], 0), a.p.capacity);
-    const int pieces = kv <= 0 ? 1 : (kv + a.split_keys(kv) - 1) / a.split_keys(kv);
-    const float2* ml = a.part_ml + out * a.splits;
-    const int per = a.p.hs >> 2;
-    const float4* po = reinterpret_cast<const float4*>(a.part_o + out * a.splits * a.p.hs) + min(lane, per - 1);
-    float top = -INFINITY;
-    for (int s = lane; s < pieces; s += 32) top = fmaxf(top, ml[s].x);
-    top = warp_max(top);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 8
-    for (int s = 0; s < pieces; ++s) {
-        const float2 x = ml[s];
-        const float4 v = po[s * per];
-        // a piece in which the row sees nothing has sum 0 (or NaN, which stays) and no reference
-        const float c = x.x == -INFINITY ? (x.y == 0.f ? 0.f : 1.f) : ex2(x.x - top);
-        if (c != 0.f) {
-            l += x.y * c;
-            o.x += v.x * c, o.y += v.y * c, o.z += v.z * c, o.w += v.w * c;
+    int pieces = 0;
+    if (r < a.rows) {
+        const int b = find_sequence(a.q_start, a.B, r);
+        if (b >= 0) {
+            const int s0 = a.q_start[b], s1 = a.q_start[b + 1];
+            if (s0 >= 0 && r >= s0 && r < s1 && s1 - s0 <= a.max_q && s1 <= a.rows) {
+                const int kv = min(max(a.p.kv_len[b], 0), a.p.capacity);
+                pieces = kv <= 0 ? 1 : (kv + a.split_keys(kv) - 1) / a.split_keys(kv);
+            }
         }
     }
+    const int per = a.p.hs >> 2;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f, top = -INFINITY;
+    if (pieces) {
+        const float2* ml = a.part_ml + out * a.splits;
+        const float4* po = reinterpret_cast<const float4*>(a.part_o + out * a.splits * a.p.hs) + min(lane, per - 1);
+        for (int s = lane; s < pieces; s += 32) top = fmaxf(top, ml[s].x);
+        top = warp_max(top);
+#pragma unroll 8
+        for (int s = sub; s < pieces; s += share) {
+            const float2 x = ml[s];
+            const float4 v = po[s * per];
+            // a piece in which the row sees nothing has sum 0 (or NaN, which stays) and no reference
+            const float c = x.x == -INFINITY ? (x.y == 0.f ? 0.f : 1.f) : ex2(x.x - top);
+            if (c != 0.f) {
+                l += x.y * c;
+                o.x += v.x * c, o.y += v.y * c, o.z += v.z * c, o.w += v.w * c;
+            }
+        }
+    }
+    if (lg) {
+        s_o[warp][lane] = o;
+        if (lane == 0) s_l[warp] = l;
+        __syncthreads();
+        if (sub) return;
+        for (int w = 1; w < share; ++w) {
+            const float4 v = s_o[warp + w][lane];
+            o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+            l += s_l[warp + w];
+        }
+    }
+    if (!pieces) return;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     if (lane < per)
         *reinterpret_cast<uint2*>(a.y + (int64_t)r * a.ldy + h * a.p.hs + lane * 4) = make_uint2(pack(o.x * inv, o.y * inv), pack(o.z * inv, o.w * inv));
@@ -474,15 +495,16 @@ gk_status few(gk_ctx* ctx, const AttnArgs& a) {
 #define FEW(NT, KG) return launch_dependent(ctx, "paged_attn", attn_few_kernel<HSP, Q8, NT, KG>, grid, block, 0, 1, a)
     if (R <= 8) FEW(1, 4);
     if (R <= 16) FEW(2, 4);
-    if (R <= 32) FEW(2, 2);
-    FEW(2, 1);
+    if constexpr (Q8)
+        if (R > 32) FEW(2, 1);
+    FEW(2, 2);
 #undef FEW
 }
 
 }  // namespace
 
 gk_status launch_attn_join(gk_ctx* ctx, const AttnArgs& a) {
-    return launch_dependent(ctx, "paged_attn_join", attn_join_kernel, dim3((unsigned)cdiv((int64_t)a.rows * a.H, JOIN_WARPS)),
+    return launch_dependent(ctx, "paged_attn_join", attn_join_kernel, dim3((unsigned)cdiv((int64_t)a.rows * a.H, JOIN_WARPS >> join_log2(a.splits))),
                             dim3(JOIN_WARPS * 32), 0, 1, a);
 }
 
@@ -524,12 +546,17 @@ extern "C" gk_status gk_paged_attn(gk_ctx* ctx, const gk_paged_kv* cache, int dt
     a.scale_log2 = scale * 1.4426950408889634f;
     a.err = ctx->d_err;
     const int64_t R = (int64_t)a.max_q * a.G, per = rows * H * (a.p.hs * 4 + 8);
-    const bool few = R <= 64;
+    // Up to 64 rows of 8-bit pages, 32 of bf16 ones, take the few-rows kernel. (48 sequences, kv up to 4000, 8
+    // key / value heads of 128, 64 rows: 8-bit 224 us against 429 in tiles; bf16 221 against 121, and with 32
+    // rows 126 against 129.)
+    const bool few = R <= (a.p.k_scale ? 64 : 32);
     const int64_t units = (int64_t)B * a.p.Hkv * (few ? 1 : cdiv(R, 256));
     char* ws = static_cast<char*>(ctx->ws);
     size_t room = ctx->ws_bytes;
-    if (!few && a.p.k_scale && R >= 512) {
-        // codes to bf16 once, in the workspace, when at least two pairs of row tiles read them
+    if (!few && a.p.k_scale && (a.p.hs > 64 || R > 512)) {
+        // Codes to bf16 once, in the workspace. Unpacking on the way is the slower the longer the rows: 2
+        // sequences, kv up to 16384, 8 heads of 128 take 69 against 98 us at 68 rows and 79 against 128 at
+        // 256; with heads of 64 (3 sequences, 12 heads) 512 rows take 80 against 74 us and 700 106 against 109.
         const int64_t er = (int64_t)B * a.p.Hkv * cdiv(a.p.capacity, 128) * 128, bytes = er * a.p.hs * 2;
         if (er < (1ll << 31) && (size_t)bytes <= room / 2) {
             a.expanded_k = reinterpret_cast<__nv_bfloat16*>(ws);
@@ -541,13 +568,19 @@ extern "C" gk_status gk_paged_attn(gk_ctx* ctx, const gk_paged_kv* cache, int dt
     }
     int64_t splits;
     if (few) {
-        // enough pieces for 16 blocks an SM in all (four are resident; the rest evens out sequences of
-        // unequal lengths), of 128 keys at least, 256 where the batch alone fills the GPU
-        a.min_split = units >= ctx->num_sms ? 256 : 128;
-        splits = cdiv(16 * (int64_t)ctx->num_sms, units);
+        // Pieces that give the GPU one wave of blocks (four an SM), or for batches that come near to filling it
+        // by themselves four waves, which even out sequences of unequal lengths; short pieces where there are
+        // few. (Sequences of up to 8191 over 8 heads of 128, 4 / 16 blocks an SM: 4 of them 17.8 / 23.3 us, 16
+        // 45 / 39, 48 105 / 94. Least pieces of 128 / 256 / 1024: 16 of them 39 / 37 / -, 48 96 / 94 / 88; one
+        // of 777 9.3 / 9.6 / 10.7.)
+        const bool alone = units < ctx->num_sms / 2;
+        a.min_split = alone ? 128 : units < ctx->num_sms ? 256 : 1024;
+        splits = cdiv((alone ? 4 : 16) * (int64_t)ctx->num_sms, units);
     } else {
-        a.min_split = 512;
-        splits = cdiv((int64_t)ctx->num_sms, units);  // one wave: more blocks cost more to join than they even out
+        // One wave: more blocks cost more to join than they even out (chunks of 1000 over 8100 keys with one /
+        // two / four waves: 86 / 85 / 99 us); pieces of 1024 (100 rows of one sequence: 27.6 us, 512 33.9).
+        a.min_split = 1024;
+        splits = cdiv((int64_t)ctx->num_sms, units);
     }
     splits = std::min<int64_t>(splits, cdiv(a.p.capacity, a.min_split));
     splits = std::min<int64_t>(splits, std::min<int64_t>(256, (int64_t)(room / per)));

@@ -33,9 +33,9 @@ struct AttnArgs {
     }
 };
 
-// Join the pieces: one block per (row, head).
+// Join the pieces of every (row, head).
 gk_status launch_attn_join(gk_ctx* ctx, const AttnArgs& a);
-// Sequences with at most 64 query rows per key / value head.
+// Sequences with at most 64 query rows per key / value head (32 where pages are bf16).
 gk_status launch_attn_few(gk_ctx* ctx, const AttnArgs& a);
 // Any number of rows, in tiles of 128 on the tensor cores (tcgen05).
 gk_status launch_attn_tiles(gk_ctx* ctx, const AttnArgs& a);

@@ -459,22 +459,27 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!ok) break;
                 uint8_t* tile = (is_v ? sV : sK) + stage * L::TILE;
                 if (!is_v) leave_scales(j, refused);
-                // lane: 16 codes of a row, 128 / HSP * 4 rows a pass; loads run four passes ahead
+                // lane: 16 codes of a row, 128 / HSP * 4 rows a pass; loads run AHEAD passes ahead
                 constexpr int TPR = HSP / 16, RPP = 32 / TPR, PASSES = KT / RPP;
                 const int c = lane % TPR, half = c >> 2, r_in = lane / TPR;
                 const int at = min(c * 16, row_bytes - 16);  // (dims past hs: Q is zero there, and they are not stored)
-                uint4 x[4];
+                constexpr int AHEAD = HSP == 64 ? 4 : 8;
+                uint4 x[AHEAD];
                 auto load = [&](int i) {
                     const int r = i * RPP + r_in;
                     const int64_t row = group_row(j, (i * RPP) >> 4) + (r & 15);
-                    return __ldg(reinterpret_cast<const uint4*>(pages + row * row_bytes + at));
+                    uint4 v;  // (volatile: kept this far ahead of its use)
+                    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                 : "l"(pages + row * row_bytes + at));
+                    return v;
                 };
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = load(i);
-#pragma unroll 4
+                for (int i = 0; i < AHEAD; ++i) x[i] = load(i);
+#pragma unroll AHEAD
                 for (int i = 0; i < PASSES; ++i) {
-                    const uint4 now = x[i & 3];
-                    if (i + 4 < PASSES) x[i & 3] = load(i + 4);
+                    const uint4 now = x[i & (AHEAD - 1)];
+                    if (i + AHEAD < PASSES) x[i & (AHEAD - 1)] = load(i + AHEAD);
                     const int r = i * RPP + r_in;
                     const uint4 lo = make_uint4(codes_pair(a.masks, now.x, 0), codes_pair(a.masks, now.x, 1), codes_pair(a.masks, now.y, 0), codes_pair(a.masks, now.y, 1));
                     const uint4 hi = make_uint4(codes_pair(a.masks, now.z, 0), codes_pair(a.masks, now.z, 1), codes_pair(a.masks, now.w, 0), codes_pair(a.masks, now.w, 1));

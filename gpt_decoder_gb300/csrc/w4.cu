@@ -268,11 +268,12 @@ gk_status run_w4(gk_ctx* ctx, W4Args& a) {
                             dim3(W4_WARPS * 32), BYTES, a.slices, a);
 }
 
-// Two tiles of outputs per warp halve the reads of X (from L1) once there are enough tiles for
-// two blocks an SM all the same.
+// Two tiles of outputs per warp halve the reads of X (from L1) once there are three such pairs for two
+// SMs: K = 8192, two tiles against one: M = 5000 12.3 / 10.6 us, 8192 12.3 / 13.1 (16 rows 15.4 / 18.0), 28672
+// 36.4 / 37.4 (16 rows 47 / 53).
 template <int LW, int NT>
 gk_status run_w4_tiles(gk_ctx* ctx, W4Args& a) {
-    return a.M >= 32 * 2 * ctx->num_sms ? run_w4<LW, NT, 2>(ctx, a) : run_w4<LW, NT, 1>(ctx, a);
+    return a.M >= 48 * ctx->num_sms ? run_w4<LW, NT, 2>(ctx, a) : run_w4<LW, NT, 1>(ctx, a);
 }
 
 template <int LW>
