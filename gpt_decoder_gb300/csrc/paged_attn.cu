@@ -72,6 +72,42 @@ __device__ __forceinline__ bool drop_odd(uint32_t& x) {
     return lo || hi;
 }
 
+// Join the pieces that the blocks of a cluster hold in shared memory: two dims a thread, over all of the
+// cluster's threads, every piece's words on their way at once.
+constexpr int MAX_CLUSTER = 8;
+__device__ __forceinline__ void join_cluster(const AttnArgs& a, int s0, int hk, int R, int kv, int split, const float* o, int ld,
+                                             const float2* ml) {
+    __syncwarp();
+    cluster_barrier();
+    const int piece = a.split_keys(kv), pieces = max(1, (kv + piece - 1) / piece), hs = a.p.hs, per = hs >> 1;
+    for (int x = split * WARPS * 32 + threadIdx.x; x < R * per; x += a.splits * WARPS * 32) {
+        const int r = x / per, d = (x - r * per) * 2;
+        float m[MAX_CLUSTER], w[MAX_CLUSTER], v[MAX_CLUSTER][2], top = -INFINITY, l = 0.f, y[2] = {0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < MAX_CLUSTER; ++s) {
+            const int from = min(s, pieces - 1);
+            m[s] = load_cluster(&ml[r].x, from), w[s] = load_cluster(&ml[r].y, from);
+            v[s][0] = load_cluster(o + r * ld + d, from), v[s][1] = load_cluster(o + r * ld + d + 1, from);
+        }
+#pragma unroll
+        for (int s = 0; s < MAX_CLUSTER; ++s)
+            if (s < pieces) top = fmaxf(top, m[s]);
+#pragma unroll
+        for (int s = 0; s < MAX_CLUSTER; ++s) {
+            // a piece in which the row sees nothing has sum 0 (or NaN, which stays) and no reference
+            const float c = s >= pieces ? 0.f : m[s] == -INFINITY ? (w[s] == 0.f ? 0.f : 1.f) : ex2(m[s] - top);
+            if (c != 0.f) l += w[s] * c, y[0] += v[s][0] * c, y[1] += v[s][1] * c;
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int query = r / a.G, h = hk * a.G + r % a.G;
+        *reinterpret_cast<uint32_t*>(a.y + (int64_t)(s0 + query) * a.ldy + h * hs + d) = pack(y[0] * inv, y[1] * inv);
+        if (a.lse && d == 0)
+            a.lse[(int64_t)(s0 + query) * a.H + h] = l == 0.f ? -INFINITY : ((top == -INFINITY ? 0.f : top) + log2f(l)) * 0.6931471805599453f;
+    }
+    __syncwarp();
+    cluster_barrier();  // no block ends while another reads its words
+}
+
 // HSP: head size rounded up to 64 or 128 (the rest reads as zeros). NT: tiles of 8 rows per warp.
 // KG: warps that share the keys; WARPS / KG groups of rows.
 template <int HSP, bool Q8, int NT, int KG>
@@ -82,6 +118,7 @@ __global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) 
     constexpr int ROWS = NT * 8 * (WARPS / KG);
     __shared__ float s_o[KG][ROWS][HSP + 4];
     __shared__ float2 s_ml[KG][ROWS];
+    __shared__ float2 s_join[ROWS];  // clustered: the piece's reference and sum, its weighted values in s_o[0]
     __shared__ int s_odd;
     wait_for_earlier_kernels();
 
@@ -96,7 +133,10 @@ __global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) 
     if (kv_all > a.p.capacity && threadIdx.x == 0) report(a.err, GK_ERR_INDEX);
     const int R = n * a.G, hs = a.p.hs;
     const int piece = a.split_keys(kv), k_begin = split * piece, k_end = min(kv, k_begin + piece);
-    if (split > 0 && k_begin >= kv) return;
+    if (split > 0 && k_begin >= kv) {
+        if (a.clustered) join_cluster(a, s0, hk, R, kv, split, &s_o[0][0][0], HSP + 4, s_join);
+        return;
+    }
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int kg = warp % KG, row0 = (warp / KG) * NT * 8;
@@ -414,7 +454,11 @@ __global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) 
             }
         }
         const int64_t out = (int64_t)(s0 + query) * a.H + h;
-        if (a.splits > 1) {
+        if (a.clustered) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s_o[0][r][d + e] = v[e];  // (this thread's own words)
+            if (d == 0) s_join[r] = make_float2(top, sum);
+        } else if (a.splits > 1) {
             float* dst = a.part_o + (out * a.splits + split) * hs + d;
             *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
             *reinterpret_cast<float4*>(dst + 4) = make_float4(v[4], v[5], v[6], v[7]);
@@ -426,6 +470,7 @@ __global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) 
             if (a.lse && d == 0) a.lse[out] = sum == 0.f ? -INFINITY : ((top == -INFINITY ? 0.f : top) + log2f(sum)) * 0.6931471805599453f;
         }
     }
+    if (a.clustered) join_cluster(a, s0, hk, R, kv, split, &s_o[0][0][0], HSP + 4, s_join);
 }
 
 // A warp per (row, head) and up to eight pieces, four dims a lane, its pieces' loads in flight together;
@@ -492,7 +537,7 @@ template <int HSP, bool Q8>
 gk_status few(gk_ctx* ctx, const AttnArgs& a) {
     const int64_t R = (int64_t)a.max_q * a.G;
     const dim3 grid((unsigned)(a.p.Hkv * a.splits), (unsigned)a.B), block(WARPS * 32);
-#define FEW(NT, KG) return launch_dependent(ctx, "paged_attn", attn_few_kernel<HSP, Q8, NT, KG>, grid, block, 0, 1, a)
+#define FEW(NT, KG) return launch_dependent(ctx, "paged_attn", attn_few_kernel<HSP, Q8, NT, KG>, grid, block, 0, a.clustered ? a.splits : 1, a)
     if (R <= 8) FEW(1, 4);
     if (R <= 16) FEW(2, 4);
     if constexpr (Q8)
@@ -550,22 +595,28 @@ extern "C" gk_status gk_paged_attn(gk_ctx* ctx, const gk_paged_kv* cache, int dt
     // key / value heads of 128, 64 rows: 8-bit 224 us against 429 in tiles; bf16 221 against 121, and with 32
     // rows 126 against 129.)
     const bool few = R <= (a.p.k_scale ? 64 : 32);
-    const int64_t units = (int64_t)B * a.p.Hkv * (few ? 1 : cdiv(R, 256));
+    a.heads = a.p.Hkv;
     char* ws = static_cast<char*>(ctx->ws);
     size_t room = ctx->ws_bytes;
     if (!few && a.p.k_scale && (a.p.hs > 64 || R > 512)) {
         // Codes to bf16 once, in the workspace. Unpacking on the way is the slower the longer the rows: 2
         // sequences, kv up to 16384, 8 heads of 128 take 69 against 98 us at 68 rows and 79 against 128 at
         // 256; with heads of 64 (3 sequences, 12 heads) 512 rows take 80 against 74 us and 700 106 against 109.
-        const int64_t er = (int64_t)B * a.p.Hkv * cdiv(a.p.capacity, 128) * 128, bytes = er * a.p.hs * 2;
-        if (er < (1ll << 31) && (size_t)bytes <= room / 2) {
+        // If not all heads have room (three quarters, the rest is for pieces), a few of them at a time, while
+        // a launch still fills half the GPU.
+        const int64_t er = (int64_t)B * cdiv(a.p.capacity, 128) * 128, bytes = er * a.p.hs * 2;  // of a head
+        const int64_t fit = (int64_t)(room / 2) >= bytes * a.p.Hkv ? a.p.Hkv : (int64_t)(room / 8 * 3) / bytes;
+        const int64_t turns = fit ? cdiv(a.p.Hkv, fit) : 0, heads = fit ? cdiv(a.p.Hkv, turns) : 0;
+        if (fit && er * heads < (1ll << 31) && (turns == 1 || 2 * heads * B * cdiv(R, 256) >= ctx->num_sms)) {
+            a.heads = (int)heads;
             a.expanded_k = reinterpret_cast<__nv_bfloat16*>(ws);
-            a.expanded_v = reinterpret_cast<__nv_bfloat16*>(ws + bytes);
-            a.expanded_rows = er;
-            ws += 2 * bytes;
-            room -= 2 * (size_t)bytes;
+            a.expanded_v = reinterpret_cast<__nv_bfloat16*>(ws + bytes * heads);
+            a.expanded_rows = er * heads;
+            ws += 2 * bytes * heads;
+            room -= 2 * (size_t)(bytes * heads);
         }
     }
+    const int64_t units = (int64_t)B * a.heads * (few ? 1 : cdiv(R, 256));
     int64_t splits;
     if (few) {
         // Pieces that give the GPU one wave of blocks (four an SM), or for batches that come near to filling it
@@ -583,10 +634,23 @@ extern "C" gk_status gk_paged_attn(gk_ctx* ctx, const gk_paged_kv* cache, int dt
         splits = cdiv((int64_t)ctx->num_sms, units);
     }
     splits = std::min<int64_t>(splits, cdiv(a.p.capacity, a.min_split));
-    splits = std::min<int64_t>(splits, std::min<int64_t>(256, (int64_t)(room / per)));
+    // With few pieces of few sequences the blocks of a cluster join them, without a second launch (one token
+    // over 777 keys 6.5 us, 9.9 with it; 3000 keys 8.7 / 10.2, 4000 10.0 / 10.4, 8000, whose pieces are long
+    // then, 14.5 / 12.0; 48 sequences of up to 8191, whose blocks wait for each other, 122 / 93).
+    const bool cluster = few && units < ctx->num_sms / 2;
+    if (cluster && a.p.capacity <= 4096) splits = std::min<int64_t>(splits, MAX_CLUSTER);
+    a.clustered = cluster && splits > 1 && splits <= MAX_CLUSTER;
+    if (!a.clustered) splits = std::min<int64_t>(splits, std::min<int64_t>(256, (int64_t)(room / per)));
     a.splits = (int)std::max<int64_t>(1, splits);
     a.part_o = reinterpret_cast<float*>(ws);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + rows * H * a.splits * a.p.hs);
-    GK_TRY(few ? launch_attn_few(ctx, a) : launch_attn_tiles(ctx, a));
-    return a.splits > 1 ? launch_attn_join(ctx, a) : GK_OK;
+    if (few) {
+        GK_TRY(launch_attn_few(ctx, a));
+    } else {
+        for (; a.head0 < a.p.Hkv; a.head0 += a.heads) {
+            a.heads = std::min(a.heads, a.p.Hkv - a.head0);
+            GK_TRY(launch_attn_tiles(ctx, a));
+        }
+    }
+    return a.splits > 1 && !a.clustered ? launch_attn_join(ctx, a) : GK_OK;
 }

@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int pair = pairs - 1 - blockIdx.x % pairs;
         it.split = blockIdx.x / pairs;
         it.b = blockIdx.z;
-        it.hk = blockIdx.y;
+        it.hk = a.head0 + blockIdx.y;
         it.s0 = a.q_start[it.b];
         const int s1 = a.q_start[it.b + 1];
         it.n = s1 - it.s0;
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 int64_t sum = 0;
                 for (int i = lane; i < it.b; i += 32) sum += expanded_rows(a.p, i);
                 for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                base_row = sum * a.p.Hkv + (int64_t)it.hk * expanded_rows(a.p, it.b) + it.k_begin;
+                base_row = sum * a.heads + (int64_t)(it.hk - a.head0) * expanded_rows(a.p, it.b) + it.k_begin;
             }
             int in_flight_k = -1, in_flight_v = -1;
             if (warp == 8 && n_kv > 0) {
@@ -701,18 +701,18 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 }
 
-// The codes of every sequence as bf16 rows, heads apart: sequence b's head h at row
-// (sum of expanded_rows before b) * Hkv + h * expanded_rows(b), zeros past its end and on refused pages.
+// The codes of every sequence's heads head0 .. as bf16 rows, heads apart: sequence b's head head0 + h at row
+// (sum of expanded_rows before b) * heads + h * expanded_rows(b), zeros past its end and on refused pages.
 // One pass, a block per 64 positions of a head.
 __global__ void __launch_bounds__(256) expand_kernel(const AttnArgs a, __nv_bfloat16* k_out, __nv_bfloat16* v_out) {
     wait_for_earlier_kernels();
-    const int b = blockIdx.z, hk = blockIdx.y, len = expanded_rows(a.p, b), p0 = blockIdx.x * 64;
+    const int b = blockIdx.z, hk = a.head0 + blockIdx.y, len = expanded_rows(a.p, b), p0 = blockIdx.x * 64;
     if (p0 >= len) return;
     const int lane = threadIdx.x & 31, kv = min(max(a.p.kv_len[b], 0), a.p.capacity), hs = a.p.hs;
     int64_t base = 0;
     for (int i = lane; i < b; i += 32) base += expanded_rows(a.p, i);
     for (int o = 16; o > 0; o >>= 1) base += __shfl_xor_sync(0xffffffffu, base, o);
-    base = base * a.p.Hkv + (int64_t)hk * len;
+    base = base * a.heads + (int64_t)blockIdx.y * len;
     const int per = hs >> 4;
     for (int i = threadIdx.x; i < 64 * per; i += 256) {
         const int pos = p0 + i / per, d = (i % per) * 16;
@@ -742,7 +742,7 @@ gk_status tiles(gk_ctx* ctx, const AttnArgs& a, const __nv_bfloat16* k, const __
                    "gk_paged_attn: tensor map");
     const int64_t pairs = cdiv((int64_t)a.max_q * a.G, 2 * QT);
     return launch_dependent(ctx, "paged_attn_tiles", attn_tiles_kernel<HSP, FROM>,
-                            dim3((unsigned)(pairs * a.splits), (unsigned)a.p.Hkv, (unsigned)a.B), dim3(THREADS), Layout<HSP>::BYTES, 1, a,
+                            dim3((unsigned)(pairs * a.splits), (unsigned)a.heads, (unsigned)a.B), dim3(THREADS), Layout<HSP>::BYTES, 1, a,
                             mk, mv);
 }
 
@@ -752,7 +752,7 @@ gk_status launch_attn_tiles(gk_ctx* ctx, const AttnArgs& a) {
     const bool small = a.p.hs <= 64;
     if (a.expanded_k) {
         const int64_t rows = a.expanded_rows;
-        GK_TRY(launch_dependent(ctx, "paged_attn_expand", expand_kernel, dim3((unsigned)cdiv(a.p.capacity, 128) * 2, (unsigned)a.p.Hkv, (unsigned)a.B),
+        GK_TRY(launch_dependent(ctx, "paged_attn_expand", expand_kernel, dim3((unsigned)cdiv(a.p.capacity, 128) * 2, (unsigned)a.heads, (unsigned)a.B),
                                 dim3(256), 0, 1, a, a.expanded_k, a.expanded_v));
         return small ? tiles<64, EXPANDED>(ctx, a, a.expanded_k, a.expanded_v, rows, KT)
                      : tiles<128, EXPANDED>(ctx, a, a.expanded_k, a.expanded_v, rows, KT);

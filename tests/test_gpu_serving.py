@@ -764,3 +764,21 @@ def test_two_contexts_at_once(gkctx):
         for each in o:
             for a, b in zip(each, want):
                 assert t.equal(a, b)
+
+
+@pytest.mark.parametrize("n, hs, ws", [(1100, 64, 2 << 20), (600, 128, 4 << 20)])
+def test_attention_of_8_bit_chunks_a_few_heads_at_a_time(gkctx, n, hs, ws):
+    """A workspace with room for the codes of two of five heads as bf16: three turns, the last of one head."""
+    from gpt_decoder_gb300 import gk
+
+    t = _t()
+    rng = np.random.default_rng(1000 + hs)
+    Hkv, G, kv = 5, 8, [1300, 1200]
+    c = cache(rng, kv, Hkv, hs, 64, True)
+    a_head = 2 * 2 * 1408 * hs * 2  # keys and values, two sequences in whole tiles of 128
+    assert 2 * a_head <= ws * 3 // 4 < 3 * a_head and 2 * 2 * 2 * -(-n * G // 256) >= 152
+    q = serving.bf16(rng.standard_normal((2 * n, Hkv * G, hs)))
+    ref = serving.paged_attn(c, q, starts([n, n]), 0.1)
+    ctx = gk.Ctx(t.cuda.current_stream().cuda_stream, workspace_bytes=ws)
+    check_attention(*attend(ctx, c, q, [n, n], 0.1), ref, hs)
+    ctx.close()
