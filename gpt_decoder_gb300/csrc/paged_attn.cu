@@ -24,6 +24,9 @@
 // the score, the value's scale the weight.
 // Weights are split into two bf16 parts (hi + lo: 16 significant bits), so the result carries no
 // rounding but the output's.
+// Measured: 48 sequences of up to 8191 keys, 32 query heads over 8 of 128, one token each: bf16 pages 122 us, 5.0
+// TB/s of the cache's bytes (0.74 of a copy); 8-bit ones 88 us, 3.6 TB/s, bound by the instructions that
+// unpack codes (four a pair), not by the bytes. One token over 777 keys of 12 heads: 6.5 us from the host.
 #include <math.h>
 
 #include <algorithm>

