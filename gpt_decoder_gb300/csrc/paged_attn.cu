@@ -24,9 +24,9 @@
 // the score, the value's scale the weight.
 // Weights are split into two bf16 parts (hi + lo: 16 significant bits), so the result carries no
 // rounding but the output's.
-// Measured: 48 sequences of up to 8191 keys, 32 query heads over 8 of 128, one token each: bf16 pages 122 us, 5.0
-// TB/s of the cache's bytes (0.74 of a copy); 8-bit ones 88 us, 3.6 TB/s, bound by the instructions that
-// unpack codes (four a pair), not by the bytes. One token over 777 keys of 12 heads: 6.5 us from the host.
+// Measured: 48 sequences of up to 8191 keys, 32 query heads over 8 of 128, one token each: bf16 pages 113 us, 5.4
+// TB/s of the cache's bytes (0.80 of a copy); 8-bit ones 88 us, 3.6 TB/s, bound by the instructions that
+// unpack codes (four a pair) and 12 warps an SM to cover the loads' latency. One token over 777 keys of 12 heads: 6.5 us from the host.
 #include <math.h>
 
 #include <algorithm>
@@ -220,6 +220,17 @@ __global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) 
             }
             bad_page |= bad;
             refused = __ballot_sync(0xffffffffu, bad);
+        }
+        // bf16 rows of more than 64: the next tile's keys and values (16 rows of its page) are sent for to L2, as
+        // a warp's own loads leave too little on its way (48 sequences of heads of 128 124 -> 113 us, 200 of them
+        // 127 -> 117, one token 7.3 -> 7.5; not with 8 bits, 89 -> 92, nor heads of 64 in pages of 16, 13.6 -> 14.9)
+        if constexpr (!Q8 && HSP == 128) {
+            if (lane == (j & 31) + 1 && j + 1 < mine) {
+                const int pos = k_begin + (kg + KG * (j + 1)) * 16;
+                const int64_t at = ((((int64_t)ids * a.p.Hkv + hk) << a.p.page_log2) + (pos & ((1 << a.p.page_log2) - 1))) * row_bytes;
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(static_cast<const char*>(a.p.k) + at), "r"(16 * row_bytes));
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(static_cast<const char*>(a.p.v) + at), "r"(16 * row_bytes));
+            }
         }
         const int id = __shfl_sync(0xffffffffu, ids, j & 31);
         const int pos = k_begin + (kg + KG * j) * 16;
