@@ -782,3 +782,34 @@ def test_attention_of_8_bit_chunks_a_few_heads_at_a_time(gkctx, n, hs, ws):
     ctx = gk.Ctx(t.cuda.current_stream().cuda_stream, workspace_bytes=ws)
     check_attention(*attend(ctx, c, q, [n, n], 0.1), ref, hs)
     ctx.close()
+
+
+@pytest.mark.parametrize("n, hs, q8", [(1, 64, False), (1, 128, True), (6, 48, True), (9, 128, False)])
+def test_attention_of_few_short_sequences_captured(gkctx, n, hs, q8):
+    """Pieces joined inside a cluster: no workspace, sequences of one piece and of several, a padding row, replays on
+    lengths that change between them."""
+    from gpt_decoder_gb300 import gk
+
+    t = _t()
+    rng = np.random.default_rng(1100 + n)
+    c = cache(rng, [1000, 40, 129, 0], 2, hs, 16, q8)
+    q = serving.bf16(rng.standard_normal((4 * n, 6, hs)))
+    w, qs = 6 * hs, dev(starts([n] * 4))
+    s = t.cuda.Stream()
+    ctx = gk.Ctx(s, workspace_bytes=0)
+    d, qd = Dev(c, poison=False), dev(q.reshape(4 * n, w), t.bfloat16)
+    y, lse = t.zeros(4 * n, w, dtype=t.bfloat16, device="cuda"), t.zeros(4 * n, 6, device="cuda")
+    t.cuda.synchronize()
+    g = t.cuda.CUDAGraph()
+    with t.cuda.graph(g, stream=s):
+        gk.gk_paged_attn(ctx, d.h, gk.GK_BF16, qd, w, y, w, lse, qs, 4, 6, 4 * n, n, 0.2)
+    for lens in ([1000, 40, 129, 0], [777, 12, 128, 0], [129, 1, 0, 0], [1000, 40, 129, 0]):
+        c.kv_len[:] = lens
+        d.kv_len.copy_(dev(c.kv_len))
+        y.fill_(7.0)
+        g.replay()
+        t.cuda.synchronize()
+        ref = serving.paged_attn(c, q, starts([n] * 4), 0.2)
+        check_attention(y.float().cpu().numpy().reshape(ref[0].shape), lse.cpu().numpy(), ref, (lens, n))
+    gk.gk_sync(ctx)
+    ctx.close()
