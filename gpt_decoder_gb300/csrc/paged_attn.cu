@@ -26,7 +26,8 @@
 // rounding but the output's.
 // Measured: 48 sequences of up to 8191 keys, 32 query heads over 8 of 128, one token each: bf16 pages 113 us, 5.4
 // TB/s of the cache's bytes (0.80 of a copy); 8-bit ones 88 us, 3.6 TB/s, bound by the instructions that
-// unpack codes (four a pair) and 12 warps an SM to cover the loads' latency. One token over 777 keys of 12 heads: 6.5 us from the host.
+// unpack codes (four a pair) and 12 warps an SM to cover the loads' latency. One token over 777 keys of 12 heads: 5.6 us
+// from the host.
 #include <math.h>
 
 #include <algorithm>
