@@ -8,7 +8,7 @@
 // row's sequence and page are looked up once by a warp, then all the block's threads go through
 // the rows' 2 Hkv vectors.
 // Measured: reading back 16 sequences of up to 16384 8-bit tokens of 8 heads of 128 as bf16 111 us, 6.2 TB/s
-// (0.91 of a copy); storing 7 chunks of up to 4096 of them and reading those back 40 us, 4.0 TB/s: two launches, each
+// (0.91 of a copy); storing 7 chunks of up to 4096 of them and reading those back 39 us, 4.0 TB/s: two launches, each
 // of a few waves. A few rows cost their launches: 4 us to read 333 rows.
 #include "paged.cuh"
 
@@ -114,8 +114,10 @@ __device__ __forceinline__ void each_vector(const Pages& p, const int32_t* __res
     }
 }
 
+// Eight blocks an SM, at a few spilled words: the last wave is fuller (7 chunks of up to 4096, with their reading:
+// six blocks 41.0 us, eight 39.1; from float32 62.2 / 59.8).
 template <typename S, bool Q8>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(THREADS, 8)
     paged_write_kernel(Pages p, const S* __restrict__ k, int64_t ldk, const S* __restrict__ v, int64_t ldv,
                        const int32_t* __restrict__ q_start, int B, int rows, int rpb, int lanes_log2, int* err) {
     wait_for_earlier_kernels();
