@@ -14,8 +14,8 @@
 // this one have been read, under the softmax. With 128 P lies over S, and the next S waits for P V.
 // The two tiles take turns: while one group of four warps turns its S into P, the tensor core
 // computes the other's products. Warp 8 sends for the keys by TMA, a box per page (pages lie anywhere).
-// 8-bit codes become bf16 (exactly) first: in one pass into the workspace, if it has room and enough
-// tiles of rows will read them; else on the way, by warps 8-11. Codes carry no scale into the products: the key's scale multiplies the score and
+// 8-bit codes become bf16 (exactly) first: in one pass into the workspace, if it has room (for all heads or a few
+// at a time) and heads are wide or rows many; else on the way, by warps 8-11. Codes carry no scale into the products: the key's scale multiplies the score and
 // the value's scale the weight, both from shared memory. Warp 12 issues the MMAs.
 // K and V have rings of their own (a K tile is free once both S are there, a V tile after both
 // products), of three tiles each for head sizes up to 64 and two for 128.
@@ -464,7 +464,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!ok) break;
                 uint8_t* tile = (is_v ? sV : sK) + stage * L::TILE;
                 if (!is_v) leave_scales(j, refused);
-                // lane: 16 codes of a row, 128 / HSP * 4 rows a pass; loads run AHEAD passes ahead
+                // lane: 16 codes of a row, 128 / HSP * 4 rows a pass; loads run AHEAD passes ahead (rows of 128: eight 429 us
+                // against 568 with four, 48 sequences of 64 rows; of 64: 98 against 88)
                 constexpr int TPR = HSP / 16, RPP = 32 / TPR, PASSES = KT / RPP;
                 const int c = lane % TPR, half = c >> 2, r_in = lane / TPR;
                 const int at = min(c * 16, row_bytes - 16);  // (dims past hs: Q is zero there, and they are not stored)
