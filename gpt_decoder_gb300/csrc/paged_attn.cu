@@ -361,8 +361,8 @@ __global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) 
         }
         if (!Q8 && part) {
             // values of keys past the end are not the cache's: zeros. An infinity or NaN that only
-            // later rows see must not meet the earlier rows' zero weights: taken out here, and put
-            // back at the end for the rows that see it.
+            // later rows see must not meet the earlier rows' zero weights: all of the tile's are taken
+            // out here, and put back at the end for the rows that see them.
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const bool none = off || pos + (x >> 1) * 8 + 2 * t + (x & 1) >= kv;
@@ -438,8 +438,9 @@ __global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) 
                 }
         }
     __syncthreads();
-    // write: a piece's sum for the join, or the result
-    const int per = hs >> 3, odd_from = s_odd ? max(k_begin, clear + 1) : 0x7fffffff;
+    // write: a piece's sum for the join, or the result. Values that are not finite were taken out of every tile from
+    // the one that holds key clear + 1 or the end on, keys before it in that tile among them.
+    const int per = hs >> 3, odd_from = s_odd ? max(k_begin, min(clear + 1, kv) & ~15) : 0x7fffffff;
     for (int x = threadIdx.x; x < R * per; x += WARPS * 32) {
         const int r = x / per, d = (x - r * per) * 8;
         float top = -INFINITY, sum = 0.f;

@@ -813,3 +813,74 @@ def test_attention_of_few_short_sequences_captured(gkctx, n, hs, q8):
         check_attention(y.float().cpu().numpy().reshape(ref[0].shape), lse.cpu().numpy(), ref, (lens, n))
     gk.gk_sync(ctx)
     ctx.close()
+
+
+# ------------------------------------------------------- what is not finite where it is seen, and scores far apart
+def attend_odd(gkctx, c, q, n, scale, refused=False):
+    """Attention with infinities or NaN among what rows see: they are in the result exactly where the oracle has
+    them (a NaN or an infinity, not which of the two), and the rest is within the bounds above."""
+    from gpt_decoder_gb300 import gk
+
+    t = _t()
+    rows, H, hs = q.shape
+    w, d = H * hs, Dev(c)
+    y, lse = t.full((rows, w), 3.0, dtype=t.bfloat16, device="cuda"), t.full((rows, H), 3.0, device="cuda")
+    gk.gk_paged_attn(gkctx, d.h, gk.GK_BF16, dev(q.reshape(rows, w), t.bfloat16), w, y, w, lse, dev(starts(n)), len(n), H, rows, max(n), scale)
+    if refused:
+        with pytest.raises(gk.GkError) as e:
+            gk.gk_sync(gkctx)
+        assert e.value.status == gk.GK_ERR_INDEX
+    else:
+        gk.gk_sync(gkctx)
+    y, lse = y.float().cpu().numpy().reshape(q.shape).astype(np.float64), lse.cpu().numpy()
+    yr, lr, spread = serving.paged_attn(c, q, starts(n), scale)
+    odd = ~np.isfinite(yr)
+    assert odd.any() and not odd.all()
+    assert np.array_equal(odd, ~np.isfinite(y)), np.argwhere(odd != ~np.isfinite(y))[:4].tolist()
+    tol = U * (np.abs(yr) + spread) + 2.0 ** -10 * spread
+    assert (np.abs(y[~odd] - yr[~odd]) <= tol[~odd]).all()
+    assert np.abs(lse - lr).max() < 2.0 ** -10 * max(1.0, np.abs(lr).max() / 64)
+
+
+def make_odd(c, b, pos):
+    """Infinities and a NaN in the value at a position: of the first and the last head (8 bits: the head's scale)."""
+    p, r = c.place(b, pos)
+    if c.v_scale is not None:
+        c.v_scale[p, 0, r] = np.nan
+    else:
+        c.v[p, 0, r, 5], c.v[p, 0, r, 9], c.v[p, -1, r, 0] = np.inf, np.nan, -np.inf
+
+
+SEEN_FEW = [  # kv_len, new tokens, H, Hkv, hs, page; sequence b's value this far before its last token is not finite (and the last sequence's all are)
+    (777, 1, 2, 2, 64, 16, [0, 3, 8, 9, 700]),  # the last tile of 16 keys begins 8 before the last of 777
+    (130, 1, 4, 1, 128, 64, [0, 1, 2, 100]),
+    (144, 1, 4, 2, 80, 16, [0, 15, 16]),
+    (5000, 1, 2, 2, 64, 16, [0, 7, 8, 4900]),  # in pieces
+    (130, 5, 2, 2, 48, 32, [0, 3, 4, 5, 17, 18, 90]),  # the first of the new tokens is 4 before the last
+    (128, 3, 4, 2, 64, 16, [0, 2, 3, 15, 16]),  # 16 rows of a key / value head: see also the next
+    (1000, 8, 4, 2, 64, 16, [0, 7, 8, 9, 23, 24]),
+    (300, 16, 2, 1, 128, 16, [0, 15, 16, 27, 28]),  # and 32
+]
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("case", range(len(SEEN_FEW)))
+def test_attention_seen_infinities_and_nan_few_rows(gkctx, case, q8):
+    kv, n, H, Hkv, hs, page, backs = SEEN_FEW[case]
+    rng = np.random.default_rng(1200 + case)
+    c = cache(rng, [kv] * (len(backs) + 1), Hkv, hs, page, q8)
+    for b, back in enumerate(backs):
+        make_odd(c, b, kv - 1 - back)
+    q = serving.bf16(rng.standard_normal((n * (len(backs) + 1), H, hs)))
+    attend_odd(gkctx, c, q, [n] * (len(backs) + 1), 0.125)
+
+
+def test_attention_seen_infinities_few_rows_of_refused_pages(gkctx):
+    """Values that are not finite on both sides of a refused page, and in the last tile behind one."""
+    rng = np.random.default_rng(1300)
+    c = cache(rng, [203] * 3, 2, 64, 16, False)
+    for b, pos in enumerate((150, 176, 202)):
+        make_odd(c, b, pos)
+    c.table[0, 10], c.table[1, 10], c.table[2, 11] = -1, c.n_pages, -5
+    for n in (1, 5):
+        attend_odd(gkctx, c, serving.bf16(rng.standard_normal((3 * n, 4, 64))), [n] * 3, 0.125, refused=True)
