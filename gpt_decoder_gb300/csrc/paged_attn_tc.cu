@@ -380,8 +380,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         if constexpr (FROM != PAGES8) {
             // Warp 8 sends for the tiles: whole boxes of a page's rows (EXPANDED: the tile's 128 rows) by TMA.
             // Tiles of V that hold keys some row must not see, or past the end, or on refused pages, it copies
-            // itself: what is not finite or not there becomes zeros (and is put back at the end for the rows
-            // that see it). EXPANDED tiles are finite, and zeros past the end.
+            // itself: what is not there becomes zeros, and so does what is not finite of keys that some row must
+            // not see (put back at the end for the rows that see it). Keys up to `clear` stay as they are.
+            // EXPANDED tiles are finite, and zeros past the end.
             const int box = FROM == EXPANDED ? KT : min(KT, 1 << a.p.page_log2);
             int64_t base_row = 0;  // EXPANDED: this head's first row
             if constexpr (FROM == EXPANDED) {
@@ -427,7 +428,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             const int r = i / L::HALVES * 4 + lane / 8, c = (i % L::HALVES) * 8 + lane % 8;
                             uint4 x = make_uint4(0, 0, 0, 0);
                             if (!none && grp * 16 + r < left && c * 8 < hs) x = __ldg(reinterpret_cast<const uint4*>(src + r * row_bytes + c * 16));
-                            odd |= drop_odd2(x.x) | drop_odd2(x.y) | drop_odd2(x.z) | drop_odd2(x.w);
+                            if (it.k_begin + j * KT + grp * 16 + r > clear) odd |= drop_odd2(x.x) | drop_odd2(x.y) | drop_odd2(x.z) | drop_odd2(x.w);
                             *reinterpret_cast<uint4*>(tile + (c >> 3) * HALF + swizzled(grp * 16 + r, c & 7)) = x;
                         }
                     }

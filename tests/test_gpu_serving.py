@@ -884,3 +884,34 @@ def test_attention_seen_infinities_few_rows_of_refused_pages(gkctx):
     c.table[0, 10], c.table[1, 10], c.table[2, 11] = -1, c.n_pages, -5
     for n in (1, 5):
         attend_odd(gkctx, c, serving.bf16(rng.standard_normal((3 * n, 4, 64))), [n] * 3, 0.125, refused=True)
+
+
+SEEN_TILES = [  # as SEEN_FEW
+    (300, 40, 1, 1, 64, 16, [0, 39, 40, 43, 44, 200]),  # the first new token is at 260, its tile of 128 keys at 256
+    (777, 100, 2, 1, 128, 64, [0, 99, 100, 136, 137, 500]),  # 200 rows
+    (500, 200, 2, 1, 64, 32, [0, 199, 200, 243, 244, 71, 72]),  # 400 rows: two blocks, the second's first token 72 before the last
+    (6000, 70, 1, 1, 80, 128, [0, 69, 70, 111, 112, 5000]),  # in pieces
+]
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("case", range(len(SEEN_TILES)))
+def test_attention_seen_infinities_and_nan_tiles(gkctx, case, q8):
+    kv, n, H, Hkv, hs, page, backs = SEEN_TILES[case]
+    rng = np.random.default_rng(1400 + case)
+    c = cache(rng, [kv] * (len(backs) + 1), Hkv, hs, page, q8)
+    for b, back in enumerate(backs):
+        make_odd(c, b, kv - 1 - back)
+    q = serving.bf16(rng.standard_normal((n * (len(backs) + 1), H, hs)))
+    attend_odd(gkctx, c, q, [n] * (len(backs) + 1), 0.125)
+
+
+@pytest.mark.parametrize("hs", [64, 128])
+def test_attention_seen_infinities_in_tiles_of_refused_pages(gkctx, hs):
+    """A refused page in a tile of keys that every row sees: its neighbours' infinities and NaN stay."""
+    rng = np.random.default_rng(1500 + hs)
+    c = cache(rng, [700] * 4, 1, hs, 16, False)
+    for b, pos in enumerate((150, 180, 120)):
+        make_odd(c, b, pos)
+    c.table[:3, 10] = -1, c.n_pages, -5  # positions 160 .. 175
+    attend_odd(gkctx, c, serving.bf16(rng.standard_normal((4 * 70, 1, hs))), [70] * 4, 0.125, refused=True)
