@@ -98,9 +98,10 @@ __device__ __forceinline__ void join_cluster(const AttnArgs& a, int s0, int hk, 
             if (s < pieces) top = fmaxf(top, m[s]);
 #pragma unroll
         for (int s = 0; s < MAX_CLUSTER; ++s) {
-            // a piece in which the row sees nothing has sum 0 (or NaN, which stays) and no reference
-            const float c = s >= pieces ? 0.f : m[s] == -INFINITY ? (w[s] == 0.f ? 0.f : 1.f) : ex2(m[s] - top);
-            if (c != 0.f) l += w[s] * c, y[0] += v[s][0] * c, y[1] += v[s][1] * c;
+            // a piece in which the row sees nothing has sum 0 (or NaN, which stays) and no reference; its values are
+            // zeros. A factor that underflows still multiplies: what is not finite stays so.
+            const float c = m[s] == -INFINITY ? (w[s] == 0.f ? 0.f : 1.f) : ex2(m[s] - top);
+            if (s < pieces) l += w[s] * c, y[0] += v[s][0] * c, y[1] += v[s][1] * c;
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const int query = r / a.G, h = hk * a.G + r % a.G;
@@ -434,7 +435,7 @@ __global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) 
                 for (int h = 0; h < 2; ++h) {
                     // the dim of tile i's row g + 8 h, as V was dealt out
                     const int d = Q8 ? (HSP == 64 ? g * 8 : g * 16) + 2 * i + h : (i >> 2) * 64 + g * 8 + 2 * (i & 3) + h;
-                    s_o[kg][r][d] = c == 0.f ? 0.f : o[nt][i][e + 2 * h] * c;
+                    s_o[kg][r][d] = o[nt][i][e + 2 * h] * c;  // (c = 0 too: what is not finite stays so)
                 }
         }
     __syncthreads();
@@ -523,12 +524,10 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_join_kernel(const AttnAr
         for (int s = sub; s < pieces; s += share) {
             const float2 x = ml[s];
             const float4 v = po[s * per];
-            // a piece in which the row sees nothing has sum 0 (or NaN, which stays) and no reference
+            // (as in join_cluster)
             const float c = x.x == -INFINITY ? (x.y == 0.f ? 0.f : 1.f) : ex2(x.x - top);
-            if (c != 0.f) {
-                l += x.y * c;
-                o.x += v.x * c, o.y += v.y * c, o.z += v.z * c, o.w += v.w * c;
-            }
+            l += x.y * c;
+            o.x += v.x * c, o.y += v.y * c, o.z += v.z * c, o.w += v.w * c;
         }
     }
     if (lg) {

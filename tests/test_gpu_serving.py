@@ -837,7 +837,9 @@ def attend_odd(gkctx, c, q, n, scale, refused=False):
     odd = ~np.isfinite(yr)
     assert odd.any() and not odd.all()
     assert np.array_equal(odd, ~np.isfinite(y)), np.argwhere(odd != ~np.isfinite(y))[:4].tolist()
-    tol = U * (np.abs(yr) + spread) + 2.0 ** -10 * spread
+    # a weight below float32's smallest normal number, 2^-126, is zero on the device: each of up to 2^14 keys is off by at
+    # most that times its value (below 2^3 here), which shows where the weights above it meet values of zero
+    tol = U * (np.abs(yr) + spread) + 2.0 ** -10 * spread + 2.0 ** (14 - 126 + 3)
     assert (np.abs(y[~odd] - yr[~odd]) <= tol[~odd]).all()
     assert np.abs(lse - lr).max() < 2.0 ** -10 * max(1.0, np.abs(lr).max() / 64)
 
@@ -915,3 +917,51 @@ def test_attention_seen_infinities_in_tiles_of_refused_pages(gkctx, hs):
         make_odd(c, b, pos)
     c.table[:3, 10] = -1, c.n_pages, -5  # positions 160 .. 175
     attend_odd(gkctx, c, serving.bf16(rng.standard_normal((4 * 70, 1, hs))), [70] * 4, 0.125, refused=True)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("kv,n,high", [(100, 1, 20), (1000, 1, 500), (9000, 1, 5000), (9000, 33, 5000), (9000, 70, 5000)])
+def test_attention_seen_infinities_behind_far_larger_scores(gkctx, kv, n, high, q8):
+    """The weight of a value that is not finite may lie below float32's smallest, in another warp's keys or another
+    piece than the row's largest score: the result is not finite all the same. (Scores are exact here: q has one
+    element of 1, and keys hold 508 there or nothing; exp(-508) is above float64's smallest.)"""
+    rng = np.random.default_rng(1600 + n)
+    c = cache(rng, [kv, kv], 2, 64, 16, q8)
+    c.k[:] = 0
+    for b in range(2):
+        p, r = c.place(b, high)
+        c.k[p, :, r, 0] = 127 if q8 else 508
+    if q8:
+        c.k_scale[:] = 4
+    make_odd(c, 0, 3)
+    q = np.zeros((2 * n, 2, 64), np.float32)
+    q[:, :, 0] = 1
+    attend_odd(gkctx, c, q, [n, n], 1.0)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("kv,n,high", [(100, 1, 20), (1000, 1, 500), (9000, 1, 5000), (9000, 33, 5000), (9000, 70, 5000)])
+def test_attention_of_a_nan_key_behind_far_larger_scores(gkctx, kv, n, high, q8):
+    """The same of a key: its score is NaN, and so are the results and log sums of every row that sees it."""
+    rng = np.random.default_rng(1650 + n)
+    c = cache(rng, [kv, kv], 2, 64, 16, q8)
+    c.k[:] = 0
+    for b in range(2):
+        p, r = c.place(b, high)
+        c.k[p, :, r, 0] = 127 if q8 else 508
+    p, r = c.place(0, 3)
+    if q8:
+        c.k_scale[:] = 4
+        c.k_scale[p, 0, r] = np.nan
+    else:
+        c.k[p, 0, r, 7] = np.nan
+    q = np.zeros((2 * n, 2, 64), np.float32)
+    q[:, :, 0] = 1
+    y, lse = attend(gkctx, c, q, [n, n], 1.0)
+    assert np.isnan(y[:n, 0]).all() and np.isnan(lse[:n, 0]).all()
+    ref = serving.paged_attn(c, q, starts([n, n]), 1.0)
+    fine = ~np.isnan(ref[0])
+    assert not fine[:n, 0].any() and fine[:n, 1].all() and fine[n:].all()
+    tol = U * (np.abs(ref[0]) + ref[2]) + 2.0 ** -10 * ref[2] + 2.0 ** (14 - 126 + 3)  # (as in attend_odd)
+    assert (np.abs(y - ref[0])[fine] <= tol[fine]).all()
+    assert np.abs(lse - ref[1])[np.isfinite(ref[1])].max() < 508 / 64 * 2.0 ** -10
