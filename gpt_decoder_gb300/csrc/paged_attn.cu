@@ -584,7 +584,8 @@ extern "C" gk_status gk_paged_attn(gk_ctx* ctx, const gk_paged_kv* cache, int dt
     GK_TRY(check_pages(ctx, "gk_paged_attn", cache, q_start, B, rows, &a.p));
     GK_REQUIRE(ctx, q && y, GK_ERR_ARG, "gk_paged_attn: null pointer");
     GK_REQUIRE(ctx, dtype == GK_BF16, GK_ERR_UNSUPPORTED, "gk_paged_attn: dtype %d (GK_BF16 only)", dtype);
-    GK_REQUIRE(ctx, H >= 1 && H <= 65535 && H % a.p.Hkv == 0 && max_q >= 1 && scale > 0.f && isfinite(scale), GK_ERR_ARG,
+    a.scale_log2 = scale * 1.4426950408889634f;
+    GK_REQUIRE(ctx, H >= 1 && H <= 65535 && H % a.p.Hkv == 0 && max_q >= 1 && scale > 0.f && isfinite(a.scale_log2), GK_ERR_ARG,
                "gk_paged_attn: bad argument");
     GK_REQUIRE(ctx, ldq >= (int64_t)H * a.p.hs && ldy >= (int64_t)H * a.p.hs, GK_ERR_ARG, "gk_paged_attn: row stride");
     GK_REQUIRE(ctx, aligned16(q) && aligned16(y) && ldq % 8 == 0 && ldy % 8 == 0, GK_ERR_ALIGN,
@@ -603,7 +604,6 @@ extern "C" gk_status gk_paged_attn(gk_ctx* ctx, const gk_paged_kv* cache, int dt
     a.G = H / a.p.Hkv;
     a.rows = (int)rows;
     a.max_q = (int)std::min<int64_t>(max_q, rows);
-    a.scale_log2 = scale * 1.4426950408889634f;
     a.err = ctx->d_err;
     const int64_t R = (int64_t)a.max_q * a.G, per = rows * H * (a.p.hs * 4 + 8);
     // Up to 64 rows of 8-bit pages, 32 of bf16 ones, take the few-rows kernel. (48 sequences, kv up to 4000, 8

@@ -459,7 +459,7 @@ gk_status gk_paged_read(gk_ctx* ctx, const gk_paged_kv* cache, int dtype, void* 
  *   max_q   at least every sequence's number of rows (host; it sizes the launch). A sequence with
  *           more rows than max_q, or with rows past `rows`, records GK_ERR_INDEX and its rows
  *           are left as they were.
- *   scale   positive and finite.
+ *   scale   positive, at most 2^127 (it is taken times log2(e): GK_ERR_ARG where that is not finite).
  * A row that sees nothing (a negative position) gets y = 0 and lse = -inf. Keys and values that a
  * row does not see never reach it, whatever they hold (infinities and NaN among it). y must not
  * overlap q, and max_q * H / Hkv stays below 2^30 (GK_ERR_UNSUPPORTED). Long

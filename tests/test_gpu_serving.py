@@ -965,3 +965,21 @@ def test_attention_of_a_nan_key_behind_far_larger_scores(gkctx, kv, n, high, q8)
     tol = U * (np.abs(ref[0]) + ref[2]) + 2.0 ** -10 * ref[2] + 2.0 ** (14 - 126 + 3)  # (as in attend_odd)
     assert (np.abs(y - ref[0])[fine] <= tol[fine]).all()
     assert np.abs(lse - ref[1])[np.isfinite(ref[1])].max() < 508 / 64 * 2.0 ** -10
+
+
+def test_attention_scale_past_its_unit_is_refused(gkctx):
+    """Scores are kept in powers of two: scale * log2(e) has to be a finite float32 too."""
+    from gpt_decoder_gb300 import gk
+
+    t = _t()
+    c = cache(np.random.default_rng(3), [20], 2, 32, 16, False)
+    d, q, qs = Dev(c), t.zeros(4, 64, dtype=t.bfloat16, device="cuda"), dev(starts([4]))
+    y = t.full((4, 64), 3.0, dtype=t.bfloat16, device="cuda")
+    refused(gk.GK_ERR_ARG, gk.gk_paged_attn, gkctx, d.h, gk.GK_BF16, q, 64, y, 64, None, qs, 1, 2, 4, 4, 3e38)
+    gk.gk_sync(gkctx)
+    assert (y == 3).all()
+    gk.gk_paged_attn(gkctx, d.h, gk.GK_BF16, q, 64, y, 64, None, qs, 1, 2, 4, 4, 2.0 ** 127)  # scores of zero: plain means
+    gk.gk_sync(gkctx)
+    ref = serving.paged_attn(c, np.zeros((4, 2, 32)), starts([4]), 1.0)
+    yr, spread = ref[0].reshape(4, 64), ref[2].reshape(4, 64)
+    assert (np.abs(y.float().cpu().numpy() - yr) <= U * (np.abs(yr) + spread) + 2.0 ** -10 * spread).all()
