@@ -983,3 +983,25 @@ def test_attention_scale_past_its_unit_is_refused(gkctx):
     ref = serving.paged_attn(c, np.zeros((4, 2, 32)), starts([4]), 1.0)
     yr, spread = ref[0].reshape(4, 64), ref[2].reshape(4, 64)
     assert (np.abs(y.float().cpu().numpy() - yr) <= U * (np.abs(yr) + spread) + 2.0 ** -10 * spread).all()
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("n,H", [(1, 2), (10, 2), (40, 4), (200, 2)])
+def test_attention_of_lengths_past_the_table(gkctx, n, H, q8):
+    """Rows at positions that the table has no room for: reported, and every token that is there is attended."""
+    from gpt_decoder_gb300 import gk
+
+    t = _t()
+    rng = np.random.default_rng(1700 + n)
+    c = cache(rng, [320, 100], 2, 64, 16, q8)
+    d = Dev(c)
+    c.kv_len[0] = 325
+    d.kv_len.copy_(dev(c.kv_len))
+    q = serving.bf16(rng.standard_normal((2 * n, H, 64)))
+    w, ref = H * 64, serving.paged_attn(c, q, starts([n, n]), 0.125)
+    y, lse = t.full((2 * n, w), 9.0, dtype=t.bfloat16, device="cuda"), t.full((2 * n, H), 9.0, device="cuda")
+    gk.gk_paged_attn(gkctx, d.h, gk.GK_BF16, dev(q.reshape(2 * n, w), t.bfloat16), w, y, w, lse, dev(starts([n, n])), 2, H, 2 * n, n, 0.125)
+    with pytest.raises(gk.GkError) as e:
+        gk.gk_sync(gkctx)
+    assert e.value.status == gk.GK_ERR_INDEX
+    check_attention(y.float().cpu().numpy().reshape(q.shape), lse.cpu().numpy(), ref)
