@@ -133,17 +133,19 @@ def _gen(seed):
     return torch.Generator(device="cuda").manual_seed(seed % (1 << 62))
 
 
-_ctx = None
+_contexts = {}
 
 
 def _context():
-    """One context on the current stream, kept as a program keeps it."""
-    global _ctx
+    """The context of the current device and stream, kept as a program keeps it. (A state has the one of the stream that
+    it was prepared on, and its passes run there.)"""
     from gpt_decoder_gb300 import gk
 
-    if _ctx is None:
-        _ctx = gk.Ctx(torch.cuda.current_stream().cuda_stream, workspace_bytes=256 << 20)
-    return _ctx
+    stream = torch.cuda.current_stream()
+    at = stream.device_index, stream.cuda_stream
+    if at not in _contexts:
+        _contexts[at] = gk.Ctx(stream.cuda_stream, workspace_bytes=256 << 20)
+    return _contexts[at]
 
 
 def prepare(case, seed):
