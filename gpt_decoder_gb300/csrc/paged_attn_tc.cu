@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint64_t* bar_o = bars + 22;     // [2] O_g is complete
     uint64_t* bar_drain = bars + 24;
     volatile uint32_t* s_bad = reinterpret_cast<volatile uint32_t*>(bars + 25);  // [4] 16-key groups on refused pages
-    volatile int* s_odd = reinterpret_cast<volatile int*>(bars + 27);
+    volatile int* s_odd = reinterpret_cast<volatile int*>(bars + 27);  // where values were taken out of V first
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 28);
     uint64_t* s_free = bars + 29;    // [2] early S: S_g has been read (one arrival per warp)
     uint64_t* bar_pv = bars + 31;    // [2] early S: P_g V is complete
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         for (int i = 0; i < 4; ++i) mbar_init(&c_full[i], 1);
         mbar_init(bar_drain, 1);
-        *s_odd = 0;
+        *s_odd = 0x7fffffff;
         for (int i = 0; i < 4; ++i) s_bad[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         const int row_bytes = FROM == PAGES8 ? hs : 2 * hs;
         const int clear = it.kv_all - it.n + it.row0 / a.G;  // every row sees the keys up to here
-        bool ok = true, bad_page = false, odd = false;
+        bool ok = true, bad_page = false, odd = false, odd_tile = false;
         int ids = 0;  // lane i < 8: the page of keys 16 i .. of the tile
         bool bad = false;
         auto look_up = [&](int j) {
@@ -380,9 +380,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         if constexpr (FROM != PAGES8) {
             // Warp 8 sends for the tiles: whole boxes of a page's rows (EXPANDED: the tile's 128 rows) by TMA.
             // Tiles of V that hold keys some row must not see, or past the end, or on refused pages, it copies
-            // itself: what is not there becomes zeros, and so does what is not finite of keys that some row must
-            // not see (put back at the end for the rows that see it). Keys up to `clear` stay as they are.
-            // EXPANDED tiles are finite, and zeros past the end.
+            // itself: what is not finite or not there becomes zeros (and is put back at the end for the rows that see
+            // it, from the first key on of the first tile that lost any). EXPANDED tiles are finite, and zeros past the
+            // end. (Chunks of 1000 take 85.2 us so, 86.7 with only the keys cleared that some row must not see.)
             const int box = FROM == EXPANDED ? KT : min(KT, 1 << a.p.page_log2);
             int64_t base_row = 0;  // EXPANDED: this head's first row
             if constexpr (FROM == EXPANDED) {
@@ -428,11 +428,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                             const int r = i / L::HALVES * 4 + lane / 8, c = (i % L::HALVES) * 8 + lane % 8;
                             uint4 x = make_uint4(0, 0, 0, 0);
                             if (!none && grp * 16 + r < left && c * 8 < hs) x = __ldg(reinterpret_cast<const uint4*>(src + r * row_bytes + c * 16));
-                            if (it.k_begin + j * KT + grp * 16 + r > clear) odd |= drop_odd2(x.x) | drop_odd2(x.y) | drop_odd2(x.z) | drop_odd2(x.w);
+                            odd |= drop_odd2(x.x) | drop_odd2(x.y) | drop_odd2(x.z) | drop_odd2(x.w);
                             *reinterpret_cast<uint4*>(tile + (c >> 3) * HALF + swizzled(grp * 16 + r, c & 7)) = x;
                         }
                     }
-                    if (odd) *s_odd = 1;
+                    if (!odd_tile && __any_sync(0xffffffffu, odd)) {
+                        odd_tile = true;
+                        if (lane == 0) *s_odd = it.k_begin + j * KT;
+                    }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&v_full[stage]);
@@ -653,7 +656,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!failed) {
             const int64_t out = (int64_t)(it.s0 + query) * a.H + h;
             const float inv = a.splits > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
-            const int odd_from = !Q8 && *s_odd ? max(it.k_begin, it.kv_all - it.n + it.row0 / a.G + 1) : 0x7fffffff;
+            const int odd_from = Q8 ? 0x7fffffff : *s_odd;
 #pragma unroll
             for (int c = 0; c < HSP / 32; ++c) {
                 uint32_t ov[32];
@@ -665,7 +668,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (mine) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) ov[i] = my_kt > 0 && l != 0.f ? __float_as_uint(__uint_as_float(ov[i]) * inv) : 0u;
-                for (int j = odd_from; j <= last; ++j) {  // rare: infinities and NaN that were taken out of V, where they are seen
+                // rare: infinities and NaN that were taken out of V, where they are seen (twice in tiles that kept theirs)
+                for (int j = odd_from; j <= last; ++j) {
                     const int id = a.p.table[it.b * a.p.ld_table + (j >> a.p.page_log2)];
                     if (id < 0 || id >= a.p.n_pages) continue;
                     const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.p.v) +
