@@ -24,10 +24,11 @@
 // the score, the value's scale the weight.
 // Weights are split into two bf16 parts (hi + lo: 16 significant bits), so the result carries no
 // rounding but the output's.
-// Measured: 48 sequences of up to 8191 keys, 32 query heads over 8 of 128, one token each: bf16 pages 113 us, 5.4
-// TB/s of the cache's bytes (0.80 of a copy); 8-bit ones 88 us, 3.6 TB/s, bound by the instructions that
-// unpack codes (four a pair) and 12 warps an SM to cover the loads' latency. One token over 777 keys of 12 heads: 5.6 us
-// from the host.
+// Measured: 48 sequences of up to 8191 keys, 32 query heads over 8 of 128, one token each: bf16 pages 111 us, 5.5
+// TB/s of the cache's bytes (0.82 of a copy); 8-bit ones 87 us, 3.6 TB/s (0.53): no pipe is full (ALU 43%, issue
+// 41%, DRAM 49%), the 12 warps an SM that the registers leave do not cover the loads' latency beside unpacking
+// (four instructions a pair of codes). One token over 777 keys of 12 heads: 5.3 us from the host; 8.1 where the
+// table has room for 131072 positions, as the pieces then go by that and are joined by a second launch.
 #include <math.h>
 
 #include <algorithm>

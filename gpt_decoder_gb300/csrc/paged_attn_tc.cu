@@ -7,8 +7,10 @@
 // walks the keys in tiles of 128:
 //   S = Q K^T   (M = 128 rows, N = 128 keys, K = head size) into tensor memory;
 //   softmax     a thread per row: P = 2^(s - m) with s in powers of two, as bf16 over S in tensor
-//               memory; the reference m moves (and O is rescaled there) only when the row's maximum
-//               passes it by more than 8;
+//               memory (an operand of the product has 16 bits; 2^-8 of a weight at most, as y's own
+//               rounding, where a second part would double the products; sums of weights stay float32);
+//               the reference m moves (and O is rescaled there) only when the row's maximum passes it
+//               by more than 8;
 //   O += P V    (N = head size, K = 128 keys), accumulated in tensor memory.
 // Head sizes up to 64 leave room there for P beside S: the next S is computed as soon as the scores of
 // this one have been read, under the softmax. With 128 P lies over S, and the next S waits for P V.
@@ -22,11 +24,11 @@
 // Registers: 512 threads at 128; the softmax warpgroups take 184 each, the copying one 96, the MMA warp's
 // 48 (where the copying one unpacks codes: 176, 104, 48).
 // All mbarrier waits are bounded (timeout -> GK_ERR_TIMEOUT in the error word).
-// Measured: two chunks of up to 2048 tokens behind 16384 keys, 32 heads over 8 of 128: bf16 pages 487 us, 1.08
-// PFLOP/s (0.56 of a dense product); 8-bit ones 670 us with the pass that expands them: the softmax warps
-// bound both, by a thread's 128 exponentials, maxima and packing a tile, for 8 bits by two more products a score.
-// Three chunks of up to 1000 over 8100 keys, 12 heads of 64: 84 us (half the products a tile for the same
-// softmax). Key tiles that two groups of blocks read side by side come from L2.
+// Measured: two chunks of up to 2048 tokens behind 16384 keys, 32 heads over 8 of 128: bf16 pages 494 us, 1.07
+// PFLOP/s (0.55 of a dense product); 8-bit ones 670 us with the pass that expands them (1980 unpacked on the way):
+// the softmax warps bound both, by a thread's 128 exponentials, maxima and packing a tile, for 8 bits by two more
+// products a score. Three chunks of up to 1000 over 8100 keys, 12 heads of 64: 85 us (half the products a tile for
+// the same softmax). Key tiles that two groups of blocks read side by side come from L2.
 #include <algorithm>
 #include <type_traits>
 

@@ -8,8 +8,9 @@
 // row's sequence and page are looked up once by a warp, then all the block's threads go through
 // the rows' 2 Hkv vectors.
 // Measured: reading back 16 sequences of up to 16384 8-bit tokens of 8 heads of 128 as bf16 111 us, 6.2 TB/s
-// (0.91 of a copy); storing 7 chunks of up to 4096 of them and reading those back 39 us, 4.0 TB/s: two launches, each
-// of a few waves. A few rows cost their launches: 4 us to read 333 rows.
+// (0.91 of a copy), of bf16 pages 136 us, 6.7 TB/s (0.99); storing 7 chunks of up to 4096 of them 22.6 us, 4.2 TB/s
+// (0.62; issue 69%: the quantiser's instructions in less than two waves of blocks), reading those back 19.1, 5.0 TB/s
+// (0.74), of bf16 pages 23.5 (0.79) and 22.0 (0.84). A few rows cost their launches: 4 us to read 333 rows.
 #include "paged.cuh"
 
 namespace gk {

@@ -21,9 +21,10 @@
 //   2^-z = 2^-n T (1 + e), T = 2^(-i / 512) from a table (in units of 2^-48, and as a pair), and
 //   e = -g + g^2/2 - g^3/6 + g^4/24, g = f ln 2, its first term as a pair;
 // T e goes to units of 2^-48 in two steps of 32 bits. Off by at most 1.6 x 2^-45 in all.
-// Measured: 192 rows of 50257 float32 with filters of every kind 85 us (0.45 TB/s: the histograms' shared-memory
-// atomics and the exponentials bound it, and a chain of about ten barriers of the cluster a row); one row 14 us,
-// the chain alone.
+// Measured: 192 rows of 50257 float32 with filters of every kind 91 us (0.42 TB/s: the histograms' shared-memory
+// atomics, the exponentials, and waits at barriers: a block's slice is a power of two, so that of four blocks the
+// last holds 1105 of 50257 logits and waits for the others); one row with top-k 13.5 us, two walks over the slice
+// with four barriers of the cluster and about a dozen of the block between them.
 #include <math.h>
 
 #include "launch.cuh"
@@ -652,7 +653,7 @@ extern "C" gk_status gk_sample_rows(gk_ctx* ctx, int dtype, const void* logits, 
     if (rows == 0) return GK_OK;
     SampleArgs a{logits, ld, V, 1, 0, u, temperature, top_k, top_p, min_p, next, prob};
     // blocks per row: as many as the GPU takes at once, while each still has 8 elements a thread; and enough that a
-    // thread has at most 32 (98 KB of shared memory, two blocks an SM), or 64 for the largest rows. (Rows of 50257
+    // thread has at most 32 (113 KB of shared memory, two blocks an SM), or 64 for the largest rows. (Rows of 50257
     // in 2 / 4 / 8 blocks, top-k: one 23 / 17 / 14 us, 32 25 / 18 / 18, 64 25 / 22 / 33; mixed filters: 32 39 / 25 / 22,
     // 64 71 / 52 / 50, 192 105 / 86 / 110.)
     while (a.cluster < MAX_CLUSTER && (V > a.cluster * (THREADS * 32) ||

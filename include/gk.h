@@ -407,7 +407,7 @@ gk_status gk_sample(gk_ctx* ctx, gk_kv* kv, const float* logits, int64_t ld, int
  *              is row p % page_size of page page_table[b][p / page_size].
  *   kv_len     device int32 [B]: tokens of each sequence, those of the current call included.
  * page_size is 16, 32, 64, 128 or 256; hs a multiple of 16, 16 .. 128; n_pages * Hkv * page_size and
- * max_pages * page_size below 2^31 and 2^30.
+ * max_pages * page_size below 2^31 and 2^30; B up to 65535.
  *
  * The three gk_paged_* calls below take `rows` token rows of B sequences packed one after the
  * other: sequence b has rows q_start[b] .. q_start[b+1]-1 (device int32 [B+1], ascending from 0;
@@ -417,8 +417,9 @@ gk_status gk_sample(gk_ctx* ctx, gk_kv* kv, const float* logits, int64_t ld, int
  * rows there are left as they were. What cannot be true on the device is refused there: a
  * position at or past max_pages * page_size, or a page id outside [0, n_pages), is never followed;
  * it records GK_ERR_INDEX (gk_sync), a token there is not stored, reads back as zeros, and
- * counts as not visible to attention. Pages that one call writes must not be shared by two of
- * its sequences at the same position (the order of the two stores would be open).
+ * counts as not visible to attention. Two tokens that one call writes must not lie at the same row
+ * of a page, be it of two sequences or of one whose table names a page twice (the order of the two
+ * stores would be open).
  * Every call needs the context's device to be current (GK_ERR_ARG). No call is affected by what
  * the cache holds outside the positions that it names. */
 typedef struct {
@@ -454,19 +455,28 @@ gk_status gk_paged_read(gk_ctx* ctx, const gk_paged_kv* cache, int dtype, void* 
  * key / value head h / (H / Hkv) (H a multiple of Hkv):
  *   y[i, h] = sum_{j <= p} softmax_j(scale q[i, h] . k[j]) v[j].
  *   dtype   GK_BF16 (GK_ERR_UNSUPPORTED otherwise): q and y, bf16 [rows, H*hs] with row strides ldq,
- *           ldy (multiples of 8, 16-byte aligned). Scores, softmax and sums are float32.
+ *           ldy (multiples of 8, 16-byte aligned). Scores, softmax and sums are float32. The weights
+ *           meet the values as 16 significant bits (two bf16 parts) where max_q * H / Hkv is at most
+ *           64 (8-bit pages) or 32 (bf16), and rounded to bf16 (2^-8 relative at most, as y itself
+ *           is) above that. The weighted sum of values is divided at the end, so it has to be below
+ *           2^127 before that.
  *   lse     float32 [rows, H] or NULL: the natural log-sum-exp of the scaled scores.
  *   max_q   at least every sequence's number of rows (host; it sizes the launch). A sequence with
  *           more rows than max_q, or with rows past `rows`, records GK_ERR_INDEX and its rows
  *           are left as they were.
  *   scale   positive, at most 2^127 (it is taken times log2(e): GK_ERR_ARG where that is not finite).
- * A row that sees nothing (a negative position) gets y = 0 and lse = -inf. Keys and values that a
- * row does not see never reach it, whatever they hold (infinities and NaN among it). y must not
+ * A row that sees nothing (a negative position) gets y = 0 and lse = -inf, and so does one whose
+ * scores are all -inf while its values are finite. Keys and values that a row does not see never
+ * reach it, whatever they hold (infinities and NaN among it). Where a value that a row sees with a
+ * score above -inf is not finite, neither is y (however small the weight; an infinity may come out
+ * as NaN); a NaN among the scores makes y and lse NaN. y must not
  * overlap q, and max_q * H / Hkv stays below 2^30 (GK_ERR_UNSUPPORTED). Long
  * sequences are split over the GPU and joined through the context's workspace: the more of it
- * there is the more they split, and any size will do. (Calls of one context are ordered on its stream;
- * graphs captured from one context share its workspace, so replay them one after the other, or
- * capture each from a context of its own.) */
+ * there is the more they split, and any size will do. Chunks over 8-bit pages are fastest where it
+ * also has room for the codes of every sequence as bf16: 4 * B * max_pages * page_size * Hkv * hs
+ * bytes (by the table's width, as the lengths are on the device; max_pages * page_size rounded up to
+ * 128). (Calls of one context are ordered on its stream; graphs captured from one context share its
+ * workspace, so replay them one after the other, or capture each from a context of its own.) */
 gk_status gk_paged_attn(gk_ctx* ctx, const gk_paged_kv* cache, int dtype, const void* q, int64_t ldq,
                         void* y, int64_t ldy, float* lse, const int32_t* q_start, int B, int H,
                         int64_t rows, int max_q, float scale);
