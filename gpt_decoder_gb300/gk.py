@@ -109,6 +109,10 @@ _SIGS = {
     "gk_paged_write": (I32, [P, ct.POINTER(gk_paged_kv), I32, P, I64, P, I64, P, I32, I64]),
     "gk_paged_read": (I32, [P, ct.POINTER(gk_paged_kv), I32, P, I64, P, I64, P, I32, I64]),
     "gk_paged_attn": (I32, [P, ct.POINTER(gk_paged_kv), I32, P, I64, P, I64, P, P, I32, I32, I64, I32, F32]),
+    "gk_paged_attn_shared": (I32, [P, ct.POINTER(gk_paged_kv), I32, P, I64, P, I64, P, P, I32, P, P, I32, I32, I64, I32, I32,
+                                   F32]),
+    "gk_paged_mass": (I32, [P, ct.POINTER(gk_paged_kv), I32, P, I64, P, P, F32, P, P, P, I32, I32, I64, I32, F32]),
+    "gk_paged_evict": (I32, [P, ct.POINTER(gk_paged_kv), P, ct.POINTER(gk_paged_kv), P, P, I32, I32, P, P, I32]),
     "gk_quant_w4": (I32, [P, P, I64, I32, P, P, I32, I64, I64]),
     "gk_matvec_w4": (I32, [P, I32, P, I64, P, P, I32, P, P, I64, P, I64, I32, I64, I64, I64]),
     "gk_sample_rows": (I32, [P, I32, P, I64, I64, I32, P, P, P, P, P, P, P]),
@@ -470,6 +474,25 @@ def gk_paged_read(ctx, cache, dtype, k, ldk, v, ldv, q_start, B, rows):
 def gk_paged_attn(ctx, cache, dtype, q, ldq, y, ldy, lse, q_start, B, H, rows, max_q, scale):
     return _check(ctx, _lib.gk_paged_attn(ctx.handle, _batch(cache, B, "gk_paged_attn"), dtype, _p(q), ldq, _p(y),
                                           ldy, _p(lse), _p(q_start), B, H, rows, max_q, scale), "gk_paged_attn")
+
+
+def gk_paged_attn_shared(ctx, cache, dtype, q, ldq, y, ldy, lse, q_start, B, group_start, prefix_len, n_groups, H, rows,
+                         max_q, max_group_q, scale):
+    return _check(ctx, _lib.gk_paged_attn_shared(ctx.handle, _batch(cache, B, "gk_paged_attn_shared"), dtype, _p(q), ldq,
+                                                 _p(y), ldy, _p(lse), _p(q_start), B, _p(group_start), _p(prefix_len),
+                                                 n_groups, H, rows, max_q, max_group_q, scale), "gk_paged_attn_shared")
+
+
+def gk_paged_mass(ctx, cache, dtype, q, ldq, lse, old, decay, mass, first, q_start, B, H, rows, max_q, scale):
+    return _check(ctx, _lib.gk_paged_mass(ctx.handle, _batch(cache, B, "gk_paged_mass"), dtype, _p(q), ldq, _p(lse),
+                                          _p(old), decay, _p(mass), _p(first), _p(q_start), B, H, rows, max_q, scale),
+                  "gk_paged_mass")
+
+
+def gk_paged_evict(ctx, cache, mass, to, to_mass, first, budget, recent, new_len, kept, B):
+    return _check(ctx, _lib.gk_paged_evict(ctx.handle, _batch(cache, B, "gk_paged_evict"), _p(mass),
+                                           _batch(to, B, "gk_paged_evict"), _p(to_mass), _p(first), budget, recent,
+                                           _p(new_len), _p(kept), B), "gk_paged_evict")
 
 
 def gk_quant_w4(ctx, W, ldw, transW, Wq, scales, group, K, M):

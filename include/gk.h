@@ -409,7 +409,7 @@ gk_status gk_sample(gk_ctx* ctx, gk_kv* kv, const float* logits, int64_t ld, int
  * page_size is 16, 32, 64, 128 or 256; hs a multiple of 16, 16 .. 128; n_pages * Hkv * page_size and
  * max_pages * page_size below 2^31 and 2^30; B up to 65535.
  *
- * The three gk_paged_* calls below take `rows` token rows of B sequences packed one after the
+ * The gk_paged_* calls below (but gk_paged_evict) take `rows` token rows of B sequences packed one after the
  * other: sequence b has rows q_start[b] .. q_start[b+1]-1 (device int32 [B+1], ascending from 0;
  * a sequence may have none), and row i of its n sits at position kv_len[b] - n + i: the rows are
  * the sequence's last n tokens. A position below zero is padding (a padded batch's dead row has
@@ -480,6 +480,67 @@ gk_status gk_paged_read(gk_ctx* ctx, const gk_paged_kv* cache, int dtype, void* 
 gk_status gk_paged_attn(gk_ctx* ctx, const gk_paged_kv* cache, int dtype, const void* q, int64_t ldq,
                         void* y, int64_t ldy, float* lse, const int32_t* q_start, int B, int H,
                         int64_t rows, int max_q, float scale);
+
+/* The same attention (the arguments of gk_paged_attn, and its result) of a batch whose sequences share prefixes: many
+ * continuations of one prompt, questions behind one document. Sequences group_start[g] .. group_start[g+1]-1 (device
+ * int32 [n_groups+1], ascending from 0) hold the same first prefix_len[g] positions (device int32 [n_groups]): a
+ * group's prefix is read once for all of its rows, and then each sequence's own positions.
+ *   The row of page_table of every sequence that shares a prefix names its pages, as gk_paged_attn needs it, and so does
+ *   the row of the group's first sequence, be it a padding row. (A page in which the prefix ends may be each
+ *   sequence's own, with a copy of its tokens.) Which of these rows the prefix is looked up in is open. A sequence that
+ *   is in no group shares nothing, and neither does one whose new rows do not all lie behind the prefix (kv_len[b] - n <
+ *   prefix_len[g], padding rows among them): its keys are read for it alone.
+ *   n_groups    1 .. 65535.
+ *   max_group_q at least every group's number of rows (host, as max_q). A group with more, or with sequences past B,
+ *               records GK_ERR_INDEX and its rows are left as they were; so does a prefix_len past the table, the part
+ *               of it that is there being attended.
+ * Infinities, NaN and refused pages are as with gk_paged_attn. Uses the context's workspace for the parts of a row's
+ * keys, (hs * 4 + 8) * H bytes a row and part, two parts at least; where it has no room for them, or the batch has few
+ * rows, the call computes gk_paged_attn (and does not look at the groups). */
+gk_status gk_paged_attn_shared(gk_ctx* ctx, const gk_paged_kv* cache, int dtype, const void* q, int64_t ldq,
+                               void* y, int64_t ldy, float* lse, const int32_t* q_start, int B,
+                               const int32_t* group_start, const int32_t* prefix_len, int n_groups, int H,
+                               int64_t rows, int max_q, int max_group_q, float scale);
+
+/* The attention weight that each cached token receives from the call's rows: with q, lse (float32 [rows, H]), q_start,
+ * scale as gk_paged_attn takes and leaves them, for key / value head hk and every position j >= first[b] of a
+ * sequence with rows in the call
+ *   mass[j, hk] = decay * old[j, hk] + sum_{rows i that see j} sum_{heads h of hk} exp(scale q[i, h] . k[j] - lse[i, h]),
+ * without the first term for the call's own tokens (the sequence's last n positions) or where old is NULL.
+ *   old, mass  float32 [n_pages][Hkv][page_size] (16-byte aligned), the value of the token in that row of the page; the same array
+ *              or two that do not overlap. mass is changed at the positions named alone.
+ *   decay      finite, not negative: 1 adds up, less than 1 forgets.
+ *   first      device int32 [B] or NULL (0): positions below it are not weighed (a prefix that other sequences hold
+ *              too). Two sequences of a call must not hold one row of a page at positions that are.
+ *   dtype      GK_BF16 (q); else GK_ERR_UNSUPPORTED. max_q as for gk_paged_attn.
+ * A row with lse = -inf gives no weight. Keys that a row does not see never reach its weights; a NaN among the
+ * score and lse makes the mass of that key NaN. The sum's order is fixed: the same call gives the same bits. Only keys
+ * are read (cache->v is not). */
+gk_status gk_paged_mass(gk_ctx* ctx, const gk_paged_kv* cache, int dtype, const void* q, int64_t ldq, const float* lse,
+                        const float* old, float decay, float* mass, const int32_t* first, const int32_t* q_start,
+                        int B, int H, int64_t rows, int max_q, float scale);
+
+/* Cut sequences to a budget by the mass of their tokens. Per sequence b of kv_len[b] tokens and per key / value head,
+ * the first first[b] tokens stay, the last `recent`, and of those between the heaviest (ties: the lowest position), so
+ * that `budget` are left behind the first ones; all of them where there are no more. They move, in their order, to
+ * positions 0 .. of row b of to->page_table, with their scales and mass:
+ *   new_len[b] = min(kv_len[b], first[b] + budget);  kept[b][hk][i] = the old position of the token at new position
+ *   first[b] + i, -1 behind the last.
+ * The tokens of one position differ by head afterwards; attention needs no more than their order.
+ *   cache, mass  the sequences (kv_len read from the device) and their tokens' mass, as for gk_paged_mass. A NaN
+ *                counts as the least.
+ *   to, to_mass  where they go: dtype, Hkv, page_size and hs as of cache; other pages of the same arrays (with mass ==
+ *                to_mass), or other arrays. to->kv_len is not read, and may be new_len. Rows behind a sequence's new
+ *                length are left as they were.
+ *   first        device int32 [B] or NULL (0); held to 0 .. kv_len[b].
+ *   budget       1 .. 2^30; recent 0 .. budget.
+ *   new_len      device int32 [B];  kept  device int32 [B][Hkv][budget]. new_len must not overlap cache->kv_len.
+ * A page that is written must not be one that the call reads. The same page may stand in both tables only at the same
+ * place, where all its positions are below first[b], or in sequences that keep all their tokens: what stays in its row
+ * is not moved. A position without a page that exists records GK_ERR_INDEX: in cache its mass counts as the least (and if
+ * it stays, zeros go to its new place); in `to` nothing is stored there. */
+gk_status gk_paged_evict(gk_ctx* ctx, const gk_paged_kv* cache, const float* mass, const gk_paged_kv* to, float* to_mass,
+                         const int32_t* first, int budget, int recent, int32_t* new_len, int32_t* kept, int B);
 
 /* ------------------------------------------------------------- serving: 4-bit weights */
 

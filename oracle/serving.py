@@ -1,4 +1,5 @@
-"""Oracle of the serving operators: the paged cache, attention over it, 4-bit products, filtered sampling.
+"""Oracle of the serving operators: the paged cache, attention over it, its tokens' weights and eviction, 4-bit products,
+filtered sampling.
 
 TEST INFRASTRUCTURE ONLY (see the package docstring): never imported by the product path.
 
@@ -121,6 +122,80 @@ def paged_attn(c, q, q_start, scale):
                     spread[s0 + i, h] = w @ np.abs(v[:m, h // G]) / l
                     lse[s0 + i, h] = t + np.log(l)
     return y, lse, spread
+
+
+class SharedPages(Pages):
+    """The cache as attention over shared prefixes reads it: groups (first sequence, end, prefix). The first `prefix`
+    positions of a group's sequences are looked up in the first one's row of the table, where all n new rows lie
+    behind them. Shares the arrays of `c`."""
+
+    def __init__(self, c, groups, q_start):
+        self.__dict__.update(c.__dict__)
+        self.lead = {}
+        for first, end, prefix in groups:
+            prefix = min(max(prefix, 0), c.table.shape[1] * c.page)
+            for b in range(first, end):
+                n = int(q_start[b + 1]) - int(q_start[b])
+                if int(c.kv_len[b]) - n >= prefix:
+                    self.lead[b] = first, prefix
+
+    def place(self, b, pos):
+        lead, prefix = self.lead.get(b, (b, 0))
+        return super().place(lead if pos < prefix else b, pos)
+
+
+def paged_mass(c, q, lse, q_start, scale, old=None, decay=1.0, first=None):
+    """{(page, head, row): (mass, size)} of every position weighed: q [rows, H, hs], lse [rows, H]; size is the sum of the
+    terms' own error scales, decay old + sum w (1 + |score| + |lse|)."""
+    H, out = q.shape[1], {}
+    G = H // c.Hkv
+    for b in range(len(q_start) - 1):
+        s0, n, kv = int(q_start[b]), int(q_start[b + 1]) - int(q_start[b]), int(c.kv_len[b])
+        if n <= 0:
+            continue
+        for j in range(0 if first is None else min(max(int(first[b]), 0), max(kv, 0)), kv):
+            at = c.place(b, j)
+            if at is None:
+                continue
+            k = c.vector("k", *at)
+            i0 = max(0, j - (kv - n))
+            for hk in range(c.Hkv):
+                with np.errstate(all="ignore"):
+                    z = scale * (q[s0 + i0 : s0 + n, hk * G : (hk + 1) * G].astype(np.float64) @ k[hk])
+                    l = lse[s0 + i0 : s0 + n, hk * G : (hk + 1) * G].astype(np.float64)
+                    w = np.where(np.isneginf(l), 0.0, np.exp(z - l))
+                    size = np.where(w == 0, 0, w * (1 + np.abs(z) + np.abs(l)))
+                before = 0.0 if old is None or j >= kv - n else float(np.float32(decay)) * float(old[at[0], hk, at[1]])
+                out[at[0], hk, at[1]] = before + w.sum(), np.abs(before) + size.sum()
+    return out
+
+
+def paged_evict(c, mass, to, to_mass, first, budget, recent):
+    """(new_len, kept); the kept tokens into `to` (Pages over its own arrays and table) and to_mass, in place."""
+    B = len(c.kv_len)
+    new_len, kept = np.zeros(B, np.int32), np.full((B, c.Hkv, budget), -1, np.int32)
+    for b in range(B):
+        kv = min(max(int(c.kv_len[b]), 0), c.table.shape[1] * c.page)
+        f = 0 if first is None else min(max(int(first[b]), 0), kv)
+        new_len[b] = f + min(kv - f, budget)
+        for hk in range(c.Hkv):
+            stay = list(range(f, kv))
+            if kv - f > budget:
+                def key(j):
+                    at = c.place(b, j)
+                    m = -np.inf if at is None else float(mass[at[0], hk, at[1]])
+                    return -np.inf if np.isnan(m) else m
+                heavy = sorted(range(f, kv - recent), key=lambda j: (-key(j), j))[: budget - recent]
+                stay = sorted(heavy) + list(range(kv - recent, kv))
+            kept[b, hk, : len(stay)] = stay
+            for i, j in enumerate(list(range(f)) + stay):
+                src, dst = c.place(b, j), to.place(b, i)
+                if dst is None or (to.k is c.k and dst == src):
+                    continue
+                for x, y in ((c.k, to.k), (c.v, to.v), (c.k_scale, to.k_scale), (c.v_scale, to.v_scale), (mass, to_mass)):
+                    if x is not None:
+                        y[dst[0], hk, dst[1]] = 0 if src is None else x[src[0], hk, src[1]]
+    return new_len, kept
 
 
 # -------------------------------------------------------------------------------- 4-bit weights
