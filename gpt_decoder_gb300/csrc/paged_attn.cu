@@ -34,25 +34,13 @@
 #include <algorithm>
 
 #include "paged_attn.cuh"
+#include "paged_mma.cuh"
 
 namespace gk {
 namespace {
 
 constexpr int WARPS = 4;
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// D += A B, bf16 operands, float32 accumulators: A 16x16, B 16x8.
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 // Transpose an 8x8 matrix of 16-bit elements held one row per four lanes.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
@@ -62,12 +50,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&t);
-}
-// The codes in bytes 0 and 2 of x as a pair of bf16.
-__device__ __forceinline__ uint32_t codes02(const CodeMasks& k, uint32_t x) {
-    const uint32_t a = and_or(x, k.low7, k.bf16_128), b = and_or(x, k.sign, k.bf16_128);
-    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&d);
 }
 // Zero the infinities and NaN of a bf16 pair; true if there were any.
 __device__ __forceinline__ bool drop_odd(uint32_t& x) {

@@ -33,6 +33,7 @@
 #include <type_traits>
 
 #include "paged_attn.cuh"
+#include "paged_mma.cuh"
 #include "tcgen05.cuh"
 
 namespace gk {
@@ -53,19 +54,9 @@ struct Layout {
     static constexpr uint32_t BYTES = BARS + 512 + 1024;
 };
 
-// Byte offset of the 16 bytes at chunk c (of 8) of row r in a 128-byte-swizzled half tile.
-__device__ __forceinline__ uint32_t swizzled(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
-
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&t);
-}
-// Codes 0 and 1 (or 2 and 3) of a word as a pair of bf16: 128 + the low seven bits, less 128 or 256.
-__device__ __forceinline__ uint32_t codes_pair(const CodeMasks& k, uint32_t w, int second) {
-    const uint32_t x = __byte_perm(w, 0, second ? 0x4342 : 0x4140);
-    const uint32_t a = and_or(x, k.low7, k.bf16_128), b = and_or(x, k.sign, k.bf16_128);
-    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&d);
 }
 __device__ __forceinline__ bool drop_odd2(uint32_t& x) {  // infinities and NaN of a bf16 pair become zeros
     const bool lo = (x & 0x7f80u) == 0x7f80u, hi = (x & 0x7f800000u) == 0x7f800000u;
@@ -92,25 +83,6 @@ __device__ __forceinline__ void mul2(uint32_t& x, uint32_t& y, float a, float b)
         : "f"(a), "f"(b));
 }
 
-__device__ __forceinline__ uint32_t test_phase(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(saddr(bar)), "r"(parity)
-        : "memory");
-    return ok;
-}
-// Wait for a phase: polled at first (try_wait suspends the thread, and its wake-up takes longer than most
-// of the waits here), then bounded by the clock.
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint64_t limit) {
-#pragma unroll 1
-    for (int i = 0; i < 4096; ++i)
-        if (test_phase(bar, parity)) return true;
-    return mbar_wait(bar, parity, nullptr, limit);
-}
 // Several at once: even a test of a completed phase takes hundreds of cycles behind the softmax warps' traffic
 // with the tensor memory, so the tests are sent together. (b and c only where asked.)
 __device__ __forceinline__ bool wait_phases(uint64_t* a, uint32_t pa, bool has_b, uint64_t* b, uint32_t pb, bool has_c, uint64_t* c,

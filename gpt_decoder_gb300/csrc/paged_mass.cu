@@ -3,15 +3,27 @@
 // a KV cache" (the new tokens' queries against every cached position, no mask but the order).
 //
 // mass_j = sum over rows i that see j of 2^(s_ij - l_i), s = scale log2(e) q k, l = lse log2(e): with the rows' log sums
-// known a key needs nothing of the other keys. A warp takes a key and walks the rows, four dims a lane.
+// known a key needs nothing of the other keys, and nothing is joined. Both kernels compute the scores transposed,
+// S^T = K Q^T, so that a key's sum stays with the thread (or the four lanes) that holds its row.
+//   Few rows: a warp takes tiles of 16 keys straight from the cache into the registers of mma.sync m16n8k16 (as the
+//   attention of few rows does), its rows eight at a time from shared memory, which holds them in operand order.
+//   Tiles: a block holds 256 keys in shared memory (8-bit codes as bf16, once) and walks the rows in tiles of 128,
+//   which TMA brings (a box of whole queries of the heads that share the keys); D = K Q^T (tcgen05, M = 128 keys, N =
+//   128 rows) into tensor memory, two buffers for each half of the keys; eight warps, a thread a key, read the row of
+//   scores and add its weights. A key's scale is its thread's, and a row's log sum a broadcast from shared memory.
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "paged.cuh"
+#include "paged_mma.cuh"
+#include "tcgen05.cuh"
 
 namespace gk {
 namespace {
+
+using namespace tc;
 
 struct MassArgs {
     Pages p;
@@ -24,51 +36,453 @@ struct MassArgs {
     const int32_t* first;  // may be null
     const int32_t* q_start;
     int B, H, G, rows, max_q;
+    int tile_heads, tile_queries;  // a tile of rows: this many heads of this many queries, 128 at most
     int* err;
+    CodeMasks masks;
 };
 
-constexpr int WARPS = 8;
-
-__global__ void __launch_bounds__(WARPS * 32) mass_kernel(const MassArgs a) {
-    wait_for_earlier_kernels();
-    const int b = blockIdx.z, hk = blockIdx.y, lane = threadIdx.x & 31, hs = a.p.hs;
-    const int s0 = a.q_start[b], s1 = a.q_start[b + 1], n = s1 - s0;
-    if (n <= 0) return;
-    if (n > a.max_q || s0 < 0 || s1 > a.rows) {
+// The sequence that a block works on.
+struct Span {
+    int s0, n, kv_all, kv, first;
+};
+__device__ __forceinline__ bool span_of(const MassArgs& a, int b, Span& s) {
+    s.s0 = a.q_start[b];
+    const int s1 = a.q_start[b + 1];
+    s.n = s1 - s.s0;
+    if (s.n <= 0) return false;
+    if (s.n > a.max_q || s.s0 < 0 || s1 > a.rows) {
         if (threadIdx.x == 0) report(a.err, GK_ERR_INDEX);
-        return;
+        return false;
     }
-    const int kv_all = max(a.p.kv_len[b], 0), kv = min(kv_all, a.p.capacity);
-    if (kv_all > a.p.capacity && threadIdx.x == 0) report(a.err, GK_ERR_INDEX);
-    const int first = a.first ? min(max(a.first[b], 0), kv) : 0;
-    for (int j = first + blockIdx.x * WARPS + (threadIdx.x >> 5); j < kv; j += gridDim.x * WARPS) {
-        const int id = __ldg(a.p.table + b * a.p.ld_table + (j >> a.p.page_log2));
-        if (id < 0 || id >= a.p.n_pages) {
-            if (lane == 0) report(a.err, GK_ERR_INDEX);
-            continue;
+    s.kv_all = max(a.p.kv_len[b], 0);
+    s.kv = min(s.kv_all, a.p.capacity);
+    if (s.kv_all > a.p.capacity && threadIdx.x == 0) report(a.err, GK_ERR_INDEX);
+    s.first = a.first ? min(max(a.first[b], 0), s.kv) : 0;
+    return s.first < s.kv;
+}
+
+// ------------------------------------------------------------------------------------- few rows
+constexpr int WARPS = 4;
+
+// HSP: head size rounded up to 64 or 128 (the rest reads as zeros). NT: tiles of 8 rows.
+template <int HSP, bool Q8, int NT>
+__global__ void __launch_bounds__(WARPS * 32) mass_few_kernel(const MassArgs a) {
+    constexpr int KC = Q8 ? HSP / 64 : HSP / 32;  // 16-byte pieces of a K row per thread
+    __shared__ uint2 s_q[NT][HSP / 16][32];       // B operands, in the order of the K registers
+    __shared__ float2 s_l[NT][4];                 // columns 2t, 2t + 1: log sums, in powers of two
+    __shared__ int2 s_last[NT][4];                // and the last positions that they see
+    wait_for_earlier_kernels();
+    const int b = blockIdx.z, hk = blockIdx.y, hs = a.p.hs;
+    Span s;
+    if (!span_of(a, b, s)) return;
+    const int tile0 = s.first >> 4, tiles = ((s.kv + 15) >> 4) - tile0;
+    if ((int)blockIdx.x * WARPS >= tiles) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int R = s.n * a.G;
+
+    for (int x = warp; x < NT * (HSP / 32); x += WARPS) {  // eight rows' 32 dims
+        const int nt = x / (HSP / 32), c = x - nt * (HSP / 32), i = nt * 8 + g;
+        const int d = Q8 ? ((c >> 1) * 4 + t) * 16 + (c & 1) * 8 : (c * 4 + t) * 8;
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (i < R && d < hs)
+            u = *reinterpret_cast<const uint4*>(a.q + (int64_t)(s.s0 + i / a.G) * a.ldq + (hk * a.G + i % a.G) * hs + d);
+        if (Q8) {
+            s_q[nt][2 * c][lane] = make_uint2(__byte_perm(u.x, u.y, 0x5410), __byte_perm(u.x, u.y, 0x7632));
+            s_q[nt][2 * c + 1][lane] = make_uint2(__byte_perm(u.z, u.w, 0x5410), __byte_perm(u.z, u.w, 0x7632));
+        } else {
+            s_q[nt][2 * c][lane] = make_uint2(u.x, u.y);
+            s_q[nt][2 * c + 1][lane] = make_uint2(u.z, u.w);
         }
-        const int64_t row = (((int64_t)id * a.p.Hkv + hk) << a.p.page_log2) + (j & ((1 << a.p.page_log2) - 1));
-        float k[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (lane * 4 + e < hs)
-                k[e] = a.p.k_scale ? (float)static_cast<const int8_t*>(a.p.k)[row * hs + lane * 4 + e]
-                                   : __bfloat162float(static_cast<const __nv_bfloat16*>(a.p.k)[row * hs + lane * 4 + e]);
-        const float f = a.scale_log2 * (a.p.k_scale ? a.p.k_scale[row] : 1.f);
-        float sum = 0.f;
-        for (int i = max(0, j - (kv_all - n)); i < n; ++i)
-            for (int h = hk * a.G; h < (hk + 1) * a.G; ++h) {
-                const __nv_bfloat16* q = a.q + (int64_t)(s0 + i) * a.ldq + h * hs + lane * 4;
-                float s = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (lane * 4 + e < hs) s += k[e] * __bfloat162float(q[e]);
-                s = warp_sum(s);
-                const float l = a.lse[(int64_t)(s0 + i) * a.H + h];
-                if (l != -INFINITY) sum += exp2f(s * f - l * 1.4426950408889634f);
-            }
-        if (lane == 0) a.mass[row] = sum + (a.old && j < kv_all - n ? a.decay * a.old[row] : 0.f);
     }
+    for (int i = threadIdx.x; i < NT * 8; i += WARPS * 32) {
+        const float l = i < R ? a.lse[(int64_t)(s.s0 + i / a.G) * a.H + hk * a.G + i % a.G] : -INFINITY;
+        // a row without weight sees nothing
+        reinterpret_cast<float*>(s_l)[i] = l * 1.4426950408889634f;
+        reinterpret_cast<int*>(s_last)[i] = l == -INFINITY ? -1 : s.kv_all - s.n + i / a.G;
+    }
+    __syncthreads();
+
+    const int row_bytes = hs * (Q8 ? 1 : 2), step = gridDim.x * WARPS;
+    int k_at[KC];  // the thread's places in a tile; dims past hs: the row's last 16 bytes (Q is zero there)
+#pragma unroll
+    for (int c = 0; c < KC; ++c) k_at[c] = g * row_bytes + min((c * 4 + t) * 16, row_bytes - 16);
+    int j = blockIdx.x * WARPS + warp;
+    int ids = 0;
+    bool bad_page = false;
+    unsigned refused = 0;  // of the 32 tiles looked up last
+    int round = 0;
+    auto tile_row = [&](int j) -> int64_t {  // the first row of the tile's part of its page
+        if ((round & 31) == 0) {             // 32 tiles' page ids at once, one per lane
+            const int mine = j + lane * step;
+            ids = 0;
+            bool bad = false;
+            if (mine < tiles) {
+                ids = __ldg(a.p.table + b * a.p.ld_table + ((tile0 + mine) * 16 >> a.p.page_log2));
+                if (ids < 0 || ids >= a.p.n_pages) {
+                    ids = 0;
+                    bad = bad_page = true;
+                }
+            }
+            refused = __ballot_sync(0xffffffffu, bad);
+        }
+        const int id = __shfl_sync(0xffffffffu, ids, round & 31);
+        const int pos = (tile0 + j) * 16;
+        ++round;
+        return (((int64_t)id * a.p.Hkv + hk) << a.p.page_log2) + (pos & ((1 << a.p.page_log2) - 1));
+    };
+    uint4 kr[2][KC];
+    float ks[2] = {1.f, 1.f};
+    auto load_k = [&](int64_t row) {
+        const char* base = static_cast<const char*>(a.p.k) + row * row_bytes;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int c = 0; c < KC; ++c) kr[h][c] = __ldg(reinterpret_cast<const uint4*>(base + (k_at[c] + h * 8 * row_bytes)));
+            if (Q8) ks[h] = __ldg(a.p.k_scale + row + h * 8 + g);
+        }
+    };
+    int64_t row = 0;
+    bool off = false;
+    if (j < tiles) {
+        row = tile_row(j);
+        off = refused & 1;
+        load_k(row);
+    }
+    for (; j < tiles; j += step) {
+        const int pos = (tile0 + j) * 16 + g;  // and pos + 8
+        const int64_t here = row;
+        const bool none = off;
+        float old[2] = {0.f, 0.f};
+        const bool mine = t < 2 && !none && pos + t * 8 < s.kv && pos + t * 8 >= s.first;  // lane t = 0, 1 of a row's four: key pos, pos + 8
+        if (mine && a.old && pos + t * 8 < s.kv_all - s.n) old[0] = a.old[here + g + t * 8];
+        float sc[NT][4] = {};
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+            const uint32_t x[2][4] = {{kr[0][c].x, kr[0][c].y, kr[0][c].z, kr[0][c].w}, {kr[1][c].x, kr[1][c].y, kr[1][c].z, kr[1][c].w}};
+            if (Q8) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const uint32_t a0 = codes02(a.masks, x[0][w]), a1 = codes02(a.masks, x[1][w]), a2 = codes02(a.masks, x[0][w] >> 8), a3 = codes02(a.masks, x[1][w] >> 8);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const uint2 q = s_q[nt][4 * c + w][lane];
+                        mma(sc[nt], a0, a1, a2, a3, q.x, q.y);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const uint2 q = s_q[nt][2 * c + e][lane];
+                        mma(sc[nt], x[0][2 * e], x[1][2 * e], x[0][2 * e + 1], x[1][2 * e + 1], q.x, q.y);
+                    }
+            }
+        }
+        float f[2] = {a.scale_log2, a.scale_log2};
+        if (Q8) f[0] *= ks[0], f[1] *= ks[1];
+        if (j + step < tiles) {  // the next keys are on their way
+            row = tile_row(j + step);
+            off = refused >> ((round - 1) & 31) & 1;
+            load_k(row);
+        }
+        float sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const float2 l = s_l[nt][t];
+            const int2 last = s_last[nt][t];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float p = ex2(fmaf(sc[nt][e], f[e >> 1], -(e & 1 ? l.y : l.x)));
+                sum[e >> 1] += pos + (e >> 1) * 8 <= (e & 1 ? last.y : last.x) ? p : 0.f;
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
+            sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
+        }
+        if (mine) a.mass[here + g + t * 8] = (t ? sum[1] : sum[0]) + a.decay * old[0];
+    }
+    if (bad_page) report(a.err, GK_ERR_INDEX);
+}
+
+// ---------------------------------------------------------------------------------------- tiles
+constexpr int KEYS = 256, RT = 128, THREADS = 384, LST = 4;  // LST: tiles whose log sums are kept
+constexpr uint32_t HALF = 128 * 128;                         // 128 rows of 64 bf16
+constexpr uint64_t WAIT_NS = 1000000000ull;
+
+template <int HSP>
+struct Layout {
+    static constexpr int HALVES = HSP / 64, STAGES = HSP == 64 ? 4 : 3;
+    static constexpr uint32_t TILE = HALVES * HALF;
+    static constexpr uint32_t Q = 2 * TILE, LSE = Q + STAGES * TILE, BARS = LSE + LST * (RT * 4 + 16), BYTES = BARS + 256 + 1024;
+};
+
+// (x, y) = (x s + a, y s + b); (x, y) += (a, b): two float32 operations an instruction.
+__device__ __forceinline__ void fma2(uint32_t& x, uint32_t& y, float s, float a, float b) {
+    asm("{\n\t.reg .b64 v, f, c;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 f, {%2, %2};\n\tmov.b64 c, {%3, %4};\n\t"
+        "fma.rn.f32x2 v, v, f, c;\n\tmov.b64 {%0, %1}, v;\n\t}"
+        : "+r"(x), "+r"(y)
+        : "f"(s), "f"(a), "f"(b));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
+    asm("{\n\t.reg .b64 v, w;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 w, {%2, %3};\n\tadd.rn.f32x2 v, v, w;\n\tmov.b64 {%0, %1}, v;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(a), "f"(b));
+}
+
+template <int HSP, bool Q8>
+__global__ void __launch_bounds__(THREADS, 1) mass_tiles_kernel(const MassArgs a, const __grid_constant__ CUtensorMap tm_q) {
+    using L = Layout<HSP>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sK = smem;  // [2 halves of the keys][halves of the dims]
+    uint8_t* sQ = smem + L::Q;
+    float* s_l = reinterpret_cast<float*>(smem + L::LSE);                       // [LST][128]: -lse log2(e)
+    uint32_t* s_mask = reinterpret_cast<uint32_t*>(smem + L::LSE + LST * RT * 4);  // [LST][4]: rows that give weight
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BARS);
+    uint64_t* q_full = bars;       // [4]
+    uint64_t* q_empty = bars + 4;  // [4]
+    uint64_t* l_full = bars + 8;   // [LST]
+    uint64_t* l_empty = bars + 12; // [LST] (an arrival per warp)
+    uint64_t* s_full = bars + 16;  // [2 halves][2 buffers]
+    uint64_t* s_free = bars + 20;  // [2][2] (an arrival per warp)
+    uint64_t* bar_drain = bars + 24;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 25);
+    wait_for_earlier_kernels();
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hs = a.p.hs;
+    const int b = blockIdx.z, hk = blockIdx.y;
+    Span s;
+    if (!span_of(a, b, s)) return;
+    const int k0 = (s.first & ~(KEYS - 1)) + blockIdx.x * KEYS;
+    if (k0 >= s.kv) return;
+    const bool on[2] = {k0 + RT > s.first, k0 + RT < s.kv};  // halves with a key to weigh
+    // tiles of rows, from the first that sees a key of the block on
+    const int parts = (a.G + a.tile_heads - 1) / a.tile_heads, seen_from = max(0, max(k0, s.first) - (s.kv_all - s.n));
+    const int block0 = min(seen_from, s.n) / a.tile_queries, n_tiles = ((s.n + a.tile_queries - 1) / a.tile_queries - block0) * parts;
+
+    if (tid == 0) {
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], 1);
+            mbar_init(&l_full[i], 1);
+            mbar_init(&l_empty[i], 4 * (on[0] + on[1]));
+            mbar_init(&s_full[i], 1);
+            mbar_init(&s_free[i], 4);
+        }
+        mbar_init(bar_drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 9) tmem_alloc(tmem_slot, 512);
+    // the block's keys as bf16; past the end, before the first and on refused pages zeros
+    bool bad_page = false;
+    constexpr int CH = Q8 ? HSP / 16 : HSP / 8;  // 16-byte pieces of a row
+#pragma unroll 4
+    for (int x = tid; x < KEYS * CH; x += THREADS) {
+        const int r = x / CH, c = x - r * CH, pos = k0 + r;
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (pos < s.kv && pos >= s.first && c * 16 < hs * (Q8 ? 1 : 2)) {
+            const int id = __ldg(a.p.table + b * a.p.ld_table + (pos >> a.p.page_log2));
+            if (id >= 0 && id < a.p.n_pages) {
+                const int64_t row = (((int64_t)id * a.p.Hkv + hk) << a.p.page_log2) + (pos & ((1 << a.p.page_log2) - 1));
+                u = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(a.p.k) + row * (hs * (Q8 ? 1 : 2)) + c * 16));
+            } else {
+                bad_page = true;
+            }
+        }
+        uint8_t* tile = sK + (r >> 7) * L::TILE;
+        if (Q8) {
+            const uint4 lo = make_uint4(codes_pair(a.masks, u.x, 0), codes_pair(a.masks, u.x, 1), codes_pair(a.masks, u.y, 0), codes_pair(a.masks, u.y, 1));
+            const uint4 hi = make_uint4(codes_pair(a.masks, u.z, 0), codes_pair(a.masks, u.z, 1), codes_pair(a.masks, u.w, 0), codes_pair(a.masks, u.w, 1));
+            *reinterpret_cast<uint4*>(tile + (c >> 2) * HALF + swizzled(r & 127, 2 * (c & 3))) = lo;
+            *reinterpret_cast<uint4*>(tile + (c >> 2) * HALF + swizzled(r & 127, 2 * (c & 3) + 1)) = hi;
+        } else {
+            *reinterpret_cast<uint4*>(tile + (c >> 3) * HALF + swizzled(r & 127, c & 7)) = u;
+        }
+    }
+    if (bad_page) report(a.err, GK_ERR_INDEX);
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    bool failed = false;
+
+    if (warp == 8) {  // rows by TMA, log sums by lanes (four each)
+        int in_flight = -1;
+        float l[4];
+        auto load_l = [&](int i) {
+            const int q0 = (block0 + i / parts) * a.tile_queries, h0 = i % parts * a.tile_heads;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int c = lane * 4 + e, query = q0 + c / a.tile_heads, h = h0 + c % a.tile_heads;
+                const bool there = c < a.tile_heads * a.tile_queries && query < s.n && h < a.G;
+                l[e] = there ? a.lse[(int64_t)(s.s0 + query) * a.H + hk * a.G + h] : -INFINITY;
+            }
+        };
+        if (n_tiles > 0) load_l(0);
+        for (int i = 0; i < n_tiles; ++i) {
+            const int st = i % L::STAGES, ls = i % LST;
+            bool ok = wait_phase(&q_empty[st], i / L::STAGES & 1 ^ 1, WAIT_NS) && wait_phase(&l_empty[ls], i / LST & 1 ^ 1, WAIT_NS);
+            if (!__all_sync(0xffffffffu, ok)) {
+                failed = true;
+                break;
+            }
+            if (lane == 0) {
+                const int q0 = (block0 + i / parts) * a.tile_queries, h0 = i % parts * a.tile_heads;
+                mbar_expect_tx(&q_full[st], (uint32_t)(L::HALVES * 128 * a.tile_heads * a.tile_queries));
+                for (int h = 0; h < L::HALVES; ++h)
+                    tma_load_3d(&tm_q, &q_full[st], sQ + st * L::TILE + h * HALF, h * 64, hk * a.G + h0, s.s0 + q0);
+            }
+            in_flight = i;
+            uint32_t given = 0;  // bits of the lane's four rows
+#pragma unroll
+            for (int e = 0; e < 4; ++e) given |= (l[e] == -INFINITY ? 0u : 1u) << e;
+            reinterpret_cast<float4*>(s_l + ls * RT)[lane] = make_float4(-l[0] * 1.4426950408889634f, -l[1] * 1.4426950408889634f,
+                                                                        -l[2] * 1.4426950408889634f, -l[3] * 1.4426950408889634f);
+            given <<= (lane & 7) * 4;
+            for (int o = 1; o < 8; o <<= 1) given |= __shfl_xor_sync(0xffffffffu, given, o);
+            if ((lane & 7) == 0) s_mask[ls * 4 + (lane >> 3)] = given;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&l_full[ls]);
+            if (i + 1 < n_tiles) load_l(i + 1);
+        }
+        if (failed)  // the copies in flight land before the block ends
+            for (int i = max(0, in_flight - L::STAGES + 1); i <= in_flight; ++i) wait_phase(&q_full[i % L::STAGES], i / L::STAGES & 1, WAIT_NS / 5);
+    } else if (warp == 9) {
+        const uint32_t id = instr_desc_bf16(false, false, 128, 128);
+        const uint64_t k_d = smem_desc(saddr(sK), 16, 1024), q_d = smem_desc(saddr(sQ), 16, 1024);
+        const int steps = hs >> 4;
+        bool ok = true;
+        for (int i = 0; ok && i < n_tiles; ++i) {
+            const int st = i % L::STAGES, buf = i & 1;
+            ok = __all_sync(0xffffffffu, wait_phase(&q_full[st], i / L::STAGES & 1, WAIT_NS));
+            for (int g = 0; g < 2 && ok; ++g) {
+                if (!on[g]) continue;
+                ok = __all_sync(0xffffffffu, wait_phase(&s_free[g * 2 + buf], i >> 1 & 1 ^ 1, WAIT_NS));
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    for (int kk = 0; kk < steps; ++kk) {
+                        const uint32_t at = (kk >> 2) * HALF + (kk & 3) * 32;
+                        umma_bf16(tmem + g * 256 + buf * 128, desc_add(k_d, g * L::TILE + at), desc_add(q_d, st * L::TILE + at), id, kk > 0);
+                    }
+                    umma_commit(&s_full[g * 2 + buf]);
+                }
+                __syncwarp();
+            }
+            if (ok) {
+                if (elect_one()) umma_commit(&q_empty[st]);
+                __syncwarp();
+            }
+        }
+        if (n_tiles > 0) {  // everything issued is complete before the block ends
+            if (elect_one()) {
+                umma_commit(bar_drain);
+                wait_phase(bar_drain, 0, ok ? WAIT_NS : WAIT_NS / 5);
+            }
+            __syncwarp();
+        }
+        if (!ok) failed = true;
+    } else if (warp < 8 && on[warp >> 2]) {
+        const int g = warp >> 2, pos = k0 + g * RT + (warp & 3) * 32 + lane;
+        const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16) + g * 256;
+        int64_t row = -1;
+        if (pos >= s.first && pos < s.kv) {
+            const int id_ = __ldg(a.p.table + b * a.p.ld_table + (pos >> a.p.page_log2));
+            if (id_ >= 0 && id_ < a.p.n_pages) row = (((int64_t)id_ * a.p.Hkv + hk) << a.p.page_log2) + (pos & ((1 << a.p.page_log2) - 1));
+        }
+        float f = a.scale_log2;
+        if (Q8) f *= row >= 0 ? __ldg(a.p.k_scale + row) : 0.f;
+        const bool earlier = pos < s.kv_all - s.n;
+        const float before = row >= 0 && a.old && earlier ? a.old[row] : 0.f;
+        const int from = max(0, pos - (s.kv_all - s.n));  // the first query that sees the key
+        float total = 0.f;
+        for (int i = 0; i < n_tiles; ++i) {
+            const int buf = i & 1, ls = i % LST;
+            bool ok = wait_phase(&s_full[g * 2 + buf], i >> 1 & 1, WAIT_NS) && wait_phase(&l_full[ls], i / LST & 1, WAIT_NS);
+            if (!__all_sync(0xffffffffu, ok)) {
+                failed = true;
+                break;
+            }
+            tc_fence_after();
+            uint32_t sv[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32_nowait(lane_addr + buf * 128 + c * 32, sv[c]);
+            tmem_wait_ld_only();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) reg_fence32(sv[c]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_free[g * 2 + buf]);
+            const uint4 mask = *reinterpret_cast<const uint4*>(s_mask + ls * 4);
+            const int lo = (from - (block0 + i / parts) * a.tile_queries) * a.tile_heads;  // columns before it do not see the key
+            const bool part = __any_sync(0xffffffffu, lo > 0) || (mask.x & mask.y & mask.z & mask.w) != 0xffffffffu;
+            const float4* l4 = reinterpret_cast<const float4*>(s_l + ls * RT);
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint32_t masks[4] = {mask.x, mask.y, mask.z, mask.w};
+            auto weights = [&](auto some) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        uint32_t* w = &sv[c][4 * e];
+                        const float4 l = l4[c * 8 + e];
+                        fma2(w[0], w[1], f, l.x, l.y);
+                        fma2(w[2], w[3], f, l.z, l.w);
+                        float p[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            p[x] = ex2_hw(__uint_as_float(w[x]));
+                            if (decltype(some)::value && (c * 32 + e * 4 + x < lo || !(masks[c] >> (e * 4 + x) & 1))) p[x] = 0.f;
+                        }
+                        add2(sum[0], sum[1], p[0], p[1]);
+                        add2(sum[2], sum[3], p[2], p[3]);
+                    }
+                }
+            };
+            if (part) weights(std::true_type{});
+            else weights(std::false_type{});
+            total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&l_empty[ls]);
+        }
+        if (!failed && row >= 0) a.mass[row] = total + a.decay * before;
+    }
+    if (failed) report(a.err, GK_ERR_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int HSP, bool Q8>
+gk_status launch(gk_ctx* ctx, MassArgs& a) {
+    const int64_t R = (int64_t)a.max_q * a.G;
+    const unsigned Hkv = (unsigned)a.p.Hkv, B = (unsigned)a.B;
+    if (R <= 64) {
+        // Four tiles of keys a warp, more where the blocks would be over 16 an SM.
+        const int64_t each = 4 * WARPS * 16, most = cdiv(16 * (int64_t)ctx->num_sms, (int64_t)Hkv * B);
+        const unsigned x = (unsigned)std::max<int64_t>(1, std::min(cdiv(a.p.capacity, each), most));
+#define FEW(NT) return launch_dependent(ctx, "paged_mass", mass_few_kernel<HSP, Q8, NT>, dim3(x, Hkv, B), dim3(WARPS * 32), 0, 1, a)
+        if (R <= 8) FEW(1);
+        if (R <= 16) FEW(2);
+        if (R <= 32) FEW(4);
+        FEW(8);
+#undef FEW
+    }
+    GK_TRY((allow_shared<mass_tiles_kernel<HSP, Q8>>(ctx, "gk_paged_mass", Layout<HSP>::BYTES)));
+    a.tile_heads = std::min(a.G, RT);
+    a.tile_queries = RT / a.tile_heads;
+    CUtensorMap map{};
+    GK_REQUIRE(ctx, make_map_3d(&map, a.q, a.p.hs, a.H, a.p.hs, a.rows, a.ldq, a.tile_heads, a.tile_queries), GK_ERR_CUDA,
+               "gk_paged_mass: tensor map");
+    return launch_dependent(ctx, "paged_mass_tiles", mass_tiles_kernel<HSP, Q8>, dim3((unsigned)cdiv(a.p.capacity, KEYS), Hkv, B),
+                            dim3(THREADS), Layout<HSP>::BYTES, 1, a, map);
 }
 
 }  // namespace
@@ -106,6 +520,7 @@ extern "C" gk_status gk_paged_mass(gk_ctx* ctx, const gk_paged_kv* cache, int dt
     a.rows = (int)rows;
     a.max_q = (int)std::min<int64_t>(max_q, rows);
     a.err = ctx->d_err;
-    const int64_t blocks = std::min<int64_t>(cdiv(a.p.capacity, WARPS), cdiv(16 * (int64_t)ctx->num_sms, (int64_t)a.p.Hkv * B) + 8);
-    return launch_dependent(ctx, "paged_mass", mass_kernel, dim3((unsigned)blocks, (unsigned)a.p.Hkv, (unsigned)B), dim3(WARPS * 32), 0, 1, a);
+    const bool small = a.p.hs <= 64;
+    if (a.p.k_scale) return small ? launch<64, true>(ctx, a) : launch<128, true>(ctx, a);
+    return small ? launch<64, false>(ctx, a) : launch<128, false>(ctx, a);
 }

@@ -58,11 +58,39 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
     }
 }
 
+__device__ __forceinline__ uint32_t test_phase(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(saddr(bar)), "r"(parity)
+        : "memory");
+    return ok;
+}
+// Wait for a phase: polled at first (try_wait suspends the thread, and its wake-up takes longer than most
+// of the waits here), then bounded by the clock.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint64_t limit) {
+#pragma unroll 1
+    for (int i = 0; i < 4096; ++i)
+        if (test_phase(bar, parity)) return true;
+    return mbar_wait(bar, parity, nullptr, limit);
+}
+
 __device__ __forceinline__ void tma_load_2d(const CUtensorMap* map, uint64_t* bar, void* dst, int x, int y) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
             saddr(dst)),
         "l"((uint64_t)map), "r"(saddr(bar)), "r"(x), "r"(y)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* bar, void* dst, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+            saddr(dst)),
+        "l"((uint64_t)map), "r"(saddr(bar)), "r"(x), "r"(y), "r"(z)
         : "memory");
 }
 
@@ -80,6 +108,9 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
     d |= (uint64_t)2 << 61;
     return d;
 }
+
+// Byte offset of the 16 bytes at chunk c (of 8) of row r in a 128-byte-swizzled half tile.
+__device__ __forceinline__ uint32_t swizzled(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
 // Instruction descriptor, kind::f16: float32 D, bf16 A and B, majorness (1 = MN-major),
 // N >> 3, M >> 4.
@@ -382,6 +413,22 @@ inline bool make_map(CUtensorMap* map, const void* base, int64_t inner, int64_t 
     cuuint32_t box[2] = {64u, (cuuint32_t)box_outer};
     cuuint32_t estr[2] = {1u, 1u};
     CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+// 3-D bf16 tensor map: inner (contiguous) extent, middle extent (stride ld_middle elements), outer extent (stride
+// ld_outer), box {64, box_middle, box_outer}, 128-byte swizzle, zero fill outside the tensor.
+inline bool make_map_3d(CUtensorMap* map, const void* base, int64_t inner, int64_t middle, int64_t ld_middle, int64_t outer,
+                        int64_t ld_outer, int box_middle, int box_outer) {
+    auto enc = encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)middle, (cuuint64_t)outer};
+    cuuint64_t strides[2] = {(cuuint64_t)ld_middle * 2, (cuuint64_t)ld_outer * 2};
+    cuuint32_t box[3] = {64u, (cuuint32_t)box_middle, (cuuint32_t)box_outer};
+    cuuint32_t estr[3] = {1u, 1u, 1u};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
