@@ -83,19 +83,6 @@ __device__ __forceinline__ void mul2(uint32_t& x, uint32_t& y, float a, float b)
         : "f"(a), "f"(b));
 }
 
-// Several at once: even a test of a completed phase takes hundreds of cycles behind the softmax warps' traffic
-// with the tensor memory, so the tests are sent together. (b and c only where asked.)
-__device__ __forceinline__ bool wait_phases(uint64_t* a, uint32_t pa, bool has_b, uint64_t* b, uint32_t pb, bool has_c, uint64_t* c,
-                                            uint32_t pc, uint64_t limit) {
-#pragma unroll 1
-    for (int i = 0; i < 4096; ++i) {
-        const uint32_t x = test_phase(a, pa), y = test_phase(has_b ? b : a, has_b ? pb : pa);
-        const uint32_t z = test_phase(has_c ? c : a, has_c ? pc : pa);
-        if (x & y & z) return true;
-    }
-    return mbar_wait(a, pa, nullptr, limit) && (!has_b || mbar_wait(b, pb, nullptr, limit)) && (!has_c || mbar_wait(c, pc, nullptr, limit));
-}
-
 // Rows that a sequence takes per head once expanded: whole tiles of keys.
 __device__ __forceinline__ int expanded_rows(const Pages& p, int b) {
     return (min(max(__ldg(p.kv_len + b), 0), p.capacity) + KT - 1) / KT * KT;

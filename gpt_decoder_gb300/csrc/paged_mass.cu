@@ -9,8 +9,11 @@
 //   attention of few rows does), its rows eight at a time from shared memory, which holds them in operand order.
 //   Tiles: a block holds 256 keys in shared memory (8-bit codes as bf16, once) and walks the rows in tiles of 128,
 //   which TMA brings (a box of whole queries of the heads that share the keys); D = K Q^T (tcgen05, M = 128 keys, N =
-//   128 rows) into tensor memory, two buffers for each half of the keys; eight warps, a thread a key, read the row of
-//   scores and add its weights. A key's scale is its thread's, and a row's log sum a broadcast from shared memory.
+//   128 rows) into tensor memory, two buffers for each half of the keys; sixteen warps, a thread a key and half of the
+//   tile's rows, read the scores and add their weights. A key's factor f (scale log2(e), times its own scale for codes) is
+//   its thread's. The rows' log sums would be a broadcast load for every element (four wavefronts of shared memory for
+//   four of them, which is all that the operands leave): they are one more 16-deep step of the product instead, of 1 / f
+//   and -l in three bf16 parts each, so that D = s / f - l / f and the weight is 2^(f D).
 #include <math.h>
 
 #include <algorithm>
@@ -208,29 +211,53 @@ __global__ void __launch_bounds__(WARPS * 32) mass_few_kernel(const MassArgs a) 
 }
 
 // ---------------------------------------------------------------------------------------- tiles
-constexpr int KEYS = 256, RT = 128, THREADS = 384, LST = 4;  // LST: tiles whose log sums are kept
-constexpr uint32_t HALF = 128 * 128;                         // 128 rows of 64 bf16
+constexpr int KEYS = 256, RT = 128, THREADS = 640, SUM_WARPS = 16;
+constexpr uint32_t HALF = 128 * 128;  // 128 rows of 64 bf16
+constexpr uint32_t STEP = 128 * 32;   // 128 rows of one 16-deep step
 constexpr uint64_t WAIT_NS = 1000000000ull;
+constexpr float LEAST_F = 0x1p-60f;    // a smaller factor (of codes): no score at all
+constexpr float NO_WEIGHT = -0x1p60f;  // instead of -l: 1 / f times it is finite
 
 template <int HSP>
 struct Layout {
     static constexpr int HALVES = HSP / 64, STAGES = HSP == 64 ? 4 : 3;
     static constexpr uint32_t TILE = HALVES * HALF;
-    static constexpr uint32_t Q = 2 * TILE, LSE = Q + STAGES * TILE, BARS = LSE + LST * (RT * 4 + 16), BYTES = BARS + 256 + 1024;
+    static constexpr uint32_t Q = 2 * TILE, KX = Q + STAGES * TILE, QX = KX + 2 * STEP, JOIN = QX + STAGES * STEP, BARS = JOIN + KEYS * 4,
+                              BYTES = BARS + 256 + 1024;
 };
 
-// (x, y) = (x s + a, y s + b); (x, y) += (a, b): two float32 operations an instruction.
-__device__ __forceinline__ void fma2(uint32_t& x, uint32_t& y, float s, float a, float b) {
-    asm("{\n\t.reg .b64 v, f, c;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 f, {%2, %2};\n\tmov.b64 c, {%3, %4};\n\t"
-        "fma.rn.f32x2 v, v, f, c;\n\tmov.b64 {%0, %1}, v;\n\t}"
+// (x, y) *= (s, s); (x, y) += (a, b): two float32 operations an instruction.
+__device__ __forceinline__ void mul2(uint32_t& x, uint32_t& y, float s) {
+    asm("{\n\t.reg .b64 v, f;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 f, {%2, %2};\n\tmul.rn.f32x2 v, v, f;\n\tmov.b64 {%0, %1}, v;\n\t}"
         : "+r"(x), "+r"(y)
-        : "f"(s), "f"(a), "f"(b));
+        : "f"(s));
 }
 __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
     asm("{\n\t.reg .b64 v, w;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 w, {%2, %3};\n\tadd.rn.f32x2 v, v, w;\n\tmov.b64 {%0, %1}, v;\n\t}"
         : "+f"(x), "+f"(y)
         : "f"(a), "f"(b));
 }
+// Barrier of `n` threads (id 1 ..; 0 is __syncthreads).
+__device__ __forceinline__ void named_bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+
+// x as three bf16 parts (24 significant bits; what is not finite is all in the first).
+struct Parts {
+    uint32_t p[3];
+};
+__device__ __forceinline__ Parts parts_of(float x) {
+    Parts r;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const __nv_bfloat16 h = __float2bfloat16_rn(x);
+        r.p[i] = __bfloat16_as_ushort(h);
+        const float rest = x - __bfloat162float(h);
+        x = isfinite(rest) ? rest : 0.f;
+    }
+    return r;
+}
+// Six products whose sum is a b: slots of the 16-deep step (the other ten are zeros).
+__device__ __forceinline__ uint4 slots_a(const Parts& a) { return make_uint4(a.p[0] | a.p[0] << 16, a.p[0] | a.p[1] << 16, a.p[1] | a.p[2] << 16, 0); }
+__device__ __forceinline__ uint4 slots_b(const Parts& b) { return make_uint4(b.p[0] | b.p[1] << 16, b.p[2] | b.p[0] << 16, b.p[1] | b.p[0] << 16, 0); }
 
 template <int HSP, bool Q8>
 __global__ void __launch_bounds__(THREADS, 1) mass_tiles_kernel(const MassArgs a, const __grid_constant__ CUtensorMap tm_q) {
@@ -239,17 +266,15 @@ __global__ void __launch_bounds__(THREADS, 1) mass_tiles_kernel(const MassArgs a
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sK = smem;  // [2 halves of the keys][halves of the dims]
     uint8_t* sQ = smem + L::Q;
-    float* s_l = reinterpret_cast<float*>(smem + L::LSE);                       // [LST][128]: -lse log2(e)
-    uint32_t* s_mask = reinterpret_cast<uint32_t*>(smem + L::LSE + LST * RT * 4);  // [LST][4]: rows that give weight
+    uint8_t* sKx = smem + L::KX;  // [2]: the step of 1 / f
+    uint8_t* sQx = smem + L::QX;  // [stages]: and of -l
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BARS);
     uint64_t* q_full = bars;       // [4]
     uint64_t* q_empty = bars + 4;  // [4]
-    uint64_t* l_full = bars + 8;   // [LST]
-    uint64_t* l_empty = bars + 12; // [LST] (an arrival per warp)
-    uint64_t* s_full = bars + 16;  // [2 halves][2 buffers]
-    uint64_t* s_free = bars + 20;  // [2][2] (an arrival per warp)
-    uint64_t* bar_drain = bars + 24;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 25);
+    uint64_t* s_full = bars + 8;   // [2 halves][2 buffers]
+    uint64_t* s_free = bars + 12;  // [2][2] (an arrival per warp)
+    uint64_t* bar_drain = bars + 16;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 17);
     wait_for_earlier_kernels();
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hs = a.p.hs;
@@ -262,32 +287,39 @@ __global__ void __launch_bounds__(THREADS, 1) mass_tiles_kernel(const MassArgs a
     // tiles of rows, from the first that sees a key of the block on
     const int parts = (a.G + a.tile_heads - 1) / a.tile_heads, seen_from = max(0, max(k0, s.first) - (s.kv_all - s.n));
     const int block0 = min(seen_from, s.n) / a.tile_queries, n_tiles = ((s.n + a.tile_queries - 1) / a.tile_queries - block0) * parts;
+    const int cols = a.tile_heads * a.tile_queries;
 
     if (tid == 0) {
         for (int i = 0; i < 4; ++i) {
             mbar_init(&q_full[i], 1);
             mbar_init(&q_empty[i], 1);
-            mbar_init(&l_full[i], 1);
-            mbar_init(&l_empty[i], 4 * (on[0] + on[1]));
             mbar_init(&s_full[i], 1);
-            mbar_init(&s_free[i], 4);
+            mbar_init(&s_free[i], 8);
         }
         mbar_init(bar_drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 9) tmem_alloc(tmem_slot, 512);
-    // the block's keys as bf16; past the end, before the first and on refused pages zeros
+    if (warp == SUM_WARPS + 1) tmem_alloc(tmem_slot, 512);
+    // the block's keys as bf16; past the end, before the first, on refused pages and without a score zeros
     bool bad_page = false;
+    auto factor = [&](int64_t row) {  // of a key's score; 0: it has none
+        const float f = Q8 ? a.scale_log2 * __ldg(a.p.k_scale + row) : a.scale_log2;
+        return Q8 && fabsf(f) < LEAST_F ? 0.f : f;
+    };
     constexpr int CH = Q8 ? HSP / 16 : HSP / 8;  // 16-byte pieces of a row
 #pragma unroll 4
     for (int x = tid; x < KEYS * CH; x += THREADS) {
         const int r = x / CH, c = x - r * CH, pos = k0 + r;
         uint4 u = make_uint4(0, 0, 0, 0);
-        if (pos < s.kv && pos >= s.first && c * 16 < hs * (Q8 ? 1 : 2)) {
+        float f = 1.f;
+        if (pos < s.kv && pos >= s.first) {
             const int id = __ldg(a.p.table + b * a.p.ld_table + (pos >> a.p.page_log2));
             if (id >= 0 && id < a.p.n_pages) {
                 const int64_t row = (((int64_t)id * a.p.Hkv + hk) << a.p.page_log2) + (pos & ((1 << a.p.page_log2) - 1));
-                u = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(a.p.k) + row * (hs * (Q8 ? 1 : 2)) + c * 16));
+                if (c * 16 < hs * (Q8 ? 1 : 2))
+                    u = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(a.p.k) + row * (hs * (Q8 ? 1 : 2)) + c * 16));
+                f = factor(row);
+                if (f == 0.f) u = make_uint4(0, 0, 0, 0), f = 1.f;
             } else {
                 bad_page = true;
             }
@@ -301,6 +333,17 @@ __global__ void __launch_bounds__(THREADS, 1) mass_tiles_kernel(const MassArgs a
         } else {
             *reinterpret_cast<uint4*>(tile + (c >> 3) * HALF + swizzled(r & 127, c & 7)) = u;
         }
+        if (c == 0) {
+            *reinterpret_cast<uint4*>(sKx + (r >> 7) * STEP + swizzled32(r & 127, 0)) = slots_a(parts_of(1.f / f));
+            *reinterpret_cast<uint4*>(sKx + (r >> 7) * STEP + swizzled32(r & 127, 1)) = make_uint4(0, 0, 0, 0);
+        }
+    }
+    for (int x = tid; x < L::STAGES * RT; x += THREADS)
+        *reinterpret_cast<uint4*>(sQx + x / RT * STEP + swizzled32(x % RT, 1)) = make_uint4(0, 0, 0, 0);
+    // rows that no box of TMA fills: zeros, whose log sum gives them no weight
+    for (int x = tid; x < L::STAGES * L::HALVES * (RT - cols) * 8; x += THREADS) {
+        const int t = x / ((RT - cols) * 8), r = cols + x % ((RT - cols) * 8) / 8;
+        *reinterpret_cast<uint4*>(sQ + t * HALF + swizzled(r, x & 7)) = make_uint4(0, 0, 0, 0);
     }
     if (bad_page) report(a.err, GK_ERR_INDEX);
     fence_proxy_async_smem();
@@ -310,64 +353,67 @@ __global__ void __launch_bounds__(THREADS, 1) mass_tiles_kernel(const MassArgs a
     const uint32_t tmem = *tmem_slot;
     bool failed = false;
 
-    if (warp == 8) {  // rows by TMA, log sums by lanes (four each)
-        int in_flight = -1;
+    if (warp == SUM_WARPS) {  // rows by TMA, log sums by lanes (four each)
+        int in_flight = -1, q0 = block0 * a.tile_queries, h0 = 0;  // of the next tile whose log sums are read
+        int query[4], head[4];  // of the lane's rows (lane, lane + 32, ..), from the tile's first
         float l[4];
-        auto load_l = [&](int i) {
-            const int q0 = (block0 + i / parts) * a.tile_queries, h0 = i % parts * a.tile_heads;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int c = lane * 4 + e, query = q0 + c / a.tile_heads, h = h0 + c % a.tile_heads;
-                const bool there = c < a.tile_heads * a.tile_queries && query < s.n && h < a.G;
-                l[e] = there ? a.lse[(int64_t)(s.s0 + query) * a.H + hk * a.G + h] : -INFINITY;
-            }
+        for (int e = 0; e < 4; ++e) {
+            const int c = lane + e * 32;
+            query[e] = c < cols ? c / a.tile_heads : 1 << 30;
+            head[e] = c % a.tile_heads;
+        }
+        auto load_l = [&]() {
+            const float* src = a.lse + (int64_t)(s.s0 + q0) * a.H + hk * a.G + h0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                l[e] = query[e] < s.n - q0 && head[e] < a.G - h0 ? __ldg(src + (int64_t)query[e] * a.H + head[e]) : INFINITY;
         };
-        if (n_tiles > 0) load_l(0);
+        if (n_tiles > 0) load_l();
         for (int i = 0; i < n_tiles; ++i) {
-            const int st = i % L::STAGES, ls = i % LST;
-            bool ok = wait_phase(&q_empty[st], i / L::STAGES & 1 ^ 1, WAIT_NS) && wait_phase(&l_empty[ls], i / LST & 1 ^ 1, WAIT_NS);
-            if (!__all_sync(0xffffffffu, ok)) {
+            const int st = i % L::STAGES;
+            if (!__all_sync(0xffffffffu, mbar_wait(&q_empty[st], i / L::STAGES & 1 ^ 1, nullptr, WAIT_NS))) {
                 failed = true;
                 break;
             }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<uint4*>(sQx + st * STEP + swizzled32(lane + e * 32, 0)) =
+                    slots_b(parts_of(isinf(l[e]) ? NO_WEIGHT : l[e] * -1.4426950408889634f));
+            fence_proxy_async_smem();
+            __syncwarp();
             if (lane == 0) {
-                const int q0 = (block0 + i / parts) * a.tile_queries, h0 = i % parts * a.tile_heads;
-                mbar_expect_tx(&q_full[st], (uint32_t)(L::HALVES * 128 * a.tile_heads * a.tile_queries));
+                mbar_expect_tx(&q_full[st], (uint32_t)(L::HALVES * 128 * cols));
                 for (int h = 0; h < L::HALVES; ++h)
                     tma_load_3d(&tm_q, &q_full[st], sQ + st * L::TILE + h * HALF, h * 64, hk * a.G + h0, s.s0 + q0);
             }
             in_flight = i;
-            uint32_t given = 0;  // bits of the lane's four rows
-#pragma unroll
-            for (int e = 0; e < 4; ++e) given |= (l[e] == -INFINITY ? 0u : 1u) << e;
-            reinterpret_cast<float4*>(s_l + ls * RT)[lane] = make_float4(-l[0] * 1.4426950408889634f, -l[1] * 1.4426950408889634f,
-                                                                        -l[2] * 1.4426950408889634f, -l[3] * 1.4426950408889634f);
-            given <<= (lane & 7) * 4;
-            for (int o = 1; o < 8; o <<= 1) given |= __shfl_xor_sync(0xffffffffu, given, o);
-            if ((lane & 7) == 0) s_mask[ls * 4 + (lane >> 3)] = given;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&l_full[ls]);
-            if (i + 1 < n_tiles) load_l(i + 1);
+            h0 += a.tile_heads;
+            if (h0 >= a.G) h0 = 0, q0 += a.tile_queries;
+            if (i + 1 < n_tiles) load_l();
         }
         if (failed)  // the copies in flight land before the block ends
-            for (int i = max(0, in_flight - L::STAGES + 1); i <= in_flight; ++i) wait_phase(&q_full[i % L::STAGES], i / L::STAGES & 1, WAIT_NS / 5);
-    } else if (warp == 9) {
+            for (int i = max(0, in_flight - L::STAGES + 1); i <= in_flight; ++i) mbar_wait(&q_full[i % L::STAGES], i / L::STAGES & 1, nullptr, WAIT_NS / 5);
+    } else if (warp == SUM_WARPS + 1) {
         const uint32_t id = instr_desc_bf16(false, false, 128, 128);
         const uint64_t k_d = smem_desc(saddr(sK), 16, 1024), q_d = smem_desc(saddr(sQ), 16, 1024);
+        const uint64_t kx_d = smem_desc32(saddr(sKx)), qx_d = smem_desc32(saddr(sQx));
         const int steps = hs >> 4;
         bool ok = true;
         for (int i = 0; ok && i < n_tiles; ++i) {
             const int st = i % L::STAGES, buf = i & 1;
-            ok = __all_sync(0xffffffffu, wait_phase(&q_full[st], i / L::STAGES & 1, WAIT_NS));
+            ok = __all_sync(0xffffffffu, mbar_wait(&q_full[st], i / L::STAGES & 1, nullptr, WAIT_NS));
             for (int g = 0; g < 2 && ok; ++g) {
                 if (!on[g]) continue;
-                ok = __all_sync(0xffffffffu, wait_phase(&s_free[g * 2 + buf], i >> 1 & 1 ^ 1, WAIT_NS));
+                ok = __all_sync(0xffffffffu, mbar_wait(&s_free[g * 2 + buf], i >> 1 & 1 ^ 1, nullptr, WAIT_NS));
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
+                    const uint32_t d = tmem + g * 256 + buf * 128;
+                    umma_bf16(d, desc_add(kx_d, g * STEP), desc_add(qx_d, st * STEP), id, 0);
                     for (int kk = 0; kk < steps; ++kk) {
                         const uint32_t at = (kk >> 2) * HALF + (kk & 3) * 32;
-                        umma_bf16(tmem + g * 256 + buf * 128, desc_add(k_d, g * L::TILE + at), desc_add(q_d, st * L::TILE + at), id, kk > 0);
+                        umma_bf16(d, desc_add(k_d, g * L::TILE + at), desc_add(q_d, st * L::TILE + at), id, 1);
                     }
                     umma_commit(&s_full[g * 2 + buf]);
                 }
@@ -381,80 +427,80 @@ __global__ void __launch_bounds__(THREADS, 1) mass_tiles_kernel(const MassArgs a
         if (n_tiles > 0) {  // everything issued is complete before the block ends
             if (elect_one()) {
                 umma_commit(bar_drain);
-                wait_phase(bar_drain, 0, ok ? WAIT_NS : WAIT_NS / 5);
+                mbar_wait(bar_drain, 0, nullptr, ok ? WAIT_NS : WAIT_NS / 5);
             }
             __syncwarp();
         }
         if (!ok) failed = true;
-    } else if (warp < 8 && on[warp >> 2]) {
-        const int g = warp >> 2, pos = k0 + g * RT + (warp & 3) * 32 + lane;
-        const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16) + g * 256;
+    } else if (warp < SUM_WARPS && on[warp >> 3]) {
+        const int g = warp >> 3, side = warp >> 2 & 1, pos = k0 + g * RT + (warp & 3) * 32 + lane;
+        const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16) + g * 256 + side * 64;
         int64_t row = -1;
         if (pos >= s.first && pos < s.kv) {
-            const int id_ = __ldg(a.p.table + b * a.p.ld_table + (pos >> a.p.page_log2));
-            if (id_ >= 0 && id_ < a.p.n_pages) row = (((int64_t)id_ * a.p.Hkv + hk) << a.p.page_log2) + (pos & ((1 << a.p.page_log2) - 1));
+            const int id = __ldg(a.p.table + b * a.p.ld_table + (pos >> a.p.page_log2));
+            if (id >= 0 && id < a.p.n_pages) row = (((int64_t)id * a.p.Hkv + hk) << a.p.page_log2) + (pos & ((1 << a.p.page_log2) - 1));
         }
-        float f = a.scale_log2;
-        if (Q8) f *= row >= 0 ? __ldg(a.p.k_scale + row) : 0.f;
-        const bool earlier = pos < s.kv_all - s.n;
-        const float before = row >= 0 && a.old && earlier ? a.old[row] : 0.f;
-        const int from = max(0, pos - (s.kv_all - s.n));  // the first query that sees the key
+        float f = row >= 0 ? factor(row) : 1.f;
+        if (f == 0.f) f = 1.f;
+        const float before = row >= 0 && a.old && pos < s.kv_all - s.n ? a.old[row] : 0.f;
+        // of the thread's columns: the first that sees the key, and the end of the rows (the tile's heads of the
+        // sequence's queries, or where a query's heads fill tiles by themselves the rest of them)
+        int lo = (max(0, pos - (s.kv_all - s.n)) - block0 * a.tile_queries) * a.tile_heads - side * 64, part = 0;
+        int left = s.n - block0 * a.tile_queries;  // queries
         float total = 0.f;
         for (int i = 0; i < n_tiles; ++i) {
-            const int buf = i & 1, ls = i % LST;
-            bool ok = wait_phase(&s_full[g * 2 + buf], i >> 1 & 1, WAIT_NS) && wait_phase(&l_full[ls], i / LST & 1, WAIT_NS);
-            if (!__all_sync(0xffffffffu, ok)) {
+            const int buf = i & 1;
+            if (!__all_sync(0xffffffffu, mbar_wait(&s_full[g * 2 + buf], i >> 1 & 1, nullptr, WAIT_NS))) {
                 failed = true;
                 break;
             }
             tc_fence_after();
-            uint32_t sv[4][32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32_nowait(lane_addr + buf * 128 + c * 32, sv[c]);
-            tmem_wait_ld_only();
-#pragma unroll
-            for (int c = 0; c < 4; ++c) reg_fence32(sv[c]);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_free[g * 2 + buf]);
-            const uint4 mask = *reinterpret_cast<const uint4*>(s_mask + ls * 4);
-            const int lo = (from - (block0 + i / parts) * a.tile_queries) * a.tile_heads;  // columns before it do not see the key
-            const bool part = __any_sync(0xffffffffu, lo > 0) || (mask.x & mask.y & mask.z & mask.w) != 0xffffffffu;
-            const float4* l4 = reinterpret_cast<const float4*>(s_l + ls * RT);
+            const int there = parts > 1 ? min(cols, a.G - part * a.tile_heads) : min(cols, min(left, RT) * a.tile_heads), hi = there - side * 64;
+            const bool some = __any_sync(0xffffffffu, lo > 0) || there < cols;
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
-            const uint32_t masks[4] = {mask.x, mask.y, mask.z, mask.w};
-            auto weights = [&](auto some) {
+            // 32 columns at a time: with four warps a scheduler the others cover the load
+            auto weights = [&](auto masked) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t w[32];
+                    tmem_ld32_nowait(lane_addr + buf * 128 + c * 32, w);
+                    tmem_wait_ld_only();
+                    reg_fence32(w);
+                    if (c) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&s_free[g * 2 + buf]);
+                    }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        uint32_t* w = &sv[c][4 * e];
-                        const float4 l = l4[c * 8 + e];
-                        fma2(w[0], w[1], f, l.x, l.y);
-                        fma2(w[2], w[3], f, l.z, l.w);
+                    for (int e = 0; e < 32; e += 4) {
+                        mul2(w[e], w[e + 1], f);
+                        mul2(w[e + 2], w[e + 3], f);
                         float p[4];
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            p[x] = ex2_hw(__uint_as_float(w[x]));
-                            if (decltype(some)::value && (c * 32 + e * 4 + x < lo || !(masks[c] >> (e * 4 + x) & 1))) p[x] = 0.f;
+                            p[x] = ex2_hw(__uint_as_float(w[e + x]));
+                            if (decltype(masked)::value && (c * 32 + e + x < lo || c * 32 + e + x >= hi)) p[x] = 0.f;
                         }
                         add2(sum[0], sum[1], p[0], p[1]);
                         add2(sum[2], sum[3], p[2], p[3]);
                     }
                 }
             };
-            if (part) weights(std::true_type{});
+            if (some) weights(std::true_type{});
             else weights(std::false_type{});
             total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&l_empty[ls]);
+            if (++part == parts) part = 0, lo -= cols, left -= a.tile_queries;
         }
-        if (!failed && row >= 0) a.mass[row] = total + a.decay * before;
+        // the two sides of a key's columns join
+        float* other = reinterpret_cast<float*>(smem + L::JOIN) + g * RT + (warp & 3) * 32 + lane;
+        if (side) *other = total;
+        named_bar_sync(1 + g, 256);
+        if (!failed && !side && row >= 0) a.mass[row] = total + *other + a.decay * before;
     }
     if (failed) report(a.err, GK_ERR_TIMEOUT);
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == SUM_WARPS + 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -498,8 +544,9 @@ extern "C" gk_status gk_paged_mass(gk_ctx* ctx, const gk_paged_kv* cache, int dt
     GK_REQUIRE(ctx, q && lse && mass, GK_ERR_ARG, "gk_paged_mass: null pointer");
     GK_REQUIRE(ctx, dtype == GK_BF16, GK_ERR_UNSUPPORTED, "gk_paged_mass: dtype %d (GK_BF16 only)", dtype);
     a.scale_log2 = scale * 1.4426950408889634f;
-    GK_REQUIRE(ctx, H >= 1 && H <= 65535 && H % a.p.Hkv == 0 && max_q >= 1 && scale > 0.f && isfinite(a.scale_log2) && decay >= 0.f && isfinite(decay),
+    GK_REQUIRE(ctx, H >= 1 && H <= 65535 && H % a.p.Hkv == 0 && max_q >= 1 && scale > 0.f && isfinite(scale) && decay >= 0.f && isfinite(decay),
                GK_ERR_ARG, "gk_paged_mass: bad argument");
+    GK_REQUIRE(ctx, scale >= 0x1p-50f && scale <= 0x1p50f, GK_ERR_UNSUPPORTED, "gk_paged_mass: scale %g (2^-50 to 2^50)", (double)scale);
     GK_REQUIRE(ctx, ldq >= (int64_t)H * a.p.hs, GK_ERR_ARG, "gk_paged_mass: row stride");
     GK_REQUIRE(ctx, aligned16(q) && ldq % 8 == 0 && aligned16(old) && aligned16(mass), GK_ERR_ALIGN,
                "gk_paged_mass: rows and masses must be 16-byte aligned, strides a multiple of 8");

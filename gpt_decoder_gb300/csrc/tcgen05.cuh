@@ -78,6 +78,19 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint6
     return mbar_wait(bar, parity, nullptr, limit);
 }
 
+// Several at once: even a test of a completed phase takes hundreds of cycles behind the softmax warps' traffic
+// with the tensor memory, so the tests are sent together. (b and c only where asked.)
+__device__ __forceinline__ bool wait_phases(uint64_t* a, uint32_t pa, bool has_b, uint64_t* b, uint32_t pb, bool has_c, uint64_t* c,
+                                            uint32_t pc, uint64_t limit) {
+#pragma unroll 1
+    for (int i = 0; i < 4096; ++i) {
+        const uint32_t x = test_phase(a, pa), y = test_phase(has_b ? b : a, has_b ? pb : pa);
+        const uint32_t z = test_phase(has_c ? c : a, has_c ? pc : pa);
+        if (x & y & z) return true;
+    }
+    return mbar_wait(a, pa, nullptr, limit) && (!has_b || mbar_wait(b, pb, nullptr, limit)) && (!has_c || mbar_wait(c, pc, nullptr, limit));
+}
+
 __device__ __forceinline__ void tma_load_2d(const CUtensorMap* map, uint64_t* bar, void* dst, int x, int y) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
@@ -108,6 +121,13 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
     d |= (uint64_t)2 << 61;
     return d;
 }
+
+// The same with a 32-byte swizzle: rows of 32 bytes (one 16-deep step of bf16), 8 rows every 256 bytes, and the
+// place of a row's 16-byte chunk c (of 2).
+__device__ __forceinline__ uint64_t smem_desc32(uint32_t addr) {
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)1 << 16 | (uint64_t)(256 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)6 << 61;
+}
+__device__ __forceinline__ uint32_t swizzled32(int r, int c) { return (uint32_t)(r * 32 + ((c ^ (r >> 2 & 1)) << 4)); }
 
 // Byte offset of the 16 bytes at chunk c (of 8) of row r in a 128-byte-swizzled half tile.
 __device__ __forceinline__ uint32_t swizzled(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }

@@ -513,8 +513,10 @@ gk_status gk_paged_attn_shared(gk_ctx* ctx, const gk_paged_kv* cache, int dtype,
  *   first      device int32 [B] or NULL (0): positions below it are not weighed (a prefix that other sequences hold
  *              too). Two sequences of a call must not hold one row of a page at positions that are.
  *   dtype      GK_BF16 (q); else GK_ERR_UNSUPPORTED. max_q as for gk_paged_attn.
- * A row with lse = -inf gives no weight. Keys that a row does not see never reach its weights; a NaN among the
- * score and lse makes the mass of that key NaN. The sum's order is fixed: the same call gives the same bits. Only keys
+ *   scale      2^-50 to 2^50 (GK_ERR_UNSUPPORTED outside).
+ * A row whose lse is infinite gives no weight to keys of finite score. Keys that a row does not see never reach its
+ * weights; a NaN among the score and lse makes the mass of that key NaN. A key of 8-bit codes whose scale times `scale`
+ * is below 2^-61 scores zero. The sum's order is fixed: the same call gives the same bits. Only keys
  * are read (cache->v is not). */
 gk_status gk_paged_mass(gk_ctx* ctx, const gk_paged_kv* cache, int dtype, const void* q, int64_t ldq, const float* lse,
                         const float* old, float decay, float* mass, const int32_t* first, const int32_t* q_start,
