@@ -1,10 +1,14 @@
-// Internal interface of the attention over the paged cache: the arguments its kernels share, and
-// the partial results of sequences split over the GPU.
+// Internal interface of the attention over the paged cache: the arguments its kernels share, the partial
+// results of sequences split over the GPU, and what a block works on where sequences share prefixes.
 #pragma once
 
 #include "paged.cuh"
 
 namespace gk {
+
+// What the "sequences" of a launch are: whole sequences; the shared prefixes, each with the rows of its group's
+// sequences; or what follows the prefix in each sequence.
+enum { WHOLE, PREFIX, OWN };
 
 struct AttnArgs {
     Pages p;
@@ -19,6 +23,11 @@ struct AttnArgs {
     // with splits > 1 piece s of row r, head h leaves its weighted sum of values (not divided) in
     // part_o[(r * H + h) * splits + s][hs] and its reference and sum of weights in part_ml
     int splits, min_split;
+    // shared prefixes: groups of sequences (of `sequences` in all); B and max_q are those of the launch. A row's parts
+    // are `slots`, this launch's from slot0 on; the prefixes' are split by prefix_splits and prefix_min.
+    const int32_t* group_start;
+    const int32_t* prefix_len;
+    int n_groups, sequences, max_group, slots, slot0, prefix_splits, prefix_min;
     int clustered;  // the pieces are the blocks of one cluster, which joins them itself
     float* part_o;
     float2* part_ml;
@@ -30,17 +39,94 @@ struct AttnArgs {
     int64_t expanded_rows;
     int* err;
     CodeMasks masks;
-    __host__ __device__ int split_keys(int kv) const {
+    __host__ __device__ static int split_keys(int kv, int splits, int min_split) {
         const int even = (kv + splits - 1) / splits;
         return max(min_split, (even + 127) & ~127);
     }
+    __host__ __device__ int split_keys(int kv) const { return split_keys(kv, splits, min_split); }
 };
 
+// The group of sequence b, or -1.
+__device__ __forceinline__ int group_of(const AttnArgs& a, int b) {
+    int lo = 0, hi = a.n_groups;  // the last start that is not past b
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (__ldg(a.group_start + mid) <= b) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo < a.n_groups && __ldg(a.group_start + lo) <= b ? lo : -1;
+}
+// The first row and the number of rows of a group's sequences; false: it cannot be.
+__device__ __forceinline__ bool group_rows(const AttnArgs& a, int g, int& s0, int& n) {
+    const int first = __ldg(a.group_start + g), end = __ldg(a.group_start + g + 1);
+    n = 0;
+    if (first >= end) return true;
+    if (first < 0 || end > a.sequences) return false;
+    s0 = __ldg(a.q_start + first);
+    const int s1 = __ldg(a.q_start + end);
+    n = s1 - s0;
+    return s0 >= 0 && s1 <= a.rows && n <= a.max_group;
+}
+__device__ __forceinline__ int prefix_of(const AttnArgs& a, int g) { return min(max(__ldg(a.prefix_len + g), 0), a.p.capacity); }
+// The prefix that sequence b shares: 0 unless all of its rows lie behind it.
+__device__ __forceinline__ int shared_by(const AttnArgs& a, int b, int n, int kv_all) {
+    const int g = group_of(a, b);
+    const int prefix = g < 0 ? 0 : prefix_of(a, g);
+    return kv_all - n >= prefix ? prefix : 0;
+}
+
+// The rows and keys of a launch's sequence b: rows s0 .. s0 + n - 1, row i seeing the positions from `from` to
+// min(kv - 1, kv_all - n + i) in row `table` of the page table.
+struct Rows {
+    int s0, n, kv_all, kv, from, table;
+};
+template <int PART>
+__device__ __forceinline__ bool rows_of(const AttnArgs& a, int b, Rows& r) {
+    r.table = b;
+    r.from = 0;
+    bool fits;
+    if constexpr (PART == PREFIX) {
+        fits = group_rows(a, b, r.s0, r.n);
+        if (fits && r.n <= 0) return false;
+    } else {
+        r.s0 = a.q_start[b];
+        const int s1 = a.q_start[b + 1];
+        r.n = s1 - r.s0;
+        if (r.n <= 0) return false;
+        fits = r.n <= a.max_q && r.s0 >= 0 && s1 <= a.rows;
+    }
+    if (!fits) {
+        if (threadIdx.x == 0) report(a.err, GK_ERR_INDEX);
+        return false;
+    }
+    if constexpr (PART == PREFIX) {
+        r.table = __ldg(a.group_start + b);
+        r.kv = prefix_of(a, b);
+        r.kv_all = r.kv + r.n;  // every row lies behind it (rows of sequences that do not are not joined with it)
+        if (__ldg(a.prefix_len + b) > a.p.capacity && threadIdx.x == 0) report(a.err, GK_ERR_INDEX);
+        return r.kv > 0;
+    } else {
+        r.kv_all = max(a.p.kv_len[b], 0);
+        r.kv = min(r.kv_all, a.p.capacity);
+        if (r.kv_all > a.p.capacity && threadIdx.x == 0) report(a.err, GK_ERR_INDEX);
+        if constexpr (PART == OWN) r.from = shared_by(a, b, r.n, r.kv_all);
+        return true;
+    }
+}
+// Pieces are cut from a whole tile of 128 on.
+__device__ __forceinline__ int first_tile(int from) { return from & ~127; }
+
+// Refuse what no kernel could run on; fill `a` with the arguments.
+gk_status check_attn(gk_ctx* ctx, const char* what, const gk_paged_kv* cache, int dtype, const void* q, int64_t ldq, void* y, int64_t ldy,
+                     float* lse, const int32_t* q_start, int B, int H, int64_t rows, int max_q, float scale, AttnArgs* a);
 // Join the pieces of every (row, head).
 gk_status launch_attn_join(gk_ctx* ctx, const AttnArgs& a);
 // Sequences with at most 64 query rows per key / value head (32 where pages are bf16).
 gk_status launch_attn_few(gk_ctx* ctx, const AttnArgs& a);
 // Any number of rows, for heads head0 .. head0 + heads - 1, in tiles of 128 on the tensor cores (tcgen05).
 gk_status launch_attn_tiles(gk_ctx* ctx, const AttnArgs& a);
+// The same for the prefixes of groups (PREFIX) or what follows them (OWN), which leave parts, and their joining.
+gk_status launch_shared_few(gk_ctx* ctx, const AttnArgs& a, int part);
+gk_status launch_shared_tiles(gk_ctx* ctx, const AttnArgs& a, int part);
 
 }  // namespace gk

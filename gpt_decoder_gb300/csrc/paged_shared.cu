@@ -1,9 +1,102 @@
-// Attention of a batch whose sequences share prefixes: the entry point.
+// Attention of a batch whose sequences share prefixes: the entry point, the kernel for few rows (paged_attn_few.cuh) over
+// prefixes and what follows them, and the joining of a row's parts.
 // [LM4] = "Build a language model in C# from scratch (4): running GPT-2 weights", "Generation with
 // a KV cache" (the new tokens' queries against every cached position, no mask but the order).
+//
+// A softmax over two sets of keys is joined from each set's reference m, sum l and weighted values o (not divided):
+// y = (o_1 2^(m_1 - m) + o_2 2^(m_2 - m)) / (l_1 2^(m_1 - m) + l_2 2^(m_2 - m)), m the larger. So a group's prefix is
+// attended as one sequence that holds the rows of all of its sequences (they lie next to each other): with S sequences its
+// bytes are read once instead of S times, and the rows that meet a key are S times as many, which is what the tensor
+// cores need. Then each sequence attends to its own keys. Both are the kernels of gk_paged_attn.
+#include <math.h>
+
 #include <algorithm>
 
-#include "paged_attn.cuh"
+#include "paged_attn_few.cuh"
+
+namespace gk {
+namespace {
+
+template <int PART>
+gk_status launch_few(gk_ctx* ctx, const AttnArgs& a) {
+    if (a.p.hs <= 64) return a.p.k_scale ? few<64, true, PART>(ctx, a) : few<64, false, PART>(ctx, a);
+    return a.p.k_scale ? few<128, true, PART>(ctx, a) : few<128, false, PART>(ctx, a);
+}
+
+// A warp per (row, head), four dims a lane: the prefix's pieces, then its own keys'.
+constexpr int JOIN_WARPS = 8;
+__global__ void __launch_bounds__(JOIN_WARPS * 32) shared_join_kernel(const AttnArgs a) {
+    wait_for_earlier_kernels();
+    const int lane = threadIdx.x & 31;
+    const int64_t out = (int64_t)blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5);
+    const int r = (int)(out / a.H), h = (int)(out - (int64_t)r * a.H);
+    if (r >= a.rows) return;
+    const int b = find_sequence(a.q_start, a.B, r);
+    if (b < 0) return;
+    const int s0 = a.q_start[b], s1 = a.q_start[b + 1], n = s1 - s0, kv_all = max(a.p.kv_len[b], 0), kv = min(kv_all, a.p.capacity);
+    if (s0 < 0 || r < s0 || r >= s1 || n > a.max_q || s1 > a.rows) return;
+    int from = 0, from_prefix = 0;
+    const int g = group_of(a, b);
+    if (g >= 0) {
+        int gs, gn;
+        if (!group_rows(a, g, gs, gn)) return;  // left as they were
+        const int prefix = prefix_of(a, g);
+        if (kv_all - n >= prefix) {
+            from = prefix;
+            const int piece = AttnArgs::split_keys(prefix, a.prefix_splits, a.prefix_min);
+            from_prefix = (prefix + piece - 1) / piece;
+        }
+    }
+    const int keys = kv - first_tile(from), piece = a.split_keys(keys);
+    const int pieces = from_prefix + max(1, (keys + piece - 1) / piece), skip = a.slot0 - from_prefix;
+    const int per = a.p.hs >> 2;
+    const float2* ml = a.part_ml + out * a.slots;
+    const float4* po = reinterpret_cast<const float4*>(a.part_o + out * a.slots * a.p.hs) + min(lane, per - 1);
+    float top = -INFINITY;
+    for (int s = lane; s < pieces; s += 32) top = fmaxf(top, ml[s < from_prefix ? s : s + skip].x);
+    top = warp_max(top);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+#pragma unroll 8
+    for (int s = 0; s < pieces; ++s) {
+        const int at = s < from_prefix ? s : s + skip;
+        const float2 x = ml[at];
+        const float4 v = po[at * per];
+        // a piece in which the row sees nothing has sum 0 (or NaN, which stays) and no reference; its values are
+        // zeros. A factor that underflows still multiplies: what is not finite stays so.
+        const float c = x.x == -INFINITY ? (x.y == 0.f ? 0.f : 1.f) : ex2(x.x - top);
+        l += x.y * c;
+        o.x += v.x * c, o.y += v.y * c, o.z += v.z * c, o.w += v.w * c;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (lane < per)
+        *reinterpret_cast<uint2*>(a.y + (int64_t)r * a.ldy + h * a.p.hs + lane * 4) = make_uint2(pack(o.x * inv, o.y * inv), pack(o.z * inv, o.w * inv));
+    if (a.lse && lane == 0) a.lse[out] = l == 0.f ? -INFINITY : ((top == -INFINITY ? 0.f : top) + log2f(l)) * 0.6931471805599453f;
+}
+
+// Up to this many rows of a key / value head take the few-rows kernel (as for gk_paged_attn).
+bool is_few(const AttnArgs& a, int64_t rows) { return rows <= (a.p.k_scale ? 64 : 32); }
+
+// Pieces of a part's `units` (sequences or groups, heads, pairs of row tiles).
+void choose_splits(gk_ctx* ctx, bool few, int64_t units, int capacity, int64_t* splits, int* least) {
+    if (few) {
+        const bool alone = units < ctx->num_sms / 2;
+        *least = alone ? 128 : units < ctx->num_sms ? 256 : 1024;
+        *splits = cdiv((alone ? 4 : 16) * (int64_t)ctx->num_sms, units);
+    } else {
+        *least = 1024;
+        *splits = cdiv((int64_t)ctx->num_sms, units);
+    }
+    *splits = std::max<int64_t>(1, std::min(*splits, cdiv(capacity, *least)));
+}
+
+}  // namespace
+
+gk_status launch_shared_few(gk_ctx* ctx, const AttnArgs& a, int part) {
+    return part == PREFIX ? launch_few<PREFIX>(ctx, a) : launch_few<OWN>(ctx, a);
+}
+
+}  // namespace gk
 
 using namespace gk;
 
@@ -11,11 +104,65 @@ extern "C" gk_status gk_paged_attn_shared(gk_ctx* ctx, const gk_paged_kv* cache,
                                           int64_t ldy, float* lse, const int32_t* q_start, int B, const int32_t* group_start,
                                           const int32_t* prefix_len, int n_groups, int H, int64_t rows, int max_q, int max_group_q,
                                           float scale) {
-    if (!ctx) return GK_ERR_ARG;
+    AttnArgs a{};
+    GK_TRY(check_attn(ctx, "gk_paged_attn_shared", cache, dtype, q, ldq, y, ldy, lse, q_start, B, H, rows, max_q, scale, &a));
     GK_REQUIRE(ctx, group_start && prefix_len, GK_ERR_ARG, "gk_paged_attn_shared: null pointer");
     GK_REQUIRE(ctx, n_groups >= 1 && n_groups <= 65535 && max_group_q >= 1, GK_ERR_ARG, "gk_paged_attn_shared: bad groups");
-    if (cache && cache->Hkv > 0 && H > 0 && rows > 0)
-        GK_REQUIRE(ctx, std::min<int64_t>(max_group_q, rows) * (H / cache->Hkv) < (1ll << 30), GK_ERR_UNSUPPORTED,
-                   "gk_paged_attn_shared: groups of %d rows of %d heads a key / value head", max_group_q, H / cache->Hkv);
-    return gk_paged_attn(ctx, cache, dtype, q, ldq, y, ldy, lse, q_start, B, H, rows, max_q, scale);
+    GK_REQUIRE(ctx, std::min<int64_t>(max_group_q, rows) * a.G < (1ll << 30), GK_ERR_UNSUPPORTED,
+               "gk_paged_attn_shared: groups of %d rows of %d heads a key / value head", max_group_q, a.G);
+    if (rows == 0) return GK_OK;
+    a.group_start = group_start;
+    a.prefix_len = prefix_len;
+    a.n_groups = n_groups;
+    a.sequences = B;
+    a.max_group = (int)std::min<int64_t>(max_group_q, rows);
+    a.heads = a.p.Hkv;
+
+    const int64_t group_rows = (int64_t)a.max_group * a.G, own_rows = (int64_t)a.max_q * a.G, per = rows * H * (a.p.hs * 4 + 8);
+    const bool prefix_few = is_few(a, group_rows), own_few = is_few(a, own_rows);
+    char* ws = static_cast<char*>(ctx->ws);
+    size_t room = ctx->ws_bytes;
+    AttnArgs p = a;  // the prefixes' launch
+    p.B = n_groups;
+    p.max_q = a.max_group;
+    if (!prefix_few && a.p.k_scale && (a.p.hs > 64 || group_rows > 512)) {
+        // 8-bit codes laid out as bf16 first, as in gk_paged_attn: of the prefixes, all heads or a few at a time
+        const int64_t er = (int64_t)n_groups * cdiv(a.p.capacity, 128) * 128, bytes = er * a.p.hs * 2;  // of a head
+        const int64_t fit = (int64_t)(room / 2) >= bytes * a.p.Hkv ? a.p.Hkv : (int64_t)(room / 8 * 3) / bytes;
+        const int64_t turns = fit ? cdiv(a.p.Hkv, fit) : 0, heads = fit ? cdiv(a.p.Hkv, turns) : 0;
+        if (fit && er * heads < (1ll << 31) && (turns == 1 || 2 * heads * n_groups * cdiv(group_rows, 256) >= ctx->num_sms)) {
+            p.heads = (int)heads;
+            p.expanded_k = reinterpret_cast<__nv_bfloat16*>(ws);
+            p.expanded_v = reinterpret_cast<__nv_bfloat16*>(ws + bytes * heads);
+            p.expanded_rows = er * heads;
+            ws += 2 * bytes * heads;
+            room -= 2 * (size_t)(bytes * heads);
+        }
+    }
+    int64_t prefix_splits, own_splits;
+    choose_splits(ctx, prefix_few, (int64_t)n_groups * p.heads * (prefix_few ? 1 : cdiv(group_rows, 256)), a.p.capacity, &prefix_splits, &p.min_split);
+    choose_splits(ctx, own_few, (int64_t)B * a.p.Hkv * (own_few ? 1 : cdiv(own_rows, 256)), a.p.capacity, &own_splits, &a.min_split);
+    const int64_t slots = std::min<int64_t>(512, (int64_t)(room / per));
+    if (slots < 2) return gk_paged_attn(ctx, cache, dtype, q, ldq, y, ldy, lse, q_start, B, H, rows, max_q, scale);
+    prefix_splits = std::min(prefix_splits, std::max<int64_t>(1, slots * prefix_splits / (prefix_splits + own_splits)));
+    own_splits = std::min(own_splits, slots - prefix_splits);
+    p.splits = (int)prefix_splits;
+    a.splits = (int)own_splits;
+    a.prefix_splits = p.splits;
+    a.prefix_min = p.min_split;
+    a.slots = p.slots = p.splits + a.splits;
+    a.slot0 = p.splits;
+    a.part_o = p.part_o = reinterpret_cast<float*>(ws);
+    a.part_ml = p.part_ml = reinterpret_cast<float2*>(a.part_o + rows * H * a.slots * a.p.hs);
+    if (prefix_few) {
+        GK_TRY(launch_shared_few(ctx, p, PREFIX));
+    } else {
+        for (; p.head0 < a.p.Hkv; p.head0 += p.heads) {
+            p.heads = std::min(p.heads, a.p.Hkv - p.head0);
+            GK_TRY(launch_shared_tiles(ctx, p, PREFIX));
+        }
+    }
+    if (own_few) GK_TRY(launch_shared_few(ctx, a, OWN));
+    else GK_TRY(launch_shared_tiles(ctx, a, OWN));
+    return launch_dependent(ctx, "paged_shared_join", shared_join_kernel, dim3((unsigned)cdiv(rows * H, JOIN_WARPS)), dim3(JOIN_WARPS * 32), 0, 1, a);
 }

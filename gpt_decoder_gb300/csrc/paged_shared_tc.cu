@@ -1,0 +1,10 @@
+// Attention of many rows over shared prefixes, and over what follows them, on the tensor cores (paged_attn_tiles.cuh).
+#include "paged_attn_tiles.cuh"
+
+namespace gk {
+
+gk_status launch_shared_tiles(gk_ctx* ctx, const AttnArgs& a, int part) {
+    return part == PREFIX ? launch_tiles<PREFIX>(ctx, a) : launch_tiles<OWN>(ctx, a);
+}
+
+}  // namespace gk

@@ -333,6 +333,39 @@ def test_shared_infinities_and_nan(gkctx, S, n, H, Hkv, hs, q8):
     assert np.array_equal(np.isnan(lse), np.isnan(ref[1]))
 
 
+@pytest.mark.parametrize("n", [1, 3, 90])
+def test_shared_bad_pages_and_groups(gkctx, n):
+    from gpt_decoder_gb300 import gk
+
+    rng = np.random.default_rng(2500 + n)
+    c, ns, gs, prefix = shared_cache(rng, [(160, [(n + 9, n)] * 3), (96, [(n, n)] * 2)], 2, 64, 16, True)
+    q = serving.bf16(rng.standard_normal((sum(ns), 2, 64)))
+    want = shared_ref(c, q, ns, gs, prefix, 0.125)
+    # a table page of the first prefix that does not exist, in every row
+    good = c.table.copy()
+    c.table[:3, 2] = c.n_pages
+    y, lse = attend_shared(gkctx, c, q, ns, gs, prefix, 0.125, fails=True, d=Dev(c, poison=False))
+    check_attention(y, lse, shared_ref(c, q, ns, gs, prefix, 0.125))
+    c.table[:] = good
+    # sequences in no group, a group that shares nothing
+    for groups, lens in (([0, 2], [160]), ([0, 3, 5], [0, 96]), ([0, 3, 5], [-7, 500]), ([0, 0, 3], [96, 160])):
+        gs2, p2 = np.array(groups, np.int32), np.array(lens, np.int32)
+        past = 500 in lens
+        y, lse = attend_shared(gkctx, c, q, ns, gs2, p2, 0.125, fails=past)
+        check_attention(y, lse, want)
+    # groups that cannot be: their rows are left as they were; the others are right
+    for groups, lens, left, most in (([0, 3, 7], [160, 96], range(3, 5), 3 * n), ([0, 3, 5], [160, 96], range(0, 3), 3 * n - 1),
+                                     ([0, 3, 5], [160, 96], range(0), 3 * n)):
+        y, lse = attend_shared(gkctx, c, q, ns, np.array(groups, np.int32), np.array(lens, np.int32), 0.125, fails=bool(left), max_group=most)
+        for b in range(5):
+            rows = slice(b * n, b * n + n)
+            if b in left:
+                assert (y[rows] == 3).all() and (lse[rows] == 3).all()
+            else:
+                check_attention(y[rows], lse[rows], [w[rows] for w in want])
+    gk.gk_sync(gkctx)
+
+
 def test_mass_infinities_nan_and_refused_pages(gkctx):
     rng = np.random.default_rng(2600)
     for n, H, Hkv, hs in ((1, 4, 2, 64), (5, 2, 2, 128), (40, 2, 1, 64), (150, 2, 2, 64), (200, 1, 1, 128)):
