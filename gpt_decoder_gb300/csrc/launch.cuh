@@ -50,6 +50,9 @@ gk_status launch_dependent(gk_ctx* ctx, const char* what, void (*kernel)(KArgs..
     return launched(ctx, what);
 }
 __device__ __forceinline__ void wait_for_earlier_kernels() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Let the next launch begin once every block of this one has come here (it waits for this one's end all the same, where it
+// calls wait_for_earlier_kernels).
+__device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // (a & b) | c in one instruction. Only one operand of it can be a constant in the code: kernels that unpack
 // codes take their masks as arguments (CodeMasks), which stay in registers.

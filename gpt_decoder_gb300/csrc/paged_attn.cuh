@@ -28,6 +28,8 @@ struct AttnArgs {
     const int32_t* group_start;
     const int32_t* prefix_len;
     int n_groups, sequences, max_group, slots, slot0, prefix_splits, prefix_min;
+    int early;        // this launch does not depend on the one before it: see begin()
+    int2* row_parts;  // [rows]: pieces of the prefix and of a row's own keys; (0, 0): the row is left as it was
     int clustered;  // the pieces are the blocks of one cluster, which joins them itself
     float* part_o;
     float2* part_ml;
@@ -45,6 +47,22 @@ struct AttnArgs {
     }
     __host__ __device__ int split_keys(int kv) const { return split_keys(kv, splits, min_split); }
 };
+
+// Wait for the launches before this one, and let the next one begin. A launch that is `early` reads nothing of the one
+// directly before it (and that one has let it begin after its own wait, so all before are complete): its blocks go on at
+// once, and the last one along `last`, which has no other work, holds up the launch's end until the other's. True:
+// this is that block.
+template <int PART>
+__device__ __forceinline__ bool begin(const AttnArgs& a, bool last) {
+    if constexpr (PART == WHOLE) {
+        wait_for_earlier_kernels();
+        return false;
+    } else {
+        if (!a.early || last) wait_for_earlier_kernels();
+        let_next_begin();
+        return a.early && last;
+    }
+}
 
 // The group of sequence b, or -1.
 __device__ __forceinline__ int group_of(const AttnArgs& a, int b) {
@@ -116,6 +134,25 @@ __device__ __forceinline__ bool rows_of(const AttnArgs& a, int b, Rows& r) {
 // Pieces are cut from a whole tile of 128 on.
 __device__ __forceinline__ int first_tile(int from) { return from & ~127; }
 
+// Leave for the join what the rows of a sequence consist of (by the launch of own keys, a block a sequence).
+__device__ __forceinline__ void leave_row_parts(const AttnArgs& a, int b) {
+    const int s0 = a.q_start[b], s1 = a.q_start[b + 1], n = s1 - s0;
+    int2 parts = make_int2(0, 0);
+    if (n > 0 && n <= a.max_q && s0 >= 0 && s1 <= a.rows) {
+        const int kv_all = max(a.p.kv_len[b], 0), kv = min(kv_all, a.p.capacity), g = group_of(a, b);
+        int prefix = 0, gs, gn;
+        const bool there = g < 0 || group_rows(a, g, gs, gn);
+        if (g >= 0) prefix = prefix_of(a, g);
+        if (kv_all - n < prefix) prefix = 0;
+        if (there) {
+            const int keys = kv - first_tile(prefix), piece = a.split_keys(keys);
+            const int first = AttnArgs::split_keys(prefix, a.prefix_splits, a.prefix_min);
+            parts = make_int2((prefix + first - 1) / first, max(1, (keys + piece - 1) / piece));
+        }
+    }
+    for (int r = max(s0, 0) + threadIdx.x; r < min(s1, a.rows); r += blockDim.x) a.row_parts[r] = parts;
+}
+
 // Refuse what no kernel could run on; fill `a` with the arguments.
 gk_status check_attn(gk_ctx* ctx, const char* what, const gk_paged_kv* cache, int dtype, const void* q, int64_t ldq, void* y, int64_t ldy,
                      float* lse, const int32_t* q_start, int B, int H, int64_t rows, int max_q, float scale, AttnArgs* a);
@@ -125,8 +162,10 @@ gk_status launch_attn_join(gk_ctx* ctx, const AttnArgs& a);
 gk_status launch_attn_few(gk_ctx* ctx, const AttnArgs& a);
 // Any number of rows, for heads head0 .. head0 + heads - 1, in tiles of 128 on the tensor cores (tcgen05).
 gk_status launch_attn_tiles(gk_ctx* ctx, const AttnArgs& a);
-// The same for the prefixes of groups (PREFIX) or what follows them (OWN), which leave parts, and their joining.
+// The same for the prefixes of groups (PREFIX) or what follows them (OWN), which leave parts.
 gk_status launch_shared_few(gk_ctx* ctx, const AttnArgs& a, int part);
 gk_status launch_shared_tiles(gk_ctx* ctx, const AttnArgs& a, int part);
+// 8-bit codes of the prefixes as bf16, before the tiles that take them.
+gk_status launch_shared_expand(gk_ctx* ctx, const AttnArgs& a);
 
 }  // namespace gk

@@ -108,7 +108,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 28);
     uint64_t* s_free = bars + 29;    // [2] early S: S_g has been read (one arrival per warp)
     uint64_t* bar_pv = bars + 31;    // [2] early S: P_g V is complete
-    wait_for_earlier_kernels();
+    if (begin<PART>(a, blockIdx.z == gridDim.z - 1)) return;
+    if (PART == OWN && blockIdx.x == 0 && blockIdx.y == 0) leave_row_parts(a, blockIdx.z);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     Item it;
@@ -655,6 +656,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 template <int PART>
 __global__ void __launch_bounds__(256) expand_kernel(const AttnArgs a, __nv_bfloat16* k_out, __nv_bfloat16* v_out) {
     wait_for_earlier_kernels();
+    if constexpr (PART != WHOLE) let_next_begin();
     const int b = blockIdx.z, hk = a.head0 + blockIdx.y, len = expanded_rows<PART>(a, b), p0 = blockIdx.x * 64;
     if (p0 >= len) return;
     const int lane = threadIdx.x & 31, hs = a.p.hs;
@@ -693,8 +695,14 @@ gk_status tiles(gk_ctx* ctx, const AttnArgs& a, const __nv_bfloat16* k, const __
                    "gk_paged_attn: tensor map");
     const int64_t pairs = cdiv((int64_t)a.max_q * a.G, 2 * QT);
     return launch_dependent(ctx, "paged_attn_tiles", attn_tiles_kernel<HSP, FROM, PART>,
-                            dim3((unsigned)(pairs * a.splits), (unsigned)a.heads, (unsigned)a.B), dim3(THREADS), Layout<HSP>::BYTES, 1, a,
+                            dim3((unsigned)(pairs * a.splits), (unsigned)a.heads, (unsigned)a.B + (PART != WHOLE && a.early)), dim3(THREADS), Layout<HSP>::BYTES, 1, a,
                             mk, mv);
+}
+
+template <int PART>
+gk_status launch_expand(gk_ctx* ctx, const AttnArgs& a) {
+    return launch_dependent(ctx, "paged_attn_expand", expand_kernel<PART>, dim3((unsigned)cdiv(a.p.capacity, 128) * 2, (unsigned)a.heads, (unsigned)a.B),
+                            dim3(256), 0, 1, a, a.expanded_k, a.expanded_v);
 }
 
 template <int PART>
@@ -703,8 +711,7 @@ gk_status launch_tiles(gk_ctx* ctx, const AttnArgs& a) {
     if constexpr (PART != OWN)
     if (a.expanded_k) {
         const int64_t rows = a.expanded_rows;
-        GK_TRY(launch_dependent(ctx, "paged_attn_expand", expand_kernel<PART>, dim3((unsigned)cdiv(a.p.capacity, 128) * 2, (unsigned)a.heads, (unsigned)a.B),
-                                dim3(256), 0, 1, a, a.expanded_k, a.expanded_v));
+        if constexpr (PART == WHOLE) GK_TRY(launch_expand<PART>(ctx, a));  // (prefixes: launched before)
         return small ? tiles<64, EXPANDED, PART>(ctx, a, a.expanded_k, a.expanded_v, rows, KT)
                      : tiles<128, EXPANDED, PART>(ctx, a, a.expanded_k, a.expanded_v, rows, KT);
     }

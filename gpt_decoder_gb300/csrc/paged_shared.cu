@@ -23,51 +23,54 @@ gk_status launch_few(gk_ctx* ctx, const AttnArgs& a) {
     return a.p.k_scale ? few<128, true, PART>(ctx, a) : few<128, false, PART>(ctx, a);
 }
 
-// A warp per (row, head), four dims a lane: the prefix's pieces, then its own keys'.
+// A row and head: four dims a lane, the prefix's pieces and then its own keys'; with more than eight pieces 2, 4 or 8
+// warps of the block share them and add their sums in shared memory.
 constexpr int JOIN_WARPS = 8;
+__host__ __device__ constexpr int join_log2(int slots) { return slots <= 8 ? 0 : slots <= 16 ? 1 : slots <= 32 ? 2 : 3; }
 __global__ void __launch_bounds__(JOIN_WARPS * 32) shared_join_kernel(const AttnArgs a) {
+    __shared__ float4 s_o[JOIN_WARPS][32];
+    __shared__ float s_l[JOIN_WARPS];
     wait_for_earlier_kernels();
-    const int lane = threadIdx.x & 31;
-    const int64_t out = (int64_t)blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lg = join_log2(a.slots), share = 1 << lg, sub = warp & (share - 1);
+    const int64_t out = (int64_t)blockIdx.x * (JOIN_WARPS >> lg) + (warp >> lg);
     const int r = (int)(out / a.H), h = (int)(out - (int64_t)r * a.H);
-    if (r >= a.rows) return;
-    const int b = find_sequence(a.q_start, a.B, r);
-    if (b < 0) return;
-    const int s0 = a.q_start[b], s1 = a.q_start[b + 1], n = s1 - s0, kv_all = max(a.p.kv_len[b], 0), kv = min(kv_all, a.p.capacity);
-    if (s0 < 0 || r < s0 || r >= s1 || n > a.max_q || s1 > a.rows) return;
-    int from = 0, from_prefix = 0;
-    const int g = group_of(a, b);
-    if (g >= 0) {
-        int gs, gn;
-        if (!group_rows(a, g, gs, gn)) return;  // left as they were
-        const int prefix = prefix_of(a, g);
-        if (kv_all - n >= prefix) {
-            from = prefix;
-            const int piece = AttnArgs::split_keys(prefix, a.prefix_splits, a.prefix_min);
-            from_prefix = (prefix + piece - 1) / piece;
-        }
-    }
-    const int keys = kv - first_tile(from), piece = a.split_keys(keys);
-    const int pieces = from_prefix + max(1, (keys + piece - 1) / piece), skip = a.slot0 - from_prefix;
+    int2 parts = make_int2(0, 0);
+    if (r < a.rows && r >= a.q_start[0] && r < a.q_start[a.B]) parts = a.row_parts[r];
+    // (held to what there is, whatever a q_start that does not ascend has left)
+    const int first = min(max(parts.x, 0), a.slot0), pieces = first + min(max(parts.y, 0), a.slots - a.slot0), skip = a.slot0 - first;
     const int per = a.p.hs >> 2;
-    const float2* ml = a.part_ml + out * a.slots;
-    const float4* po = reinterpret_cast<const float4*>(a.part_o + out * a.slots * a.p.hs) + min(lane, per - 1);
     float top = -INFINITY;
-    for (int s = lane; s < pieces; s += 32) top = fmaxf(top, ml[s < from_prefix ? s : s + skip].x);
-    top = warp_max(top);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
+    if (pieces) {
+        const float2* ml = a.part_ml + out * a.slots;
+        const float4* po = reinterpret_cast<const float4*>(a.part_o + out * a.slots * a.p.hs) + min(lane, per - 1);
+        for (int s = lane; s < pieces; s += 32) top = fmaxf(top, ml[s < first ? s : s + skip].x);
+        top = warp_max(top);
 #pragma unroll 8
-    for (int s = 0; s < pieces; ++s) {
-        const int at = s < from_prefix ? s : s + skip;
-        const float2 x = ml[at];
-        const float4 v = po[at * per];
-        // a piece in which the row sees nothing has sum 0 (or NaN, which stays) and no reference; its values are
-        // zeros. A factor that underflows still multiplies: what is not finite stays so.
-        const float c = x.x == -INFINITY ? (x.y == 0.f ? 0.f : 1.f) : ex2(x.x - top);
-        l += x.y * c;
-        o.x += v.x * c, o.y += v.y * c, o.z += v.z * c, o.w += v.w * c;
+        for (int s = sub; s < pieces; s += share) {
+            const int at = s < first ? s : s + skip;
+            const float2 x = ml[at];
+            const float4 v = po[at * per];
+            // a piece in which the row sees nothing has sum 0 (or NaN, which stays) and no reference; its values are
+            // zeros. A factor that underflows still multiplies: what is not finite stays so.
+            const float c = x.x == -INFINITY ? (x.y == 0.f ? 0.f : 1.f) : ex2(x.x - top);
+            l += x.y * c;
+            o.x += v.x * c, o.y += v.y * c, o.z += v.z * c, o.w += v.w * c;
+        }
     }
+    if (lg) {
+        s_o[warp][lane] = o;
+        if (lane == 0) s_l[warp] = l;
+        __syncthreads();
+        if (sub) return;
+        for (int w = 1; w < share; ++w) {
+            const float4 v = s_o[warp + w][lane];
+            o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+            l += s_l[warp + w];
+        }
+    }
+    if (!pieces) return;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     if (lane < per)
         *reinterpret_cast<uint2*>(a.y + (int64_t)r * a.ldy + h * a.p.hs + lane * 4) = make_uint2(pack(o.x * inv, o.y * inv), pack(o.z * inv, o.w * inv));
@@ -119,6 +122,7 @@ extern "C" gk_status gk_paged_attn_shared(gk_ctx* ctx, const gk_paged_kv* cache,
     a.heads = a.p.Hkv;
 
     const int64_t group_rows = (int64_t)a.max_group * a.G, own_rows = (int64_t)a.max_q * a.G, per = rows * H * (a.p.hs * 4 + 8);
+    const size_t info = ((size_t)rows * sizeof(int2) + 15) & ~size_t(15);
     const bool prefix_few = is_few(a, group_rows), own_few = is_few(a, own_rows);
     char* ws = static_cast<char*>(ctx->ws);
     size_t room = ctx->ws_bytes;
@@ -142,7 +146,7 @@ extern "C" gk_status gk_paged_attn_shared(gk_ctx* ctx, const gk_paged_kv* cache,
     int64_t prefix_splits, own_splits;
     choose_splits(ctx, prefix_few, (int64_t)n_groups * p.heads * (prefix_few ? 1 : cdiv(group_rows, 256)), a.p.capacity, &prefix_splits, &p.min_split);
     choose_splits(ctx, own_few, (int64_t)B * a.p.Hkv * (own_few ? 1 : cdiv(own_rows, 256)), a.p.capacity, &own_splits, &a.min_split);
-    const int64_t slots = std::min<int64_t>(512, (int64_t)(room / per));
+    const int64_t slots = room < info ? 0 : std::min<int64_t>(512, (int64_t)((room - info) / per));
     if (slots < 2) return gk_paged_attn(ctx, cache, dtype, q, ldq, y, ldy, lse, q_start, B, H, rows, max_q, scale);
     prefix_splits = std::min(prefix_splits, std::max<int64_t>(1, slots * prefix_splits / (prefix_splits + own_splits)));
     own_splits = std::min(own_splits, slots - prefix_splits);
@@ -152,17 +156,25 @@ extern "C" gk_status gk_paged_attn_shared(gk_ctx* ctx, const gk_paged_kv* cache,
     a.prefix_min = p.min_split;
     a.slots = p.slots = p.splits + a.splits;
     a.slot0 = p.splits;
-    a.part_o = p.part_o = reinterpret_cast<float*>(ws);
+    a.row_parts = reinterpret_cast<int2*>(ws);
+    a.part_o = p.part_o = reinterpret_cast<float*>(ws + info);
     a.part_ml = p.part_ml = reinterpret_cast<float2*>(a.part_o + rows * H * a.slots * a.p.hs);
+    // Own keys beside the pass that lays out codes, or the prefixes beside own keys (their launches do not depend on
+    // each other, and each by itself leaves much of the GPU idle).
+    const bool expanded = p.expanded_k && p.heads == a.p.Hkv;
+    if (expanded) GK_TRY(launch_shared_expand(ctx, p));
+    a.early = expanded;
+    GK_TRY(own_few ? launch_shared_few(ctx, a, OWN) : launch_shared_tiles(ctx, a, OWN));
+    p.early = !p.expanded_k;
     if (prefix_few) {
         GK_TRY(launch_shared_few(ctx, p, PREFIX));
     } else {
         for (; p.head0 < a.p.Hkv; p.head0 += p.heads) {
             p.heads = std::min(p.heads, a.p.Hkv - p.head0);
+            if (p.expanded_k && !expanded) GK_TRY(launch_shared_expand(ctx, p));
             GK_TRY(launch_shared_tiles(ctx, p, PREFIX));
         }
     }
-    if (own_few) GK_TRY(launch_shared_few(ctx, a, OWN));
-    else GK_TRY(launch_shared_tiles(ctx, a, OWN));
-    return launch_dependent(ctx, "paged_shared_join", shared_join_kernel, dim3((unsigned)cdiv(rows * H, JOIN_WARPS)), dim3(JOIN_WARPS * 32), 0, 1, a);
+    return launch_dependent(ctx, "paged_shared_join", shared_join_kernel, dim3((unsigned)cdiv(rows * H, JOIN_WARPS >> join_log2(a.slots))),
+                            dim3(JOIN_WARPS * 32), 0, 1, a);
 }

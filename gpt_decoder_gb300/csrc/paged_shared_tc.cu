@@ -7,4 +7,6 @@ gk_status launch_shared_tiles(gk_ctx* ctx, const AttnArgs& a, int part) {
     return part == PREFIX ? launch_tiles<PREFIX>(ctx, a) : launch_tiles<OWN>(ctx, a);
 }
 
+gk_status launch_shared_expand(gk_ctx* ctx, const AttnArgs& a) { return launch_expand<PREFIX>(ctx, a); }
+
 }  // namespace gk
