@@ -64,16 +64,6 @@ __device__ __forceinline__ bool begin(const AttnArgs& a, bool last) {
     }
 }
 
-// The group of sequence b, or -1.
-__device__ __forceinline__ int group_of(const AttnArgs& a, int b) {
-    int lo = 0, hi = a.n_groups;  // the last start that is not past b
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (__ldg(a.group_start + mid) <= b) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo < a.n_groups && __ldg(a.group_start + lo) <= b ? lo : -1;
-}
 // The first row and the number of rows of a group's sequences; false: it cannot be.
 __device__ __forceinline__ bool group_rows(const AttnArgs& a, int g, int& s0, int& n) {
     const int first = __ldg(a.group_start + g), end = __ldg(a.group_start + g + 1);
@@ -85,10 +75,11 @@ __device__ __forceinline__ bool group_rows(const AttnArgs& a, int g, int& s0, in
     n = s1 - s0;
     return s0 >= 0 && s1 <= a.rows && n <= a.max_group;
 }
+// The part of a group's prefix that there is room for.
 __device__ __forceinline__ int prefix_of(const AttnArgs& a, int g) { return min(max(__ldg(a.prefix_len + g), 0), a.p.capacity); }
-// The prefix that sequence b shares: 0 unless all of its rows lie behind it.
+// The prefix that sequence b shares, by the whole warp: 0 unless all of its rows lie behind it.
 __device__ __forceinline__ int shared_by(const AttnArgs& a, int b, int n, int kv_all) {
-    const int g = group_of(a, b);
+    const int g = find_sequence(a.group_start, a.n_groups, b);
     const int prefix = g < 0 ? 0 : prefix_of(a, g);
     return kv_all - n >= prefix ? prefix : 0;
 }
@@ -134,12 +125,13 @@ __device__ __forceinline__ bool rows_of(const AttnArgs& a, int b, Rows& r) {
 // Pieces are cut from a whole tile of 128 on.
 __device__ __forceinline__ int first_tile(int from) { return from & ~127; }
 
-// Leave for the join what the rows of a sequence consist of (by the launch of own keys, a block a sequence).
+// Leave for the join what the rows of a sequence consist of (in the launch of own keys, by a block a sequence that has
+// no other work: the loads that it takes follow on each other).
 __device__ __forceinline__ void leave_row_parts(const AttnArgs& a, int b) {
     const int s0 = a.q_start[b], s1 = a.q_start[b + 1], n = s1 - s0;
     int2 parts = make_int2(0, 0);
     if (n > 0 && n <= a.max_q && s0 >= 0 && s1 <= a.rows) {
-        const int kv_all = max(a.p.kv_len[b], 0), kv = min(kv_all, a.p.capacity), g = group_of(a, b);
+        const int kv_all = max(a.p.kv_len[b], 0), kv = min(kv_all, a.p.capacity), g = find_sequence(a.group_start, a.n_groups, b);
         int prefix = 0, gs, gn;
         const bool there = g < 0 || group_rows(a, g, gs, gn);
         if (g >= 0) prefix = prefix_of(a, g);

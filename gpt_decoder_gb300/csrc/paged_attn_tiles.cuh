@@ -109,12 +109,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint64_t* s_free = bars + 29;    // [2] early S: S_g has been read (one arrival per warp)
     uint64_t* bar_pv = bars + 31;    // [2] early S: P_g V is complete
     if (begin<PART>(a, blockIdx.z == gridDim.z - 1)) return;
-    if (PART == OWN && blockIdx.x == 0 && blockIdx.y == 0) leave_row_parts(a, blockIdx.z);
+    if (PART == OWN && blockIdx.x == gridDim.x - 1) {
+        if (blockIdx.y == 0) leave_row_parts(a, blockIdx.z);
+        return;
+    }
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     Item it;
     {
-        const int pairs = gridDim.x / a.splits;
+        const int pairs = (gridDim.x - (PART == OWN)) / a.splits;
         // the last rows see the most keys: first; and pairs that read the same keys next to each other
         const int pair = pairs - 1 - blockIdx.x % pairs;
         it.split = blockIdx.x / pairs;
@@ -695,7 +698,7 @@ gk_status tiles(gk_ctx* ctx, const AttnArgs& a, const __nv_bfloat16* k, const __
                    "gk_paged_attn: tensor map");
     const int64_t pairs = cdiv((int64_t)a.max_q * a.G, 2 * QT);
     return launch_dependent(ctx, "paged_attn_tiles", attn_tiles_kernel<HSP, FROM, PART>,
-                            dim3((unsigned)(pairs * a.splits), (unsigned)a.heads, (unsigned)a.B + (PART != WHOLE && a.early)), dim3(THREADS), Layout<HSP>::BYTES, 1, a,
+                            dim3((unsigned)(pairs * a.splits + (PART == OWN)), (unsigned)a.heads, (unsigned)a.B + (PART != WHOLE && a.early)), dim3(THREADS), Layout<HSP>::BYTES, 1, a,
                             mk, mv);
 }
 

@@ -80,16 +80,20 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) shared_join_kernel(const Attn
 // Up to this many rows of a key / value head take the few-rows kernel (as for gk_paged_attn).
 bool is_few(const AttnArgs& a, int64_t rows) { return rows <= (a.p.k_scale ? 64 : 32); }
 
-// Pieces of a part's `units` (sequences or groups, heads, pairs of row tiles).
-void choose_splits(gk_ctx* ctx, bool few, int64_t units, int capacity, int64_t* splits, int* least) {
-    if (few) {
-        const bool alone = units < ctx->num_sms / 2;
-        *least = alone ? 128 : units < ctx->num_sms ? 256 : 1024;
-        *splits = cdiv((alone ? 4 : 16) * (int64_t)ctx->num_sms, units);
-    } else {
-        *least = 1024;
-        *splits = cdiv((int64_t)ctx->num_sms, units);
-    }
+// Pieces of the prefixes' `units` (groups, heads, pairs of row tiles). Few rows: four or sixteen blocks an SM, as
+// for gk_paged_attn, but pieces of 512 where there are some groups (7 of up to 8100 keys, 12 heads of 64: 44.5 us against
+// 50 with pieces of 256). Tiles: one wave, pieces of 256 at least.
+void split_prefixes(gk_ctx* ctx, bool few, int64_t units, int capacity, int64_t* splits, int* least) {
+    const bool alone = units < ctx->num_sms / 2;
+    *least = !few ? 256 : alone ? 128 : 512;
+    *splits = cdiv((!few ? 1 : alone ? 4 : 16) * (int64_t)ctx->num_sms, units);
+    *splits = std::max<int64_t>(1, std::min(*splits, cdiv(capacity, *least)));
+}
+// And of what follows them: mostly short, so pieces of 256 and two of them at most once they fill the GPU (64 sequences of
+// up to 1024 own keys, 8 heads: two pieces 85.3 us in all, five 87.2, five of 1024 93.7; 54 sequences 49.1, 50.2, 49.2).
+void split_own(gk_ctx* ctx, bool few, int64_t units, int capacity, int64_t* splits, int* least) {
+    *least = few ? (units < ctx->num_sms / 2 ? 128 : 256) : 1024;
+    *splits = few ? std::max<int64_t>(2, cdiv(4 * (int64_t)ctx->num_sms, units)) : cdiv((int64_t)ctx->num_sms, units);
     *splits = std::max<int64_t>(1, std::min(*splits, cdiv(capacity, *least)));
 }
 
@@ -114,6 +118,12 @@ extern "C" gk_status gk_paged_attn_shared(gk_ctx* ctx, const gk_paged_kv* cache,
     GK_REQUIRE(ctx, std::min<int64_t>(max_group_q, rows) * a.G < (1ll << 30), GK_ERR_UNSUPPORTED,
                "gk_paged_attn_shared: groups of %d rows of %d heads a key / value head", max_group_q, a.G);
     if (rows == 0) return GK_OK;
+    // Sharing costs two launches more and a join, and wins from prefixes of about 2000 positions and two sequences a group on
+    // (a token of 16 / 64 sequences, 12 heads of 64, prefixes of 250 / 1000 / 4000 / 16000: 10.5 / 12.6 / 14.8 / 24 us
+    // against 7 / 18 / 35 / 95 for each alone, and 19 / 27 / 29 / 45 against 14 / 36 / 96 / 324; 32 heads over 8 of 128,
+    // 64 sequences: 33 / 43 / 47 / 50 against 19 / 48 / 142 / 518; 2 sequences of 4000 / 16000: 12 / 17 against 12 / 20).
+    // The lengths are on the device; the table's width bounds them.
+    if (a.p.capacity < 2048 || 2 * (int64_t)n_groups > B) return gk_paged_attn(ctx, cache, dtype, q, ldq, y, ldy, lse, q_start, B, H, rows, max_q, scale);
     a.group_start = group_start;
     a.prefix_len = prefix_len;
     a.n_groups = n_groups;
@@ -144,8 +154,8 @@ extern "C" gk_status gk_paged_attn_shared(gk_ctx* ctx, const gk_paged_kv* cache,
         }
     }
     int64_t prefix_splits, own_splits;
-    choose_splits(ctx, prefix_few, (int64_t)n_groups * p.heads * (prefix_few ? 1 : cdiv(group_rows, 256)), a.p.capacity, &prefix_splits, &p.min_split);
-    choose_splits(ctx, own_few, (int64_t)B * a.p.Hkv * (own_few ? 1 : cdiv(own_rows, 256)), a.p.capacity, &own_splits, &a.min_split);
+    split_prefixes(ctx, prefix_few, (int64_t)n_groups * p.heads * (prefix_few ? 1 : cdiv(group_rows, 256)), a.p.capacity, &prefix_splits, &p.min_split);
+    split_own(ctx, own_few, (int64_t)B * a.p.Hkv * (own_few ? 1 : cdiv(own_rows, 256)), a.p.capacity, &own_splits, &a.min_split);
     const int64_t slots = room < info ? 0 : std::min<int64_t>(512, (int64_t)((room - info) / per));
     if (slots < 2) return gk_paged_attn(ctx, cache, dtype, q, ldq, y, ldy, lse, q_start, B, H, rows, max_q, scale);
     prefix_splits = std::min(prefix_splits, std::max<int64_t>(1, slots * prefix_splits / (prefix_splits + own_splits)));

@@ -52,6 +52,8 @@ def shared_cache(rng, groups, Hkv, hs, page, q8):
                         x[c.table[i, full], :, : p % page] = x[c.table[lead, full], :, : p % page]
         b += len(seqs)
     group_start = starts([len(s) for _, s in groups])
+    # room for 2048 positions: with less a call does not look at the groups
+    c.table = np.pad(c.table, ((0, 0), (0, max(0, 2048 // page - c.table.shape[1]))), constant_values=-1)
     return c, [n for _, _, n in tails], group_start, np.array([p for p, _ in groups], np.int32)
 
 
@@ -95,7 +97,7 @@ SHARED = [  # groups (prefix, [(own tokens or -1: a padding row, new rows)]), H,
     ([(2500, [(1, 1)] * 70), (100, [(200, 1)] * 65)], 1, 1, 64, 16),
     ([(513, [(70, 64), (65, 65), (300, 1)]), (128, [(128, 128)])], 2, 1, 64, 64),
     ([(300, [(40, 40), (60, 33), (200, 129)])], 6, 3, 96, 32),
-    ([(1500, [(260, 200), (333, 257)]), (2, [(700, 600)])], 2, 2, 128, 256),
+    ([(1500, [(260, 200), (333, 257)]), (2, [(700, 600), (4, 3)])], 2, 2, 128, 256),
     ([(5000, [(37, 5)] * 12), (6000, [(-1, 2), (9, 9)])], 4, 4, 32, 16),
     ([(200, [(3, 3), (500, 40)]), (9000, [(1, 1), (2, 2)] * 4)], 16, 2, 48, 128),
 ]
@@ -104,13 +106,17 @@ SHARED = [  # groups (prefix, [(own tokens or -1: a padding row, new rows)]), H,
 @pytest.mark.parametrize("q8", [False, True])
 @pytest.mark.parametrize("case", range(len(SHARED)))
 def test_shared_prefixes(gkctx, case, q8):
+    """Each also with no more room in the table than there are tokens, where short prefixes are not shared."""
     groups, H, Hkv, hs, page = SHARED[case]
     rng = np.random.default_rng(2000 + case)
     c, n, gs, prefix = shared_cache(rng, groups, Hkv, hs, page, q8)
     q = serving.bf16(rng.standard_normal((sum(n), H, hs)) * 2)
     scale = 1 / math.sqrt(hs)
-    y, lse = attend_shared(gkctx, c, q, n, gs, prefix, scale, extra_rows=case % 3, pad=8 * (case % 2))
-    check_attention(y, lse, shared_ref(c, q, n, gs, prefix, scale))
+    ref = shared_ref(c, q, n, gs, prefix, scale)
+    assert 2 * len(prefix) <= len(n)
+    check_attention(*attend_shared(gkctx, c, q, n, gs, prefix, scale, extra_rows=case % 3, pad=8 * (case % 2)), ref)
+    c.table = np.ascontiguousarray(c.table[:, : -(-int(c.kv_len.max()) // page)])
+    check_attention(*attend_shared(gkctx, c, q, n, gs, prefix, scale), ref)
 
 
 # ---------------------------------------------------------------------------------------------- mass
@@ -348,9 +354,9 @@ def test_shared_bad_pages_and_groups(gkctx, n):
     check_attention(y, lse, shared_ref(c, q, ns, gs, prefix, 0.125))
     c.table[:] = good
     # sequences in no group, a group that shares nothing
-    for groups, lens in (([0, 2], [160]), ([0, 3, 5], [0, 96]), ([0, 3, 5], [-7, 500]), ([0, 0, 3], [96, 160])):
+    for groups, lens in (([0, 2], [160]), ([0, 3, 5], [0, 96]), ([0, 3, 5], [-7, 5000]), ([0, 0, 3], [96, 160])):
         gs2, p2 = np.array(groups, np.int32), np.array(lens, np.int32)
-        past = 500 in lens
+        past = 5000 in lens
         y, lse = attend_shared(gkctx, c, q, ns, gs2, p2, 0.125, fails=past)
         check_attention(y, lse, want)
     # groups that cannot be: their rows are left as they were; the others are right
@@ -452,14 +458,14 @@ def test_sampling_from_a_prompt_under_a_budget(gkctx, q8):
     groups = [(37, [(20, 1)] * 3), (80, [(20, 1)] * 3)]
     c, _, gs, prefix = shared_cache(rng, groups, Hkv, hs, page, q8)
     # room for all that is to come: every sequence has two sets of pages behind its prefix's whole ones
-    width, spare = 8, 60
+    width, spare, room = 8, 60, c.table.shape[1]
     grow = lambda x: None if x is None else np.concatenate([x, np.zeros((spare, *x.shape[1:]), x.dtype)])  # noqa: E731
     free = list(range(c.n_pages, c.n_pages + spare))
     c.k, c.v, c.k_scale, c.v_scale = (grow(x) for x in (c.k, c.v, c.k_scale, c.v_scale))
     c.n_pages = c.k.shape[0]
     full = [int(p) // page for p in first]
-    table = np.full((B, width), -1, np.int32)
-    table[:, : c.table.shape[1]] = c.table
+    table = c.table.copy()
+    assert table.shape == (B, room) and room * page >= 2048
     for b in range(B):
         for j in range(-(-int(c.kv_len[b]) // page), width):
             table[b, j] = free.pop()
