@@ -79,6 +79,14 @@ __device__ __forceinline__ uint32_t load_cluster_u32(const void* p, int rank) {
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at));
     return v;
 }
+// Four words (16-byte aligned) of block `rank`.
+__device__ __forceinline__ uint4 load_cluster_u32x4(const void* p, int rank) {
+    uint32_t at;
+    uint4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
+}
 __device__ __forceinline__ float load_cluster(const float* p, int rank) { return __uint_as_float(load_cluster_u32(p, rank)); }
 
 }  // namespace gk

@@ -2,9 +2,11 @@
 // [LM4] = "Build a language model in C# from scratch (4): running GPT-2 weights", "Generation with
 // a KV cache" (the cache that grows by a row a token; here it is held to a size).
 //
-// Two launches. Select: per sequence and key / value head the n-th largest mass by its bits, eight at a time
-// (a histogram of the digit among what still matches), then one walk in order that writes down the positions
-// that stay. Move: those rows, with scales and mass, a tile of tokens a block.
+// Two launches. Select: a cluster of blocks per sequence and key / value head holds the head's masses in shared memory, as
+// integers that order like them, and finds the n-th largest by its bits: three digits of 11, 11 and 10 bits, for each a
+// histogram of what still matches, summed over the cluster through distributed shared memory. Then each warp counts what
+// stays of its stretch of positions and walks it, so the positions come out in order without a sort: keys above the
+// n-th, and the first of those equal to it. Move: those rows, with scales and mass, a tile of tokens a block.
 #include <math.h>
 
 #include <algorithm>
@@ -52,72 +54,147 @@ __device__ __forceinline__ int64_t row_at(const Pages& p, int b, int hk, int pos
     return (((int64_t)id * p.Hkv + hk) << p.page_log2) + (pos & ((1 << p.page_log2) - 1));
 }
 
-constexpr int SELECT = 1024;
+constexpr int SELECT = 512, SELECT_WARPS = SELECT / 32, BINS = 2048, MAX_CLUSTER = 8;
+constexpr int HELD = 48 * 1024;  // masses that a block can hold
 
-__global__ void __launch_bounds__(SELECT) evict_select_kernel(const EvictArgs a) {
-    __shared__ int s_hist[256];
-    __shared__ uint2 s_warp[SELECT / 32];
+// `each`: positions of a block, a multiple of 128. HOLD: they are kept in shared memory (else read again each time).
+template <bool HOLD>
+__global__ void __launch_bounds__(SELECT) evict_select_kernel(const EvictArgs a, int each_most) {
+    extern __shared__ __align__(16) uint32_t s_keys[];
+    __shared__ __align__(16) uint32_t s_hist[3][BINS];
+    __shared__ uint2 s_warp[SELECT_WARPS], s_mine;
+    __shared__ uint32_t s_sum[SELECT_WARPS];
     __shared__ int s_digit, s_left;
     wait_for_earlier_kernels();
-    const int b = blockIdx.y, hk = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int blocks = gridDim.x, rank = blockIdx.x, b = blockIdx.z, hk = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Cut c = cut_of(a, b);
     int32_t* kept = a.kept + ((int64_t)b * a.from.Hkv + hk) * a.budget;
-    if (hk == 0 && tid == 0) {
+    if (hk == 0 && rank == 0 && tid == 0) {
         a.new_len[b] = c.first + min(c.behind, a.budget);
         if (a.from.kv_len[b] > a.from.capacity) report(a.err, GK_ERR_INDEX);
     }
-    if (c.behind <= a.budget) {
-        for (int i = tid; i < a.budget; i += SELECT) kept[i] = i < c.behind ? c.first + i : -1;
+    if (c.behind <= a.budget) {  // (all blocks of the cluster)
+        for (int i = rank * SELECT + tid; i < a.budget; i += blocks * SELECT) kept[i] = i < c.behind ? c.first + i : -1;
         return;
     }
-    const int need = a.budget - a.recent, n = c.behind - a.recent;  // the heaviest `need` of n: 0 <= need < n
-    auto key = [&](int i) {
-        const int64_t r = row_at(a.from, b, hk, c.first + i);
-        if (r < 0) report(a.err, GK_ERR_INDEX);
-        return ordered(r < 0 ? -INFINITY : a.mass[r]);
+    const int need = a.budget - a.recent, end = c.kv - a.recent;  // the heaviest `need` of positions first .. end - 1
+    for (int i = rank * SELECT + tid; i < a.recent; i += blocks * SELECT) kept[need + i] = end + i;
+    if (need == 0) return;
+    auto barrier = [&]() {
+        __syncwarp();
+        if (blocks > 1) cluster_barrier();
+        else __syncthreads();
     };
+
+    // this block's positions p0 .. p0 + each - 1, four at a time (they share a page); 0: not one to choose from
+    const int base = c.first & ~127, each = min(each_most, ((end - base + blocks - 1) / blocks + 127) & ~127), p0 = base + rank * each;
+    auto load4 = [&](int i) {
+        uint4 k = make_uint4(0, 0, 0, 0);
+        const int pos = p0 + i;
+        if (pos < end) {
+            const int64_t r = row_at(a.from, b, hk, pos);
+            float4 m = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            if (r >= 0) m = __ldg(reinterpret_cast<const float4*>(a.mass + r));
+            else report(a.err, GK_ERR_INDEX);
+            k.x = pos >= c.first ? ordered(m.x) : 0;
+            k.y = pos + 1 >= c.first && pos + 1 < end ? ordered(m.y) : 0;
+            k.z = pos + 2 >= c.first && pos + 2 < end ? ordered(m.z) : 0;
+            k.w = pos + 3 >= c.first && pos + 3 < end ? ordered(m.w) : 0;
+        }
+        return k;
+    };
+    for (int i = tid; i < 3 * BINS; i += SELECT) (&s_hist[0][0])[i] = 0;
+    if (HOLD) {
+#pragma unroll 4
+        for (int i = tid * 4; i < each; i += SELECT * 4) *reinterpret_cast<uint4*>(s_keys + i) = load4(i);
+    }
+    __syncthreads();
     uint32_t top = 0;  // the digits found so far
     int left = need;   // how many of the keys that match them stay
-    for (int shift = 24; shift >= 0 && need; shift -= 8) {
-        if (tid < 256) s_hist[tid] = 0;
-        __syncthreads();
-        for (int i = tid; i < n; i += SELECT) {
-            const uint32_t k = key(i);
-            if (shift == 24 || k >> (shift + 8) == top >> (shift + 8)) atomicAdd(&s_hist[k >> shift & 255], 1);
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+        for (int i = tid * 4; i < each; i += SELECT * 4) {
+            const uint4 k4 = HOLD ? *reinterpret_cast<const uint4*>(s_keys + i) : load4(i);
+            const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (k[e] && (pass == 0 || k[e] >> (shift + bits) == top >> (shift + bits))) atomicAdd(&s_hist[pass][k[e] >> shift & ((1 << bits) - 1)], 1u);
         }
+        barrier();
+        // four bins a thread, from the highest down: which of them holds the left-th key
+        static_assert(SELECT * 4 == BINS, "four bins a thread");
+        const int first_bin = BINS - 4 - 4 * tid;
+        uint4 h = make_uint4(0, 0, 0, 0);
+        for (int r = 0; r < blocks; ++r) {
+            const uint4 x = blocks > 1 ? load_cluster_u32x4(&s_hist[pass][first_bin], r) : *reinterpret_cast<const uint4*>(&s_hist[pass][first_bin]);
+            h.x += x.x, h.y += x.y, h.z += x.z, h.w += x.w;
+        }
+        const uint32_t mine = h.x + h.y + h.z + h.w;
+        uint32_t run = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += y;
+        }
+        if (lane == 31) s_sum[warp] = run;
         __syncthreads();
-        if (tid == 0) {
-            int d = 255, sum = 0;
-            while (d > 0 && sum + s_hist[d] < left) sum += s_hist[d--];
-            s_digit = d;
-            s_left = left - sum;
+        uint32_t before = run - mine;  // keys in higher bins
+        for (int w = 0; w < warp; ++w) before += s_sum[w];
+        if (before < (uint32_t)left && before + mine >= (uint32_t)left) {
+            const uint32_t n[4] = {h.w, h.z, h.y, h.x};
+            int d = 0;
+            while (d < 3 && before + n[d] < (uint32_t)left) before += n[d++];
+            s_digit = first_bin + 3 - d;
+            s_left = left - (int)before;
         }
         __syncthreads();
         top |= (uint32_t)s_digit << shift;
         left = s_left;
-        __syncthreads();
     }
-    // in order: keys above `top`, and the first `left` of those equal to it
-    uint2 base = make_uint2(0, 0);  // (above, equal) before this round
-    for (int i0 = 0; i0 < n && need; i0 += SELECT) {
-        const int i = i0 + tid;
-        const uint32_t k = i < n ? key(i) : 0;
-        const bool more = i < n && k > top, same = i < n && k == top;
-        const unsigned m = __ballot_sync(0xffffffffu, more), e = __ballot_sync(0xffffffffu, same);
-        if (lane == 0) s_warp[warp] = make_uint2(__popc(m), __popc(e));
-        __syncthreads();
-        uint2 at = base;
-        for (int w = 0; w < SELECT / 32; ++w) {
-            const uint2 x = s_warp[w];
-            if (w < warp) at.x += x.x, at.y += x.y;
-            base.x += x.x, base.y += x.y;
+    // each warp's stretch of the block: what stays of it, and where it goes
+    const int stretch = ((each + SELECT_WARPS - 1) / SELECT_WARPS + 127) & ~127, w0 = min(warp * stretch, each), w1 = min(w0 + stretch, each);
+    uint2 n = make_uint2(0, 0);  // keys above `top`, and equal to it
+    for (int i = w0 + lane * 4; i < w1; i += 128) {
+        const uint4 k = HOLD ? *reinterpret_cast<const uint4*>(s_keys + i) : load4(i);
+        n.x += (k.x > top) + (k.y > top) + (k.z > top) + (k.w > top);
+        n.y += (k.x == top) + (k.y == top) + (k.z == top) + (k.w == top);
+    }
+    for (int o = 16; o > 0; o >>= 1) n.x += __shfl_xor_sync(0xffffffffu, n.x, o), n.y += __shfl_xor_sync(0xffffffffu, n.y, o);
+    if (lane == 0) s_warp[warp] = n;
+    __syncthreads();
+    uint2 at = make_uint2(0, 0), all = at;
+    for (int w = 0; w < SELECT_WARPS; ++w) {
+        const uint2 x = s_warp[w];
+        if (w < warp) at.x += x.x, at.y += x.y;
+        all.x += x.x, all.y += x.y;
+    }
+    if (blocks > 1) {
+        if (tid == 0) s_mine = all;
+        barrier();
+        for (int r = 0; r < rank; ++r) at.x += load_cluster_u32(&s_mine.x, r), at.y += load_cluster_u32(&s_mine.y, r);
+    }
+    for (int i = w0; i < w1; i += 128) {
+        const uint4 k4 = HOLD ? *reinterpret_cast<const uint4*>(s_keys + i + lane * 4) : load4(i + lane * 4);
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+        // the lane's four keys follow those of the lanes below it
+        uint32_t above = 0, same = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) above += k[e] > top, same += k[e] == top;
+        uint32_t both = above | same << 16;
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, both, o);
+            if (lane >= o) both += y;
         }
-        const unsigned below = (1u << lane) - 1;
-        at.x += __popc(m & below), at.y += __popc(e & below);
-        if (more || (same && (int)at.y < left)) kept[at.x + min((int)at.y, left)] = c.first + i;
-        __syncthreads();
+        uint32_t x = at.x + (both & 0xffff) - above, y = at.y + (both >> 16) - same;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (k[e] > top || (k[e] == top && (int)y < left)) kept[x + min((int)y, left)] = p0 + i + lane * 4 + e;
+            x += k[e] > top, y += k[e] == top;
+        }
+        const uint32_t total = __shfl_sync(0xffffffffu, both, 31);
+        at.x += total & 0xffff, at.y += total >> 16;
     }
-    for (int i = tid; i < a.recent; i += SELECT) kept[need + i] = c.kv - a.recent + i;
+    if (blocks > 1) barrier();  // no block ends while another reads its words
 }
 
 // A block moves TOKENS of the kept tokens, and its share of the first ones: 16-byte pieces of keys and values.
@@ -195,7 +272,17 @@ extern "C" gk_status gk_paged_evict(gk_ctx* ctx, const gk_paged_kv* cache, const
     a.new_len = new_len;
     a.kept = kept;
     a.err = ctx->d_err;
-    GK_TRY(launch_dependent(ctx, "paged_evict_select", evict_select_kernel, dim3((unsigned)a.from.Hkv, (unsigned)B), dim3(SELECT), 0, 1, a));
+    // Blocks of a cluster: of about 4096 positions each.
+    int blocks = 1;
+    while (blocks < MAX_CLUSTER && a.from.capacity > 4096 * blocks) blocks *= 2;
+    const int each = (int)((cdiv(a.from.capacity, blocks) + 255) & ~int64_t(127));
+    const dim3 grid((unsigned)blocks, (unsigned)a.from.Hkv, (unsigned)B);
+    if (each <= HELD) {
+        GK_TRY((allow_shared<evict_select_kernel<true>>(ctx, "gk_paged_evict", HELD * sizeof(uint32_t))));
+        GK_TRY(launch_dependent(ctx, "paged_evict_select", evict_select_kernel<true>, grid, dim3(SELECT), each * sizeof(uint32_t), blocks, a, each));
+    } else {
+        GK_TRY(launch_dependent(ctx, "paged_evict_select", evict_select_kernel<false>, grid, dim3(SELECT), 0, blocks, a, each));
+    }
     const int64_t tiles = cdiv(std::min(budget, a.from.capacity), TOKENS);
     return launch_dependent(ctx, "paged_evict_move", evict_move_kernel, dim3((unsigned)tiles, (unsigned)a.from.Hkv, (unsigned)B), dim3(MOVE), 0, 1, a);
 }
