@@ -61,7 +61,8 @@ constexpr int HELD = 48 * 1024;  // masses that a block can hold
 template <bool HOLD>
 __global__ void __launch_bounds__(SELECT) evict_select_kernel(const EvictArgs a, int each_most) {
     extern __shared__ __align__(16) uint32_t s_keys[];
-    __shared__ __align__(16) uint32_t s_hist[3][BINS];
+    __shared__ __align__(16) uint32_t s_hist[3][BINS], s_total[BINS / 2];
+    __shared__ uint32_t s_share[3];
     __shared__ uint2 s_warp[SELECT_WARPS], s_mine;
     __shared__ uint32_t s_sum[SELECT_WARPS];
     __shared__ int s_digit, s_left;
@@ -88,25 +89,39 @@ __global__ void __launch_bounds__(SELECT) evict_select_kernel(const EvictArgs a,
 
     // this block's positions p0 .. p0 + each - 1, four at a time (they share a page); 0: not one to choose from
     const int base = c.first & ~127, each = min(each_most, ((end - base + blocks - 1) / blocks + 127) & ~127), p0 = base + rank * each;
-    auto load4 = [&](int i) {
-        uint4 k = make_uint4(0, 0, 0, 0);
-        const int pos = p0 + i;
-        if (pos < end) {
-            const int64_t r = row_at(a.from, b, hk, pos);
-            float4 m = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-            if (r >= 0) m = __ldg(reinterpret_cast<const float4*>(a.mass + r));
-            else report(a.err, GK_ERR_INDEX);
-            k.x = pos >= c.first ? ordered(m.x) : 0;
-            k.y = pos + 1 >= c.first && pos + 1 < end ? ordered(m.y) : 0;
-            k.z = pos + 2 >= c.first && pos + 2 < end ? ordered(m.z) : 0;
-            k.w = pos + 3 >= c.first && pos + 3 < end ? ordered(m.w) : 0;
-        }
-        return k;
+    bool missing = false;
+    auto row4 = [&](int i) -> int64_t {
+        if (i >= each || p0 + i >= end) return -1;
+        const int64_t r = row_at(a.from, b, hk, p0 + i);
+        missing |= r < 0;
+        return r;
     };
+    auto mass4 = [&](int64_t r) {
+        return r >= 0 ? __ldg(reinterpret_cast<const float4*>(a.mass + r)) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    };
+    auto keys4 = [&](int i, const float4& m) {
+        const int pos = p0 + i;
+        return make_uint4(pos >= c.first && pos < end ? ordered(m.x) : 0, pos + 1 >= c.first && pos + 1 < end ? ordered(m.y) : 0,
+                          pos + 2 >= c.first && pos + 2 < end ? ordered(m.z) : 0, pos + 3 >= c.first && pos + 3 < end ? ordered(m.w) : 0);
+    };
+    auto load4 = [&](int i) { return keys4(i, mass4(row4(i))); };
     for (int i = tid; i < 3 * BINS; i += SELECT) (&s_hist[0][0])[i] = 0;
+    if (tid < 3) s_share[tid] = 0;
     if (HOLD) {
-#pragma unroll 4
-        for (int i = tid * 4; i < each; i += SELECT * 4) *reinterpret_cast<uint4*>(s_keys + i) = load4(i);
+        constexpr int AHEAD = 4;  // page ids, then masses, of this many places on their way together
+        for (int i0 = tid * 4; i0 < each; i0 += AHEAD * SELECT * 4) {
+            int64_t r[AHEAD];
+            float4 m[AHEAD];
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) r[u] = row4(i0 + u * SELECT * 4);
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) m[u] = mass4(r[u]);
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                const int i = i0 + u * SELECT * 4;
+                if (i < each) *reinterpret_cast<uint4*>(s_keys + i) = keys4(i, m[u]);
+            }
+        }
     }
     __syncthreads();
     uint32_t top = 0;  // the digits found so far
@@ -124,11 +139,35 @@ __global__ void __launch_bounds__(SELECT) evict_select_kernel(const EvictArgs a,
         barrier();
         // four bins a thread, from the highest down: which of them holds the left-th key
         static_assert(SELECT * 4 == BINS, "four bins a thread");
-        const int first_bin = BINS - 4 - 4 * tid;
+        int first_bin = BINS - 4 - 4 * tid;
         uint4 h = make_uint4(0, 0, 0, 0);
-        for (int r = 0; r < blocks; ++r) {
-            const uint4 x = blocks > 1 ? load_cluster_u32x4(&s_hist[pass][first_bin], r) : *reinterpret_cast<const uint4*>(&s_hist[pass][first_bin]);
-            h.x += x.x, h.y += x.y, h.z += x.z, h.w += x.w;
+        uint32_t higher = 0;  // keys in the bins of higher shares
+        if (blocks == 1) {
+            h = *reinterpret_cast<const uint4*>(&s_hist[pass][first_bin]);
+        } else {
+            // each block sums a share of the bins over the cluster; then all look at the share that holds the key (all bins
+            // of all blocks read by each took 3 to 5 us a digit, 8 blocks)
+            const int share = BINS / blocks;
+            if (tid * 4 < share) {
+                for (int r = 0; r < blocks; ++r) {
+                    const uint4 x = load_cluster_u32x4(&s_hist[pass][rank * share + tid * 4], r);
+                    h.x += x.x, h.y += x.y, h.z += x.z, h.w += x.w;
+                }
+                *reinterpret_cast<uint4*>(s_total + tid * 4) = h;
+                uint32_t sum = h.x + h.y + h.z + h.w;
+                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (lane == 0) atomicAdd(&s_share[pass], sum);
+            }
+            barrier();
+            uint32_t n[MAX_CLUSTER];
+#pragma unroll
+            for (int r = 0; r < MAX_CLUSTER; ++r) n[r] = r < blocks ? load_cluster_u32(&s_share[pass], r) : 0;
+            int owner = MAX_CLUSTER - 1;
+#pragma unroll
+            for (int r = MAX_CLUSTER - 1; r > 0; --r)
+                if (owner == r && higher + n[r] < (uint32_t)left) higher += n[r], owner = r - 1;
+            first_bin = owner * share + share - 4 - 4 * tid;
+            h = tid * 4 < share ? load_cluster_u32x4(s_total + share - 4 - 4 * tid, owner) : make_uint4(0, 0, 0, 0);
         }
         const uint32_t mine = h.x + h.y + h.z + h.w;
         uint32_t run = mine;
@@ -138,7 +177,7 @@ __global__ void __launch_bounds__(SELECT) evict_select_kernel(const EvictArgs a,
         }
         if (lane == 31) s_sum[warp] = run;
         __syncthreads();
-        uint32_t before = run - mine;  // keys in higher bins
+        uint32_t before = higher + run - mine;  // keys in higher bins
         for (int w = 0; w < warp; ++w) before += s_sum[w];
         if (before < (uint32_t)left && before + mine >= (uint32_t)left) {
             const uint32_t n[4] = {h.w, h.z, h.y, h.x};
@@ -151,6 +190,7 @@ __global__ void __launch_bounds__(SELECT) evict_select_kernel(const EvictArgs a,
         top |= (uint32_t)s_digit << shift;
         left = s_left;
     }
+    if (missing) report(a.err, GK_ERR_INDEX);
     // each warp's stretch of the block: what stays of it, and where it goes
     const int stretch = ((each + SELECT_WARPS - 1) / SELECT_WARPS + 127) & ~127, w0 = min(warp * stretch, each), w1 = min(w0 + stretch, each);
     uint2 n = make_uint2(0, 0);  // keys above `top`, and equal to it
@@ -272,9 +312,10 @@ extern "C" gk_status gk_paged_evict(gk_ctx* ctx, const gk_paged_kv* cache, const
     a.new_len = new_len;
     a.kept = kept;
     a.err = ctx->d_err;
-    // Blocks of a cluster: of about 4096 positions each.
+    // Blocks of a cluster: of about 4096 positions each while they fit the GPU at once, four an SM (48 sequences of up to 8191,
+    // 8 heads: one block a head 129.3 us with the moving, two 135.6).
     int blocks = 1;
-    while (blocks < MAX_CLUSTER && a.from.capacity > 4096 * blocks) blocks *= 2;
+    while (blocks < MAX_CLUSTER && a.from.capacity > 4096 * blocks && (int64_t)a.from.Hkv * B * blocks * 2 <= 4 * (int64_t)ctx->num_sms) blocks *= 2;
     const int each = (int)((cdiv(a.from.capacity, blocks) + 255) & ~int64_t(127));
     const dim3 grid((unsigned)blocks, (unsigned)a.from.Hkv, (unsigned)B);
     if (each <= HELD) {
