@@ -170,6 +170,12 @@ MASS = [  # kv_len, n, H, Hkv, hs, page, first
     ([140] * 40, [2] * 40, 5, 5, 112, 16, [16] * 40),
     ([2600, 0, 900], [513, 3, 600], 2, 2, 64, 128, [129, 0, 0]),
     ([3000], [2], 16, 2, 128, 64, None),
+    ([400, 130], [70, 33], 6, 2, 64, 16, [3, 128]),  # three heads a key head: 42 queries of a tile of 128 rows, 126 rows
+    ([300], [50], 10, 2, 96, 32, None),  # five
+    ([150], [3], 200, 1, 32, 16, None),  # 200: a query's heads fill two tiles, the second in part
+    ([290, 40], [90, 1], 24, 2, 128, 128, [256, 0]),  # twelve
+    ([64], [64], 8, 1, 64, 16, None),
+    ([2000], [2000], 1, 1, 16, 256, [1999]),
 ]
 
 
@@ -442,6 +448,211 @@ def test_evict_keeps_shared_pages_where_they_are(gkctx):
     got = evict(gkctx, c, mass, to, mass, first, 200, 50)
     check_evict(got, c, mass, to, mass, first, 200, 50)
     assert np.array_equal(got[0][0][c.table[0, :4]], before)
+
+
+# ------------------------------------------------------------------ workspaces, graphs, streams, far offsets
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("S,n,H,Hkv,hs", [(6, 1, 4, 2, 64), (70, 1, 4, 2, 128), (5, 40, 2, 2, 64), (4, 200, 4, 2, 128)])
+def test_shared_small_workspace_graph_and_streams(gkctx, S, n, H, Hkv, hs, q8):
+    """Any workspace will do; a captured call replays on changed lengths; two contexts at once give the bits of one."""
+    from gpt_decoder_gb300 import gk
+
+    t = _t()
+    rng = np.random.default_rng(3000 + S)
+    groups = [(2300, [(n + 40, n)] * S), (700, [(n, n)] * 3)]
+    c, ns, gs, prefix = shared_cache(rng, groups, Hkv, hs, 64, q8)
+    q = serving.bf16(rng.standard_normal((sum(ns), H, hs)))
+    ref = shared_ref(c, q, ns, gs, prefix, 0.125)
+    rows, w, B = sum(ns), H * hs, len(ns)
+    part = rows * H * (hs * 4 + 8)
+    for ws in (0, part, 2 * part + 8 * rows + 64, 3 << 20, 64 << 20):
+        ctx = gk.Ctx(t.cuda.current_stream().cuda_stream, workspace_bytes=ws)
+        check_attention(*attend_shared(ctx, c, q, ns, gs, prefix, 0.125), ref, ws)
+        ctx.close()
+    d, qd, qs, dgs, dpl = Dev(c, poison=False), dev(q.reshape(rows, w), t.bfloat16), dev(starts(ns)), dev(gs), dev(prefix)
+    most = int(max(starts(ns)[gs[1:]] - starts(ns)[gs[:-1]]))
+
+    def call(ctx, y, lse):
+        gk.gk_paged_attn_shared(ctx, d.h, gk.GK_BF16, qd, w, y, w, lse, qs, B, dgs, dpl, 2, H, rows, n, most, 0.125)
+
+    out = lambda: (t.zeros(rows, w, dtype=t.bfloat16, device="cuda"), t.zeros(rows, H, device="cuda"))  # noqa: E731
+    side = t.cuda.Stream()
+    ctx = gk.Ctx(side, workspace_bytes=64 << 20)
+    y, lse = out()
+    t.cuda.synchronize()
+    g = t.cuda.CUDAGraph()
+    with t.cuda.graph(g, stream=side):
+        call(ctx, y, lse)
+    want = out()
+    for cut in (0, 900, 0):  # prefixes shorter by so much, and with them the sequences
+        p2, kv2 = np.maximum(prefix - cut, 0).astype(np.int32), c.kv_len.copy()
+        kv2[:S] -= min(cut, 2300)
+        kv2[S:] -= min(cut, 700)
+        old, c.kv_len = c.kv_len, kv2
+        d.kv_len.copy_(dev(kv2))
+        dpl.copy_(dev(p2))
+        y.fill_(7)
+        t.cuda.synchronize()
+        g.replay()
+        t.cuda.synchronize()
+        # the own keys now begin inside what was the prefix: the first sequence's pages and each one's own agree there
+        r2 = shared_ref(c, q, ns, gs, p2, 0.125)
+        check_attention(y.float().cpu().numpy().reshape(q.shape).astype(np.float64), lse.cpu().numpy().astype(np.float64), r2, cut)
+        if cut == 0:
+            want[0].copy_(y)
+            want[1].copy_(lse)
+        c.kv_len = old
+    gk.gk_sync(ctx)
+    ctx.close()
+    ctxs = [gk.Ctx(t.cuda.Stream(), workspace_bytes=64 << 20) for _ in range(2)]
+    got = [[out() for _ in range(8)] for _ in ctxs]
+    t.cuda.synchronize()
+    for i in range(8):
+        for ctx, o in zip(ctxs, got):
+            call(ctx, *o[i])
+    for ctx, o in zip(ctxs, got):
+        gk.gk_sync(ctx)
+        assert all(t.equal(a, b) for each in o for a, b in zip(each, want))
+        ctx.close()
+
+
+def test_shared_8_bit_prefixes_a_few_heads_at_a_time(gkctx):
+    """A workspace with room for the codes of three of five heads' prefixes as bf16: two turns, the second of two."""
+    from gpt_decoder_gb300 import gk
+
+    t = _t()
+    rng = np.random.default_rng(3100)
+    Hkv, G, hs, n, S, cap = 5, 8, 128, 40, 10, 65536
+    c, ns, gs, prefix = shared_cache(rng, [(1900, [(n + 5, n)] * S), (100, [(n, n)] * 2)], Hkv, hs, 64, True)
+    c.table = np.pad(c.table, ((0, 0), (0, cap // 64 - c.table.shape[1])), constant_values=-1)
+    q = serving.bf16(rng.standard_normal((sum(ns), Hkv * G, hs)))
+    ref = shared_ref(c, q, ns, gs, prefix, 0.1)
+    a_head, part = 2 * cap * hs * 2, sum(ns) * Hkv * G * (hs * 4 + 8)  # two groups' keys; a part of every row
+    ws = 9 * a_head
+    assert ws // 2 < Hkv * a_head and 3 <= ws // 8 * 3 // a_head < 4 and 2 * 3 * 2 * -(-S * n * G // 256) >= 152 and 3 * a_head > 2 * part + 8 * sum(ns)
+    ctx = gk.Ctx(t.cuda.current_stream().cuda_stream, workspace_bytes=ws)
+    check_attention(*attend_shared(ctx, c, q, ns, gs, prefix, 0.1), ref)
+    ctx.close()
+
+
+def test_mass_and_evict_graph_and_streams(gkctx):
+    """Captured and replayed on changed lengths, beside another context's calls: the bits of one alone."""
+    from gpt_decoder_gb300 import gk
+
+    t = _t()
+    rng = np.random.default_rng(3200)
+    for n, H, Hkv, hs, q8 in ((1, 4, 2, 64, True), (1, 8, 2, 128, False), (90, 4, 2, 128, True), (200, 2, 2, 64, False)):
+        c = cache(rng, [1500, 900], Hkv, hs, 64, q8)
+        q, w, qs = serving.bf16(rng.standard_normal((2 * n, H, hs))), H * hs, dev(starts([n, n]))
+        lse = serving.paged_attn(c, q, starts([n, n]), 0.125)[1].astype(np.float32)
+        to = to_pages(rng, c, [300, 300], False)
+        d, td, qd, ld = Dev(c, poison=False), Dev(to, poison=False), dev(q.reshape(2 * n, w), t.bfloat16), dev(lse)
+        first = dev(np.array([20, 0], np.int32))
+
+        class Out:
+            def __init__(self):
+                self.mass, self.to_mass = t.zeros(c.k.shape[:3], device="cuda"), t.zeros(to.k.shape[:3], device="cuda")
+                self.k, self.v = (t.zeros_like(x) for x in (td.k, td.v))
+                self.ks, self.vs = (None if x is None else t.zeros_like(x) for x in (td.ks, td.vs))
+                self.new, self.kept = t.zeros(2, dtype=t.int32, device="cuda"), t.zeros(2, Hkv, 280, dtype=t.int32, device="cuda")
+                self.h = gk.PagedKv(self.k, self.v, self.ks, self.vs, td.table, self.new)
+
+            def all(self):
+                return [x for x in (self.mass, self.to_mass, self.k, self.v, self.new, self.kept) if x is not None]
+
+        def call(ctx, o):
+            gk.gk_paged_mass(ctx, d.h, gk.GK_BF16, qd, w, ld, None, 1.0, o.mass, None, qs, 2, H, 2 * n, n, 0.125)
+            gk.gk_paged_evict(ctx, d.h, o.mass, o.h, o.to_mass, first, 280, 30, o.new, o.kept, 2)
+
+        want = Out()
+        call(gkctx, want)
+        gk.gk_sync(gkctx)
+        side = t.cuda.Stream()
+        ctx, o = gk.Ctx(side, workspace_bytes=0), Out()
+        t.cuda.synchronize()
+        g = t.cuda.CUDAGraph()
+        with t.cuda.graph(g, stream=side):
+            call(ctx, o)
+        for lens in ([n, n + 3], [700, 900], [1500, 900]):
+            d.kv_len.copy_(dev(np.array(lens, np.int32)))
+            for x in o.all():
+                x.zero_()
+            t.cuda.synchronize()
+            g.replay()
+            t.cuda.synchronize()
+            assert o.new.tolist() == [min(lens[0], 300), min(lens[1], 280)]
+        assert all(t.equal(a, b) for a, b in zip(o.all(), want.all()))
+        gk.gk_sync(ctx)
+        ctx.close()
+        ctxs, outs = [gk.Ctx(t.cuda.Stream(), workspace_bytes=0) for _ in range(2)], [[Out() for _ in range(5)] for _ in range(2)]
+        t.cuda.synchronize()
+        for i in range(5):
+            for ctx, each in zip(ctxs, outs):
+                call(ctx, each[i])
+        for ctx, each in zip(ctxs, outs):
+            gk.gk_sync(ctx)
+            assert all(t.equal(a, b) for o in each for a, b in zip(o.all(), want.all()))
+            ctx.close()
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_shared_mass_and_evict_offsets_past_32_bits(gkctx, q8):
+    """Pages whose first element lies past 2^32 elements of the cache: the bits of a small one."""
+    from gpt_decoder_gb300 import gk
+
+    t = _t()
+    rng = np.random.default_rng(3300)
+    Hkv, hs, page, n_pages = 8, 128, 128, 33000
+    c, ns, gs, prefix = shared_cache(rng, [(2100, [(40, 1)] * 4), (1000, [(300, 200)] * 2)], Hkv, hs, page, q8)
+    to = to_pages(rng, c, [400] * 6, True)
+    assert (n_pages - c.n_pages) * Hkv * hs * page > 1 << 32
+    d, rows, w, B = Dev(c, poison=False), sum(ns), Hkv * hs, len(ns)
+    at = n_pages - c.n_pages
+    q, qs = dev(rng.standard_normal((rows, w)).astype(np.float32), t.bfloat16), dev(starts(ns))
+    results = []
+    for base in (0, at):
+
+        def big(x):  # the last pages are the small cache's
+            if x is None or not base:
+                return None if x is None else x.clone()
+            y = t.empty(n_pages, *x.shape[1:], dtype=x.dtype, device="cuda")
+            y[base:].copy_(x)
+            return y
+
+        k, v, ks, vs = (big(x) for x in (d.k, d.v, d.ks, d.vs))
+        h = gk.PagedKv(k, v, ks, vs, d.table + base, d.kv_len)
+        y, lse = t.zeros(rows, w, dtype=t.bfloat16, device="cuda"), t.zeros(rows, Hkv, device="cuda")
+        gk.gk_paged_attn_shared(gkctx, h, gk.GK_BF16, q, w, y, w, lse, qs, B, dev(gs), dev(prefix), 2, Hkv, rows, 200, 400, 0.088)
+        mass = t.zeros((n_pages if base else c.n_pages), Hkv, page, device="cuda")
+        new, kept = t.zeros(B, dtype=t.int32, device="cuda"), t.zeros(B, Hkv, 400, dtype=t.int32, device="cuda")
+        first = dev(np.array([0] * 6, np.int32))
+        for b in range(4):  # (the group's sequences hold the prefix's pages together: one at a time)
+            one = gk.PagedKv(k, v, ks, vs, (d.table + base)[b : b + 1], d.kv_len[b : b + 1])
+            gk.gk_paged_mass(gkctx, one, gk.GK_BF16, q[b:], w, lse[b:], mass, 1.0, mass, None, dev(starts([1])), 1, Hkv, 1, 1, 0.088)
+        for b in (4, 5):
+            one = gk.PagedKv(k, v, ks, vs, (d.table + base)[b : b + 1], d.kv_len[b : b + 1])
+            r = 4 + 200 * (b - 4)
+            gk.gk_paged_mass(gkctx, one, gk.GK_BF16, q[r:], w, lse[r:], mass, 1.0, mass, None, dev(starts([200])), 1, Hkv, 200, 200, 0.088)
+        gk.gk_paged_evict(gkctx, h, mass, gk.PagedKv(k, v, ks, vs, dev(to.table) + base, new), mass, first, 400, 100, new, kept, B)
+        gk.gk_sync(gkctx)
+        results.append([y, lse, mass[-c.n_pages :], k[-c.n_pages :], v[-c.n_pages :], new, kept])
+    assert results[0][0].abs().sum() > 0 and results[0][2].sum() > 0
+    for a, b in zip(*results):
+        assert t.equal(a, b)
+
+
+def test_evict_of_tables_wider_than_the_blocks_hold(gkctx):
+    """More positions than a cluster's shared memory has room for: masses are read again for each digit."""
+    rng = np.random.default_rng(3400)
+    for kv, page in (([500000], 256), ([1000, 30], 64)):
+        c = cache(rng, kv, 1, 16, page, False, spare=0)
+        if len(kv) > 1:
+            c.table = np.pad(c.table, ((0, 0), (0, 400000 // page)), constant_values=-1)
+        mass = np.exp(rng.standard_normal(c.k.shape[:3]) * 3).astype(np.float32)
+        to = to_pages(rng, c, [107] * len(kv), False)
+        to_mass = np.full(to.k.shape[:3], 3, np.float32)
+        got = evict(gkctx, c, mass, to, to_mass, None, 107, 9)
+        check_evict(got, c, mass, to, to_mass, None, 107, 9)
 
 
 # --------------------------------------------------------------------------------------- together
