@@ -7,6 +7,9 @@
 // histogram of what still matches, summed over the cluster through distributed shared memory. Then each warp counts what
 // stays of its stretch of positions and walks it, so the positions come out in order without a sort: keys above the
 // n-th, and the first of those equal to it. Move: those rows, with scales and mass, a tile of tokens a block.
+// The bytes of what moves bound it where there are many: 48 sequences of up to 8191 tokens to 2064, 8 heads of 128, bf16:
+// 127 us, 5.9 TB/s (0.89 of a copy), the selection 15 of them; 3 of up to 65536 to 8256 52 us, 19 the selection (a chain:
+// page ids, masses, three digits at about 2.5 us, the walk). One of 1100 to 516, 12 heads of 64: 8.8 us, two launches.
 #include <math.h>
 
 #include <algorithm>
@@ -97,7 +100,7 @@ __global__ void __launch_bounds__(SELECT) evict_select_kernel(const EvictArgs a,
         return r;
     };
     auto mass4 = [&](int64_t r) {
-        return r >= 0 ? __ldg(reinterpret_cast<const float4*>(a.mass + r)) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        return r >= 0 ? *reinterpret_cast<const float4*>(a.mass + r) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
     };
     auto keys4 = [&](int i, const float4& m) {
         const int pos = p0 + i;
@@ -299,6 +302,8 @@ extern "C" gk_status gk_paged_evict(gk_ctx* ctx, const gk_paged_kv* cache, const
     GK_TRY(check_pages(ctx, "gk_paged_evict", &t, new_len, B, 0, &a.to));
     GK_REQUIRE(ctx, to->dtype == cache->dtype && to->Hkv == cache->Hkv && to->page_size == cache->page_size && to->hs == cache->hs,
                GK_ERR_ARG, "gk_paged_evict: the two caches differ");
+    GK_REQUIRE(ctx, cache->k != to->k || (cache->v == to->v && cache->k_scale == to->k_scale && cache->v_scale == to->v_scale && mass == to_mass),
+               GK_ERR_ARG, "gk_paged_evict: one pool has one set of arrays");
     GK_REQUIRE(ctx, budget >= 1 && budget <= 1 << 30 && recent >= 0 && recent <= budget, GK_ERR_ARG, "gk_paged_evict: budget %d, recent %d",
                budget, recent);
     GK_REQUIRE(ctx, aligned16(mass) && aligned16(to_mass), GK_ERR_ALIGN, "gk_paged_evict: mass must be 16-byte aligned");

@@ -7,7 +7,14 @@
 // y = (o_1 2^(m_1 - m) + o_2 2^(m_2 - m)) / (l_1 2^(m_1 - m) + l_2 2^(m_2 - m)), m the larger. So a group's prefix is
 // attended as one sequence that holds the rows of all of its sequences (they lie next to each other): with S sequences its
 // bytes are read once instead of S times, and the rows that meet a key are S times as many, which is what the tensor
-// cores need. Then each sequence attends to its own keys. Both are the kernels of gk_paged_attn.
+// cores need. Then each sequence attends to its own keys. Both are the kernels of gk_paged_attn, and neither waits for
+// the other (begin(), paged_attn.cuh).
+// Measured: a token of 64 sequences behind 16384 shared 8-bit keys and up to 1024 own ones, 32 heads over 8 of 128: 83 us
+// (gk_paged_attn 365): 19 own keys beside 23 that lay the codes out as bf16, 42 the prefix in tiles of 128 rows (8 key
+// tiles a block at 2.7 us, its softmax warps' rate for codes, and 15 to begin and end), 12 the join; bf16 pages 58. 7
+// groups of up to 16 sequences behind up to 8100 keys, 12 heads of 64, bf16: 43 us, 3.0 TB/s (122): blocks of few tiles, a
+// third of their time the loads that lead to the first key. Chunks of 256 behind 16384 keys, 12 sequences a group: 784
+// (787): the tensor cores' part bounds both.
 #include <math.h>
 
 #include <algorithm>
@@ -173,9 +180,9 @@ extern "C" gk_status gk_paged_attn_shared(gk_ctx* ctx, const gk_paged_kv* cache,
     // each other, and each by itself leaves much of the GPU idle).
     const bool expanded = p.expanded_k && p.heads == a.p.Hkv;
     if (expanded) GK_TRY(launch_shared_expand(ctx, p));
-    a.early = expanded;
+    a.early = expanded && B < 65535;  // (a block more along the sequences)
     GK_TRY(own_few ? launch_shared_few(ctx, a, OWN) : launch_shared_tiles(ctx, a, OWN));
-    p.early = !p.expanded_k;
+    p.early = !p.expanded_k && n_groups < 65535;
     if (prefix_few) {
         GK_TRY(launch_shared_few(ctx, p, PREFIX));
     } else {

@@ -732,6 +732,36 @@ def test_sampling_from_a_prompt_under_a_budget(gkctx, q8):
     assert cuts >= 2
 
 
+# --------------------------------------------------------------------------------- the measured cases
+@pytest.mark.parametrize("name", ["shared_few", "shared_groups", "mass_one_token", "mass_chunk", "evict_one", "evict_step"])
+def test_measured_cases_under_a_side_stream(monkeypatch, name):
+    """The calls that they make, beside their plain forms, and again on a stream that is not the default one."""
+    import torch
+
+    from perf import more_operators
+
+    case = next(c for c in more_operators.listed() if c["name"] == name)
+
+    def outputs(own):
+        monkeypatch.setattr(more_operators, "own", own)
+        out = more_operators.run(more_operators.prepare(case, 3))
+        return [x.clone() for x in (out if isinstance(out, tuple) else (out,))]
+
+    plain, want = outputs(False), outputs(True)
+    for a, b in zip(want, plain):
+        if a.dtype == torch.int32 or name == "evict_one":
+            assert torch.equal(a, b)
+        else:  # both within a rounding or two of the same numbers (bf16; masses in 32 bits)
+            assert ((a.float() - b.float()).abs() <= 2.0 ** (-6 if a.dtype == torch.bfloat16 else -14) * (b.float().abs() + 0.05)).all()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # the stream is about 10 ms behind the host: nothing is there yet by chance
+        got = outputs(True)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 # ---------------------------------------------------------------------------------------- refusals
 def test_shared_mass_and_evict_refuse(gkctx):
     from gpt_decoder_gb300 import gk
@@ -769,6 +799,8 @@ def test_shared_mass_and_evict_refuse(gkctx):
         refused(status, gk.gk_paged_evict, *ev(**bad))
     for Hkv, hs, page, q8 in ((1, 32, 16, True), (2, 48, 16, True), (2, 32, 32, True), (2, 32, 16, False)):
         refused(A, gk.gk_paged_evict, *ev(to=Dev(cache(np.random.default_rng(3), [20], Hkv, hs, page, q8)).h))
+    same = gk.PagedKv(d.k, d.v, d.ks, d.vs, d.table, new)
+    refused(A, gk.gk_paged_evict, *ev(to=same))  # one pool, two arrays of masses
     s = dt_.h.struct
     for name, bad, status in (("page_size", 24, UN), ("hs", 24, UN), ("dtype", gk.GK_F32, A), ("k_scale", None, A), ("n_pages", 0, A),
                               ("ld_table", 1, A), ("v", s.v + 2, L), ("page_table", None, A)):
