@@ -416,11 +416,12 @@ __global__ void __launch_bounds__(THREADS, 1) mass_tiles_kernel(const MassArgs a
                 tc_fence_after();
                 if (elect_one()) {
                     const uint32_t d = tmem + g * 256 + buf * 128;
-                    umma_bf16(d, desc_add(kx_d, g * STEP), desc_add(qx_d, st * STEP), id, 0);
                     for (int kk = 0; kk < steps; ++kk) {
                         const uint32_t at = (kk >> 2) * HALF + (kk & 3) * 32;
-                        umma_bf16(d, desc_add(k_d, g * L::TILE + at), desc_add(q_d, st * L::TILE + at), id, 1);
+                        umma_bf16(d, desc_add(k_d, g * L::TILE + at), desc_add(q_d, st * L::TILE + at), id, kk > 0);
                     }
+                    // (last: the sums before it are cut at the size of the scores, not of the log sums)
+                    umma_bf16(d, desc_add(kx_d, g * STEP), desc_add(qx_d, st * STEP), id, 1);
                     umma_commit(&s_full[g * 2 + buf]);
                 }
                 __syncwarp();
