@@ -7,10 +7,11 @@
 // S^T = K Q^T, so that a key's sum stays with the thread (or the four lanes) that holds its row.
 //   Few rows: a warp takes tiles of 16 keys straight from the cache into the registers of mma.sync m16n8k16 (as the
 //   attention of few rows does), its rows eight at a time from shared memory, which holds them in operand order.
-//   Tiles: a block holds 256 keys in shared memory (8-bit codes as bf16, once) and walks the rows in tiles of 128,
-//   which TMA brings (a box of whole queries of the heads that share the keys); D = K Q^T (tcgen05, M = 128 keys, N =
-//   128 rows) into tensor memory, two buffers for each half of the keys; sixteen warps, a thread a key and half of the
-//   tile's rows, read the scores and add their weights. A key's factor f (scale log2(e), times its own scale for codes) is
+//   Tiles: a block holds 256 keys in shared memory (8-bit codes as bf16, once) and walks the rows in pairs of tiles of
+//   128, which TMA brings (a box of whole queries of the heads that share the keys); D = K Q^T (tcgen05, M = 128 keys, N
+//   = 256 rows, so that the keys' trip through shared memory serves twice the rows) into tensor memory, a buffer for each
+//   half of the keys: one is computed while the other is summed. Sixteen warps, a thread a key and one tile's rows of a
+//   pair, read the scores and add their weights. A key's factor f (scale log2(e), times its own scale for codes) is
 //   its thread's. The rows' log sums would be a broadcast load for every element (four wavefronts of shared memory for
 //   four of them, which is all that the operands leave): they are one more 16-deep step of the product instead, of 1 / f
 //   and -l in three bf16 parts each, so that D = s / f - l / f and the weight is 2^(f D).
@@ -220,15 +221,16 @@ __global__ void __launch_bounds__(WARPS * 32) mass_few_kernel(const MassArgs a) 
 constexpr int KEYS = 256, RT = 128, THREADS = 640, SUM_WARPS = 16;
 constexpr uint32_t HALF = 128 * 128;  // 128 rows of 64 bf16
 constexpr uint32_t STEP = 128 * 32;   // 128 rows of one 16-deep step
+constexpr int PAIR = 2;               // tiles of rows a product
 constexpr uint64_t WAIT_NS = 1000000000ull;
 constexpr float LEAST_F = 0x1p-60f;    // a smaller factor (of codes): no score at all
 constexpr float NO_WEIGHT = -0x1p60f;  // instead of -l: 1 / f times it is finite
 
 template <int HSP>
 struct Layout {
-    static constexpr int HALVES = HSP / 64, STAGES = HSP == 64 ? 4 : 3;
+    static constexpr int HALVES = HSP / 64, STAGES = HSP == 64 ? 4 : 2;
     static constexpr uint32_t TILE = HALVES * HALF;
-    static constexpr uint32_t Q = 2 * TILE, KX = Q + STAGES * TILE, QX = KX + 2 * STEP, JOIN = QX + STAGES * STEP, BARS = JOIN + KEYS * 4,
+    static constexpr uint32_t Q = 2 * TILE, KX = Q + STAGES * PAIR * TILE, QX = KX + 2 * STEP, JOIN = QX + STAGES * PAIR * STEP, BARS = JOIN + KEYS * 4,
                               BYTES = BARS + 256 + 1024;
 };
 
@@ -277,8 +279,8 @@ __global__ void __launch_bounds__(THREADS, 1) mass_tiles_kernel(const MassArgs a
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BARS);
     uint64_t* q_full = bars;       // [4]
     uint64_t* q_empty = bars + 4;  // [4]
-    uint64_t* s_full = bars + 8;   // [2 halves][2 buffers]
-    uint64_t* s_free = bars + 12;  // [2][2] (an arrival per warp)
+    uint64_t* s_full = bars + 8;   // [2 halves of the keys]
+    uint64_t* s_free = bars + 12;  // [2] (an arrival per warp)
     uint64_t* bar_drain = bars + 16;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 17);
     wait_for_earlier_kernels();
@@ -293,7 +295,7 @@ __global__ void __launch_bounds__(THREADS, 1) mass_tiles_kernel(const MassArgs a
     // tiles of rows, from the first that sees a key of the block on
     const int parts = (a.G + a.tile_heads - 1) / a.tile_heads, seen_from = max(0, max(k0, s.first) - (s.kv_all - s.n));
     const int block0 = min(seen_from, s.n) / a.tile_queries, n_tiles = ((s.n + a.tile_queries - 1) / a.tile_queries - block0) * parts;
-    const int cols = a.tile_heads * a.tile_queries;
+    const int cols = a.tile_heads * a.tile_queries, n_pairs = (n_tiles + PAIR - 1) / PAIR;
 
     if (tid == 0) {
         for (int i = 0; i < 4; ++i) {
@@ -344,10 +346,10 @@ __global__ void __launch_bounds__(THREADS, 1) mass_tiles_kernel(const MassArgs a
             *reinterpret_cast<uint4*>(sKx + (r >> 7) * STEP + swizzled32(r & 127, 1)) = make_uint4(0, 0, 0, 0);
         }
     }
-    for (int x = tid; x < L::STAGES * RT; x += THREADS)
+    for (int x = tid; x < L::STAGES * PAIR * RT; x += THREADS)
         *reinterpret_cast<uint4*>(sQx + x / RT * STEP + swizzled32(x % RT, 1)) = make_uint4(0, 0, 0, 0);
     // rows that no box of TMA fills: zeros, whose log sum gives them no weight
-    for (int x = tid; x < L::STAGES * L::HALVES * (RT - cols) * 8; x += THREADS) {
+    for (int x = tid; x < L::STAGES * PAIR * L::HALVES * (RT - cols) * 8; x += THREADS) {
         const int t = x / ((RT - cols) * 8), r = cols + x % ((RT - cols) * 8) / 8;
         *reinterpret_cast<uint4*>(sQ + t * HALF + swizzled(r, x & 7)) = make_uint4(0, 0, 0, 0);
     }
@@ -360,69 +362,81 @@ __global__ void __launch_bounds__(THREADS, 1) mass_tiles_kernel(const MassArgs a
     bool failed = false;
 
     if (warp == SUM_WARPS) {  // rows by TMA, log sums by lanes (four each)
-        int in_flight = -1, q0 = block0 * a.tile_queries, h0 = 0;  // of the next tile whose log sums are read
+        int in_flight = -1, q0 = block0 * a.tile_queries, h0 = 0;  // of the next tile that is sent for
+        int ql = q0, hl = 0;                                       // and whose log sums are read
         int query[4], head[4];  // of the lane's rows (lane, lane + 32, ..), from the tile's first
-        float l[4];
+        float l[PAIR][4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int c = lane + e * 32;
             query[e] = c < cols ? c / a.tile_heads : 1 << 30;
             head[e] = c % a.tile_heads;
         }
+        auto next = [&](int& q, int& h) {
+            h += a.tile_heads;
+            if (h >= a.G) h = 0, q += a.tile_queries;
+        };
         auto load_l = [&]() {
-            const float* src = a.lse + (int64_t)(s.s0 + q0) * a.H + hk * a.G + h0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                l[e] = query[e] < s.n - q0 && head[e] < a.G - h0 ? __ldg(src + (int64_t)query[e] * a.H + head[e]) : INFINITY;
+            for (int t = 0; t < PAIR; ++t) {  // (past the last tile: no query is left)
+                const float* src = a.lse + (int64_t)(s.s0 + ql) * a.H + hk * a.G + hl;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    l[t][e] = query[e] < s.n - ql && head[e] < a.G - hl ? __ldg(src + (int64_t)query[e] * a.H + head[e]) : INFINITY;
+                next(ql, hl);
+            }
         };
         if (n_tiles > 0) load_l();
-        for (int i = 0; i < n_tiles; ++i) {
+        for (int i = 0; i < n_pairs; ++i) {
             const int st = i % L::STAGES;
             if (!__all_sync(0xffffffffu, mbar_wait(&q_empty[st], i / L::STAGES & 1 ^ 1, nullptr, WAIT_NS))) {
                 failed = true;
                 break;
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                *reinterpret_cast<uint4*>(sQx + st * STEP + swizzled32(lane + e * 32, 0)) =
-                    slots_b(parts_of(isinf(l[e]) ? NO_WEIGHT : l[e] * -1.4426950408889634f));
+            for (int t = 0; t < PAIR; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    *reinterpret_cast<uint4*>(sQx + (st * PAIR + t) * STEP + swizzled32(lane + e * 32, 0)) =
+                        slots_b(parts_of(isinf(l[t][e]) ? NO_WEIGHT : l[t][e] * -1.4426950408889634f));
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
-                mbar_expect_tx(&q_full[st], (uint32_t)(L::HALVES * 128 * cols));
-                for (int h = 0; h < L::HALVES; ++h)
-                    tma_load_3d(&tm_q, &q_full[st], sQ + st * L::TILE + h * HALF, h * 64, hk * a.G + h0, s.s0 + q0);
+            const int here = min(PAIR, n_tiles - i * PAIR);
+            if (lane == 0) mbar_expect_tx(&q_full[st], (uint32_t)(L::HALVES * 128 * cols * here));
+            for (int t = 0; t < here; ++t) {
+                if (lane == 0)
+                    for (int h = 0; h < L::HALVES; ++h)
+                        tma_load_3d(&tm_q, &q_full[st], sQ + st * PAIR * L::TILE + (h * PAIR + t) * HALF, h * 64, hk * a.G + h0, s.s0 + q0);
+                next(q0, h0);
             }
             in_flight = i;
-            h0 += a.tile_heads;
-            if (h0 >= a.G) h0 = 0, q0 += a.tile_queries;
-            if (i + 1 < n_tiles) load_l();
+            if (i + 1 < n_pairs) load_l();
         }
         if (failed)  // the copies in flight land before the block ends
             for (int i = max(0, in_flight - L::STAGES + 1); i <= in_flight; ++i) mbar_wait(&q_full[i % L::STAGES], i / L::STAGES & 1, nullptr, WAIT_NS / 5);
     } else if (warp == SUM_WARPS + 1) {
-        const uint32_t id = instr_desc_bf16(false, false, 128, 128);
+        const uint32_t id = instr_desc_bf16(false, false, 128, PAIR * RT);
         const uint64_t k_d = smem_desc(saddr(sK), 16, 1024), q_d = smem_desc(saddr(sQ), 16, 1024);
         const uint64_t kx_d = smem_desc32(saddr(sKx)), qx_d = smem_desc32(saddr(sQx));
         const int steps = hs >> 4;
         bool ok = true;
-        for (int i = 0; ok && i < n_tiles; ++i) {
-            const int st = i % L::STAGES, buf = i & 1;
+        for (int i = 0; ok && i < n_pairs; ++i) {
+            const int st = i % L::STAGES;
             ok = __all_sync(0xffffffffu, mbar_wait(&q_full[st], i / L::STAGES & 1, nullptr, WAIT_NS));
             for (int g = 0; g < 2 && ok; ++g) {
                 if (!on[g]) continue;
-                ok = __all_sync(0xffffffffu, mbar_wait(&s_free[g * 2 + buf], i >> 1 & 1 ^ 1, nullptr, WAIT_NS));
+                ok = __all_sync(0xffffffffu, mbar_wait(&s_free[g], i & 1 ^ 1, nullptr, WAIT_NS));
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint32_t d = tmem + g * 256 + buf * 128;
+                    const uint32_t d = tmem + g * 256;
                     for (int kk = 0; kk < steps; ++kk) {
-                        const uint32_t at = (kk >> 2) * HALF + (kk & 3) * 32;
-                        umma_bf16(d, desc_add(k_d, g * L::TILE + at), desc_add(q_d, st * L::TILE + at), id, kk > 0);
+                        const uint32_t half = (kk >> 2) * HALF, at = (kk & 3) * 32;
+                        umma_bf16(d, desc_add(k_d, g * L::TILE + half + at), desc_add(q_d, st * PAIR * L::TILE + PAIR * half + at), id, kk > 0);
                     }
                     // (last: the sums before it are cut at the size of the scores, not of the log sums)
-                    umma_bf16(d, desc_add(kx_d, g * STEP), desc_add(qx_d, st * STEP), id, 1);
-                    umma_commit(&s_full[g * 2 + buf]);
+                    umma_bf16(d, desc_add(kx_d, g * STEP), desc_add(qx_d, st * PAIR * STEP), id, 1);
+                    umma_commit(&s_full[g]);
                 }
                 __syncwarp();
             }
@@ -441,7 +455,7 @@ __global__ void __launch_bounds__(THREADS, 1) mass_tiles_kernel(const MassArgs a
         if (!ok) failed = true;
     } else if (warp < SUM_WARPS && on[warp >> 3]) {
         const int g = warp >> 3, side = warp >> 2 & 1, pos = k0 + g * RT + (warp & 3) * 32 + lane;
-        const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16) + g * 256 + side * 64;
+        const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16) + g * 256 + side * RT;
         int64_t row = -1;
         if (pos >= s.first && pos < s.kv) {
             const int id = __ldg(a.p.table + b * a.p.ld_table + (pos >> a.p.page_log2));
@@ -450,33 +464,36 @@ __global__ void __launch_bounds__(THREADS, 1) mass_tiles_kernel(const MassArgs a
         float f = row >= 0 ? factor(row) : 1.f;
         if (f == 0.f) f = 1.f;
         const float before = row >= 0 && a.old && pos < s.kv_all - s.n ? a.old[row] : 0.f;
-        // of the thread's columns: the first that sees the key, and the end of the rows (the tile's heads of the
+        // of the tile's columns: the first that sees the key, and the end of the rows (the tile's heads of the
         // sequence's queries, or where a query's heads fill tiles by themselves the rest of them)
-        int lo = (max(0, pos - (s.kv_all - s.n)) - block0 * a.tile_queries) * a.tile_heads - side * 64, part = 0;
+        int lo = (max(0, pos - (s.kv_all - s.n)) - block0 * a.tile_queries) * a.tile_heads, part = 0;
         int left = s.n - block0 * a.tile_queries;  // queries
+        auto next = [&]() {
+            if (++part == parts) part = 0, lo -= cols, left -= a.tile_queries;
+        };
+        if (side) next();  // this thread's tiles are every other one
         float total = 0.f;
-        for (int i = 0; i < n_tiles; ++i) {
-            const int buf = i & 1;
-            if (!__all_sync(0xffffffffu, mbar_wait(&s_full[g * 2 + buf], i >> 1 & 1, nullptr, WAIT_NS))) {
+        for (int i = 0; i < n_pairs; ++i) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&s_full[g], i & 1, nullptr, WAIT_NS))) {
                 failed = true;
                 break;
             }
             tc_fence_after();
-            const int there = parts > 1 ? min(cols, a.G - part * a.tile_heads) : min(cols, min(left, RT) * a.tile_heads), hi = there - side * 64;
-            const bool some = __any_sync(0xffffffffu, lo > 0) || there < cols;
+            const int hi = parts > 1 ? (left > 0 ? min(cols, a.G - part * a.tile_heads) : 0) : min(cols, max(0, min(left, RT)) * a.tile_heads);
+            const bool some = __any_sync(0xffffffffu, lo > 0) || hi < cols;
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
             // 32 columns at a time: with four warps a scheduler the others cover the load
             auto weights = [&](auto masked) {
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
+                for (int c = 0; c < 4; ++c) {
                     uint32_t w[32];
-                    tmem_ld32_nowait(lane_addr + buf * 128 + c * 32, w);
+                    tmem_ld32_nowait(lane_addr + c * 32, w);
                     tmem_wait_ld_only();
                     reg_fence32(w);
-                    if (c) {
+                    if (c == 3) {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&s_free[g * 2 + buf]);
+                        if (lane == 0) mbar_arrive(&s_free[g]);
                     }
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
@@ -496,9 +513,10 @@ __global__ void __launch_bounds__(THREADS, 1) mass_tiles_kernel(const MassArgs a
             if (some) weights(std::true_type{});
             else weights(std::false_type{});
             total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            if (++part == parts) part = 0, lo -= cols, left -= a.tile_queries;
+            next();
+            next();
         }
-        // the two sides of a key's columns join
+        // the two halves of a key's rows join
         float* other = reinterpret_cast<float*>(smem + L::JOIN) + g * RT + (warp & 3) * 32 + lane;
         if (side) *other = total;
         named_bar_sync(1 + g, 256);
