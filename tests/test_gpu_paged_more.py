@@ -99,6 +99,7 @@ SHARED = [  # groups (prefix, [(own tokens or -1: a padding row, new rows)]), H,
     ([(300, [(40, 40), (60, 33), (200, 129)])], 6, 3, 96, 32),
     ([(1500, [(260, 200), (333, 257)]), (2, [(700, 600), (4, 3)])], 2, 2, 128, 256),
     ([(5000, [(37, 5)] * 12), (6000, [(-1, 2), (9, 9)])], 4, 4, 32, 16),
+    ([(90 + i, [(3, 1), (5, 2)]) for i in range(40)] + [(2048, [(1, 1)] * 3)], 2, 1, 32, 32),  # more groups than a lookup's round
     ([(200, [(3, 3), (500, 40)]), (9000, [(1, 1), (2, 2)] * 4)], 16, 2, 48, 128),
 ]
 
