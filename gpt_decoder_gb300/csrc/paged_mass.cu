@@ -308,44 +308,6 @@ __global__ void __launch_bounds__(THREADS, 1) mass_tiles_kernel(const MassArgs a
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == SUM_WARPS + 1) tmem_alloc(tmem_slot, 512);
-    // the block's keys as bf16; past the end, before the first, on refused pages and without a score zeros
-    bool bad_page = false;
-    auto factor = [&](int64_t row) {  // of a key's score; 0: it has none
-        const float f = Q8 ? a.scale_log2 * __ldg(a.p.k_scale + row) : a.scale_log2;
-        return Q8 && fabsf(f) < LEAST_F ? 0.f : f;
-    };
-    constexpr int CH = Q8 ? HSP / 16 : HSP / 8;  // 16-byte pieces of a row
-#pragma unroll 4
-    for (int x = tid; x < KEYS * CH; x += THREADS) {
-        const int r = x / CH, c = x - r * CH, pos = k0 + r;
-        uint4 u = make_uint4(0, 0, 0, 0);
-        float f = 1.f;
-        if (pos < s.kv && pos >= s.first) {
-            const int id = __ldg(a.p.table + b * a.p.ld_table + (pos >> a.p.page_log2));
-            if (id >= 0 && id < a.p.n_pages) {
-                const int64_t row = (((int64_t)id * a.p.Hkv + hk) << a.p.page_log2) + (pos & ((1 << a.p.page_log2) - 1));
-                if (c * 16 < hs * (Q8 ? 1 : 2))
-                    u = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(a.p.k) + row * (hs * (Q8 ? 1 : 2)) + c * 16));
-                f = factor(row);
-                if (f == 0.f) u = make_uint4(0, 0, 0, 0), f = 1.f;
-            } else {
-                bad_page = true;
-            }
-        }
-        uint8_t* tile = sK + (r >> 7) * L::TILE;
-        if (Q8) {
-            const uint4 lo = make_uint4(codes_pair(a.masks, u.x, 0), codes_pair(a.masks, u.x, 1), codes_pair(a.masks, u.y, 0), codes_pair(a.masks, u.y, 1));
-            const uint4 hi = make_uint4(codes_pair(a.masks, u.z, 0), codes_pair(a.masks, u.z, 1), codes_pair(a.masks, u.w, 0), codes_pair(a.masks, u.w, 1));
-            *reinterpret_cast<uint4*>(tile + (c >> 2) * HALF + swizzled(r & 127, 2 * (c & 3))) = lo;
-            *reinterpret_cast<uint4*>(tile + (c >> 2) * HALF + swizzled(r & 127, 2 * (c & 3) + 1)) = hi;
-        } else {
-            *reinterpret_cast<uint4*>(tile + (c >> 3) * HALF + swizzled(r & 127, c & 7)) = u;
-        }
-        if (c == 0) {
-            *reinterpret_cast<uint4*>(sKx + (r >> 7) * STEP + swizzled32(r & 127, 0)) = slots_a(parts_of(1.f / f));
-            *reinterpret_cast<uint4*>(sKx + (r >> 7) * STEP + swizzled32(r & 127, 1)) = make_uint4(0, 0, 0, 0);
-        }
-    }
     for (int x = tid; x < L::STAGES * PAIR * RT; x += THREADS)
         *reinterpret_cast<uint4*>(sQx + x / RT * STEP + swizzled32(x % RT, 1)) = make_uint4(0, 0, 0, 0);
     // rows that no box of TMA fills: zeros, whose log sum gives them no weight
@@ -353,13 +315,56 @@ __global__ void __launch_bounds__(THREADS, 1) mass_tiles_kernel(const MassArgs a
         const int t = x / ((RT - cols) * 8), r = cols + x % ((RT - cols) * 8) / 8;
         *reinterpret_cast<uint4*>(sQ + t * HALF + swizzled(r, x & 7)) = make_uint4(0, 0, 0, 0);
     }
-    if (bad_page) report(a.err, GK_ERR_INDEX);
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     bool failed = false;
+    auto factor = [&](int64_t row) {  // of a key's score; 0: it has none
+        const float f = Q8 ? a.scale_log2 * __ldg(a.p.k_scale + row) : a.scale_log2;
+        return Q8 && fabsf(f) < LEAST_F ? 0.f : f;
+    };
+    if (warp < SUM_WARPS) {
+        // the block's keys as bf16, while the first rows are on their way; past the end, before the first, on refused
+        // pages and without a score zeros
+        bool bad_page = false;
+        constexpr int CH = Q8 ? HSP / 16 : HSP / 8;  // 16-byte pieces of a row
+#pragma unroll 4
+        for (int x = tid; x < KEYS * CH; x += SUM_WARPS * 32) {
+            const int r = x / CH, c = x - r * CH, pos = k0 + r;
+            uint4 u = make_uint4(0, 0, 0, 0);
+            float f = 1.f;
+            if (pos < s.kv && pos >= s.first) {
+                const int id = __ldg(a.p.table + b * a.p.ld_table + (pos >> a.p.page_log2));
+                if (id >= 0 && id < a.p.n_pages) {
+                    const int64_t row = (((int64_t)id * a.p.Hkv + hk) << a.p.page_log2) + (pos & ((1 << a.p.page_log2) - 1));
+                    if (c * 16 < hs * (Q8 ? 1 : 2))
+                        u = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(a.p.k) + row * (hs * (Q8 ? 1 : 2)) + c * 16));
+                    f = factor(row);
+                    if (f == 0.f) u = make_uint4(0, 0, 0, 0), f = 1.f;
+                } else {
+                    bad_page = true;
+                }
+            }
+            uint8_t* tile = sK + (r >> 7) * L::TILE;
+            if (Q8) {
+                const uint4 lo = make_uint4(codes_pair(a.masks, u.x, 0), codes_pair(a.masks, u.x, 1), codes_pair(a.masks, u.y, 0), codes_pair(a.masks, u.y, 1));
+                const uint4 hi = make_uint4(codes_pair(a.masks, u.z, 0), codes_pair(a.masks, u.z, 1), codes_pair(a.masks, u.w, 0), codes_pair(a.masks, u.w, 1));
+                *reinterpret_cast<uint4*>(tile + (c >> 2) * HALF + swizzled(r & 127, 2 * (c & 3))) = lo;
+                *reinterpret_cast<uint4*>(tile + (c >> 2) * HALF + swizzled(r & 127, 2 * (c & 3) + 1)) = hi;
+            } else {
+                *reinterpret_cast<uint4*>(tile + (c >> 3) * HALF + swizzled(r & 127, c & 7)) = u;
+            }
+            if (c == 0) {
+                *reinterpret_cast<uint4*>(sKx + (r >> 7) * STEP + swizzled32(r & 127, 0)) = slots_a(parts_of(1.f / f));
+                *reinterpret_cast<uint4*>(sKx + (r >> 7) * STEP + swizzled32(r & 127, 1)) = make_uint4(0, 0, 0, 0);
+            }
+        }
+        if (bad_page) report(a.err, GK_ERR_INDEX);
+        fence_proxy_async_smem();
+    }
+    if (warp != SUM_WARPS) named_bar_sync(3, (SUM_WARPS + 3) * 32);  // the keys are there
 
     if (warp == SUM_WARPS) {  // rows by TMA, log sums by lanes (four each)
         int in_flight = -1, q0 = block0 * a.tile_queries, h0 = 0;  // of the next tile that is sent for

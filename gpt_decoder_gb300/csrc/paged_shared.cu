@@ -52,19 +52,35 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) shared_join_kernel(const Attn
     if (pieces) {
         const float2* ml = a.part_ml + out * a.slots;
         const float4* po = reinterpret_cast<const float4*>(a.part_o + out * a.slots * a.p.hs) + min(lane, per - 1);
-        for (int s = lane; s < pieces; s += 32) top = fmaxf(top, ml[s < first ? s : s + skip].x);
+        auto place = [&](int s) { return s < first ? s : s + skip; };
+        // the first eight of the warp's values are on their way while the references are looked through
+        constexpr int AHEAD = 8;
+        float4 v[AHEAD];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+            if (sub + u * share < pieces) v[u] = po[place(sub + u * share) * per];
+        const float2 mine = lane < pieces ? ml[place(lane)] : make_float2(-INFINITY, 0.f);
+        top = mine.x;
+        for (int s = lane + 32; s < pieces; s += 32) top = fmaxf(top, ml[place(s)].x);
         top = warp_max(top);
-#pragma unroll 8
-        for (int s = sub; s < pieces; s += share) {
-            const int at = s < first ? s : s + skip;
-            const float2 x = ml[at];
-            const float4 v = po[at * per];
+        auto add = [&](const float2& x, const float4& v) {
             // a piece in which the row sees nothing has sum 0 (or NaN, which stays) and no reference; its values are
             // zeros. A factor that underflows still multiplies: what is not finite stays so.
             const float c = x.x == -INFINITY ? (x.y == 0.f ? 0.f : 1.f) : ex2(x.x - top);
             l += x.y * c;
             o.x += v.x * c, o.y += v.y * c, o.z += v.z * c, o.w += v.w * c;
+        };
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            const int s = sub + u * share;
+            if (s >= pieces) break;
+            float2 x;
+            if (s < 32) x = make_float2(__shfl_sync(0xffffffffu, mine.x, s), __shfl_sync(0xffffffffu, mine.y, s));
+            else x = ml[place(s)];
+            add(x, v[u]);
         }
+#pragma unroll 4
+        for (int s = sub + AHEAD * share; s < pieces; s += share) add(ml[place(s)], po[place(s) * per]);
     }
     if (lg) {
         s_o[warp][lane] = o;
