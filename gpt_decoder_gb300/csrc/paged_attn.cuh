@@ -50,17 +50,17 @@ struct AttnArgs {
 
 // Wait for the launches before this one, and let the next one begin. A launch that is `early` reads nothing of the one
 // directly before it (and that one has let it begin after its own wait, so all before are complete): its blocks go on at
-// once, and the last one along `last`, which has no other work, holds up the launch's end until the other's. True:
-// this is that block.
+// once. It has a slice of blocks more (`extra`), of which one (`only`) holds up the launch's end until the other's. True:
+// this block has no other work.
 template <int PART>
-__device__ __forceinline__ bool begin(const AttnArgs& a, bool last) {
+__device__ __forceinline__ bool begin(const AttnArgs& a, bool extra, bool only) {
     if constexpr (PART == WHOLE) {
         wait_for_earlier_kernels();
         return false;
     } else {
-        if (!a.early || last) wait_for_earlier_kernels();
+        if (!a.early || (extra && only)) wait_for_earlier_kernels();
         let_next_begin();
-        return a.early && last;
+        return a.early && extra;
     }
 }
 

@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) 
     __shared__ float2 s_ml[KG][ROWS];
     __shared__ float2 s_join[ROWS];  // clustered: the piece's reference and sum, its weighted values in s_o[0]
     __shared__ int s_odd;
-    if (begin<PART>(a, blockIdx.y == gridDim.y - 1)) return;
+    if (begin<PART>(a, blockIdx.y == gridDim.y - 1, blockIdx.x == 0)) return;
 
     const int b = blockIdx.y, hk = blockIdx.x / a.splits, split = blockIdx.x - hk * a.splits;
     if (PART == OWN && hk == a.p.Hkv) return leave_row_parts(a, b);

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 28);
     uint64_t* s_free = bars + 29;    // [2] early S: S_g has been read (one arrival per warp)
     uint64_t* bar_pv = bars + 31;    // [2] early S: P_g V is complete
-    if (begin<PART>(a, blockIdx.z == gridDim.z - 1)) return;
+    if (begin<PART>(a, blockIdx.z == gridDim.z - 1, blockIdx.x == 0 && blockIdx.y == 0)) return;
     if (PART == OWN && blockIdx.x == gridDim.x - 1) {
         if (blockIdx.y == 0) leave_row_parts(a, blockIdx.z);
         return;

@@ -17,10 +17,10 @@
 //   and -l in three bf16 parts each, so that D = s / f - l / f and the weight is 2^(f D).
 // Measured: 48 sequences of up to 8191 8-bit keys, 8 heads of 128, a token of 32 heads each: 37 us, 4.3 TB/s (0.65 of a
 // copy; ALU 55%, issue 51%: the unpacking's instructions); bf16 pages 52 us, 5.9 TB/s (0.88). Two chunks of up to 2048 rows
-// behind 16384 keys, 32 heads over 8 of 128: 293 us, 1.16 PFLOP/s (0.59 of a dense product; tensor pipe 60%, exponentials
-// 55% of their pipe): 40 us are the blocks' beginnings (one of 256 keys an SM at a time), the rest waits that sixteen warps do
-// not cover. (128 rows a product and two buffers: 340 us, the operands' trips through shared memory; a broadcast load of
-// the log sums: 358; eight warps: 409.) Chunks of up to 1000, 12 heads of 64, 8 bits: 47 us, 14 of them beginnings.
+// behind 16384 keys, 32 heads over 8 of 128: 287 us, 1.19 PFLOP/s (0.60 of a dense product; tensor pipe 60%, exponentials
+// 55% of their pipe): some 35 us are the blocks' beginnings (one of 256 keys an SM at a time), the rest waits that sixteen
+// warps do not cover. (128 rows a product and two buffers: 340 us, the operands' trips through shared memory; a broadcast load of
+// the log sums: 358; eight warps: 409.) Chunks of up to 1000, 12 heads of 64, 8 bits: 43 us, a third of it beginnings.
 #include <math.h>
 
 #include <algorithm>

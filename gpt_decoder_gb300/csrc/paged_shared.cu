@@ -9,11 +9,11 @@
 // bytes are read once instead of S times, and the rows that meet a key are S times as many, which is what the tensor
 // cores need. Then each sequence attends to its own keys. Both are the kernels of gk_paged_attn, and neither waits for
 // the other (begin(), paged_attn.cuh).
-// Measured: a token of 64 sequences behind 16384 shared 8-bit keys and up to 1024 own ones, 32 heads over 8 of 128: 83 us
+// Measured: a token of 64 sequences behind 16384 shared 8-bit keys and up to 1024 own ones, 32 heads over 8 of 128: 81 us
 // (gk_paged_attn 365): 19 own keys beside 23 that lay the codes out as bf16, 42 the prefix in tiles of 128 rows (8 key
-// tiles a block at 2.7 us, its softmax warps' rate for codes, and 15 to begin and end), 12 the join; bf16 pages 58. 7
-// groups of up to 16 sequences behind up to 8100 keys, 12 heads of 64, bf16: 43 us, 3.0 TB/s (122): blocks of few tiles, a
-// third of their time the loads that lead to the first key. Chunks of 256 behind 16384 keys, 12 sequences a group: 784
+// tiles a block at 2.7 us, its softmax warps' rate for codes, and 15 to begin and end), 10 the join; bf16 pages 56. 7
+// groups of up to 16 sequences behind up to 8100 keys, 12 heads of 64, bf16: 41 us, 3.1 TB/s (122): blocks of few tiles, a
+// third of their time the loads that lead to the first key. Chunks of 256 behind 16384 keys, 12 sequences a group: 782
 // (787): the tensor cores' part bounds both.
 #include <math.h>
 
