@@ -508,8 +508,8 @@ gk_status gk_paged_attn_shared(gk_ctx* ctx, const gk_paged_kv* cache, int dtype,
  * sequence with rows in the call
  *   mass[j, hk] = decay * old[j, hk] + sum_{rows i that see j} sum_{heads h of hk} exp(scale q[i, h] . k[j] - lse[i, h]),
  * without the first term for the call's own tokens (the sequence's last n positions) or where old is NULL.
- *   old, mass  float32 [n_pages][Hkv][page_size] (16-byte aligned), the value of the token in that row of the page; the same array
- *              or two that do not overlap. mass is changed at the positions named alone.
+ *   old, mass  float32 [n_pages][Hkv][page_size] (16-byte aligned), the value of the token in that row of the page; the
+ *              same array or two that do not overlap. mass is changed at the positions named alone.
  *   decay      finite, not negative: 1 adds up, less than 1 forgets.
  *   first      device int32 [B] or NULL (0): positions below it are not weighed (a prefix that other sequences hold
  *              too). Two sequences of a call must not hold one row of a page at positions that are.
@@ -533,8 +533,8 @@ gk_status gk_paged_mass(gk_ctx* ctx, const gk_paged_kv* cache, int dtype, const 
  *   cache, mass  the sequences (kv_len read from the device) and their tokens' mass, as for gk_paged_mass. A NaN
  *                counts as the least.
  *   to, to_mass  where they go: dtype, Hkv, page_size and hs as of cache; other pages of the same arrays (with mass ==
- *                to_mass), or other arrays. to->kv_len is not read, and may be new_len. Rows behind a sequence's new
- *                length are left as they were.
+ *                to_mass, else GK_ERR_ARG), or other arrays. to->kv_len is not read, and may be new_len. Rows behind a
+ *                sequence's new length are left as they were.
  *   first        device int32 [B] or NULL (0); held to 0 .. kv_len[b].
  *   budget       1 .. 2^30; recent 0 .. budget.
  *   new_len      device int32 [B];  kept  device int32 [B][Hkv][budget]. new_len must not overlap cache->kv_len.
