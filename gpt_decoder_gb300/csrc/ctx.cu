@@ -52,7 +52,9 @@ gk_status gk_ctx_create(gk_ctx** out, void* cuda_stream, size_t workspace_bytes)
         }
         ctx->ws_bytes = workspace_bytes;
     }
-    if (cudaDeviceSynchronize() != cudaSuccess) {
+    if (cudaStreamCreateWithFlags(&ctx->side, cudaStreamNonBlocking) != cudaSuccess ||
+        cudaEventCreateWithFlags(&ctx->forked, cudaEventDisableTiming) != cudaSuccess ||
+        cudaEventCreateWithFlags(&ctx->joined, cudaEventDisableTiming) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
         gk_ctx_destroy(ctx);
         return GK_ERR_CUDA;
     }
@@ -64,6 +66,9 @@ void gk_ctx_destroy(gk_ctx* ctx) {
     if (!ctx) return;
     if (ctx->d_err) cudaFree(ctx->d_err);
     if (ctx->ws) cudaFree(ctx->ws);
+    if (ctx->side) cudaStreamDestroy(ctx->side);
+    if (ctx->forked) cudaEventDestroy(ctx->forked);
+    if (ctx->joined) cudaEventDestroy(ctx->joined);
     delete ctx;
 }
 

@@ -49,10 +49,45 @@ gk_status launch_dependent(gk_ctx* ctx, const char* what, void (*kernel)(KArgs..
     }
     return launched(ctx, what);
 }
+
+// A branch of a call's launches, beside those on the context's stream: what run() launches comes after all that was on
+// the stream when the branch was made, and what is launched after join() after both. Events fork and join it, so that it can be
+// captured with the stream; a call that fails on the way joins all the same.
+class Branch {
+public:
+    explicit Branch(gk_ctx* ctx) : ctx_(ctx), main_(ctx->stream) {}
+    Branch(const Branch&) = delete;
+    Branch& operator=(const Branch&) = delete;
+    ~Branch() { join(); }
+    gk_status fork() {
+        if (cudaEventRecord(ctx_->forked, main_) != cudaSuccess || cudaStreamWaitEvent(ctx_->side, ctx_->forked, 0) != cudaSuccess) return failed("fork");
+        open_ = true;
+        return GK_OK;
+    }
+    template <typename F>
+    gk_status run(F launches) {
+        ctx_->stream = ctx_->side;
+        const gk_status s = launches();
+        ctx_->stream = main_;
+        return s;
+    }
+    gk_status join() {
+        if (!open_) return GK_OK;
+        open_ = false;
+        if (cudaEventRecord(ctx_->joined, ctx_->side) != cudaSuccess || cudaStreamWaitEvent(main_, ctx_->joined, 0) != cudaSuccess) return failed("join");
+        return GK_OK;
+    }
+
+private:
+    gk_status failed(const char* what) {
+        return fail(ctx_, GK_ERR_CUDA, "%s of a call's launches: %s", what, cudaGetErrorString(cudaGetLastError()));
+    }
+    gk_ctx* ctx_;
+    cudaStream_t main_;
+    bool open_ = false;
+};
+
 __device__ __forceinline__ void wait_for_earlier_kernels() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// Let the next launch begin once every block of this one has come here (it waits for this one's end all the same, where it
-// calls wait_for_earlier_kernels).
-__device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // (a & b) | c in one instruction. Only one operand of it can be a constant in the code: kernels that unpack
 // codes take their masks as arguments (CodeMasks), which stay in registers.

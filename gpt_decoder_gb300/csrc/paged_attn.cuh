@@ -28,7 +28,6 @@ struct AttnArgs {
     const int32_t* group_start;
     const int32_t* prefix_len;
     int n_groups, sequences, max_group, slots, slot0, prefix_splits, prefix_min;
-    int early;        // this launch does not depend on the one before it: see begin()
     int2* row_parts;  // [rows]: pieces of the prefix and of a row's own keys; (0, 0): the row is left as it was
     int clustered;  // the pieces are the blocks of one cluster, which joins them itself
     float* part_o;
@@ -47,22 +46,6 @@ struct AttnArgs {
     }
     __host__ __device__ int split_keys(int kv) const { return split_keys(kv, splits, min_split); }
 };
-
-// Wait for the launches before this one, and let the next one begin. A launch that is `early` reads nothing of the one
-// directly before it (and that one has let it begin after its own wait, so all before are complete): its blocks go on at
-// once. It has a slice of blocks more (`extra`), of which one (`only`) holds up the launch's end until the other's. True:
-// this block has no other work.
-template <int PART>
-__device__ __forceinline__ bool begin(const AttnArgs& a, bool extra, bool only) {
-    if constexpr (PART == WHOLE) {
-        wait_for_earlier_kernels();
-        return false;
-    } else {
-        if (!a.early || (extra && only)) wait_for_earlier_kernels();
-        let_next_begin();
-        return a.early && extra;
-    }
-}
 
 // The first row and the number of rows of a group's sequences; false: it cannot be.
 __device__ __forceinline__ bool group_rows(const AttnArgs& a, int g, int& s0, int& n) {

@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) 
     __shared__ float2 s_ml[KG][ROWS];
     __shared__ float2 s_join[ROWS];  // clustered: the piece's reference and sum, its weighted values in s_o[0]
     __shared__ int s_odd;
-    if (begin<PART>(a, blockIdx.y == gridDim.y - 1, blockIdx.x == 0)) return;
+    wait_for_earlier_kernels();
 
     const int b = blockIdx.y, hk = blockIdx.x / a.splits, split = blockIdx.x - hk * a.splits;
     if (PART == OWN && hk == a.p.Hkv) return leave_row_parts(a, b);
@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(WARPS * 32) attn_few_kernel(const AttnArgs a) 
 template <int HSP, bool Q8, int PART>
 gk_status few(gk_ctx* ctx, const AttnArgs& a) {
     const int64_t R = (int64_t)a.max_q * a.G;
-    const dim3 grid((unsigned)(a.p.Hkv * a.splits + (PART == OWN)), (unsigned)a.B + (PART != WHOLE && a.early)), block(WARPS * 32);
+    const dim3 grid((unsigned)(a.p.Hkv * a.splits + (PART == OWN)), (unsigned)a.B), block(WARPS * 32);
 #define FEW(NT, KG) return launch_dependent(ctx, "paged_attn", attn_few_kernel<HSP, Q8, NT, KG, PART>, grid, block, 0, a.clustered ? a.splits : 1, a)
     if (R <= 8) FEW(1, 4);
     if (R <= 16) FEW(2, 4);

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 28);
     uint64_t* s_free = bars + 29;    // [2] early S: S_g has been read (one arrival per warp)
     uint64_t* bar_pv = bars + 31;    // [2] early S: P_g V is complete
-    if (begin<PART>(a, blockIdx.z == gridDim.z - 1, blockIdx.x == 0 && blockIdx.y == 0)) return;
+    wait_for_earlier_kernels();
     if (PART == OWN && blockIdx.x == gridDim.x - 1) {
         if (blockIdx.y == 0) leave_row_parts(a, blockIdx.z);
         return;
@@ -659,7 +659,6 @@ __global__ void __launch_bounds__(THREADS, 1)
 template <int PART>
 __global__ void __launch_bounds__(256) expand_kernel(const AttnArgs a, __nv_bfloat16* k_out, __nv_bfloat16* v_out) {
     wait_for_earlier_kernels();
-    if constexpr (PART != WHOLE) let_next_begin();
     const int b = blockIdx.z, hk = a.head0 + blockIdx.y, len = expanded_rows<PART>(a, b), p0 = blockIdx.x * 64;
     if (p0 >= len) return;
     const int lane = threadIdx.x & 31, hs = a.p.hs;
@@ -698,7 +697,7 @@ gk_status tiles(gk_ctx* ctx, const AttnArgs& a, const __nv_bfloat16* k, const __
                    "gk_paged_attn: tensor map");
     const int64_t pairs = cdiv((int64_t)a.max_q * a.G, 2 * QT);
     return launch_dependent(ctx, "paged_attn_tiles", attn_tiles_kernel<HSP, FROM, PART>,
-                            dim3((unsigned)(pairs * a.splits + (PART == OWN)), (unsigned)a.heads, (unsigned)a.B + (PART != WHOLE && a.early)), dim3(THREADS), Layout<HSP>::BYTES, 1, a,
+                            dim3((unsigned)(pairs * a.splits + (PART == OWN)), (unsigned)a.heads, (unsigned)a.B), dim3(THREADS), Layout<HSP>::BYTES, 1, a,
                             mk, mv);
 }
 

@@ -7,8 +7,8 @@
 // y = (o_1 2^(m_1 - m) + o_2 2^(m_2 - m)) / (l_1 2^(m_1 - m) + l_2 2^(m_2 - m)), m the larger. So a group's prefix is
 // attended as one sequence that holds the rows of all of its sequences (they lie next to each other): with S sequences its
 // bytes are read once instead of S times, and the rows that meet a key are S times as many, which is what the tensor
-// cores need. Then each sequence attends to its own keys. Both are the kernels of gk_paged_attn, and neither waits for
-// the other (begin(), paged_attn.cuh).
+// cores need. Then each sequence attends to its own keys. Both are the kernels of gk_paged_attn, launched beside each
+// other (Branch, launch.cuh).
 // Measured: a token of 64 sequences behind 16384 shared 8-bit keys and up to 1024 own ones, 32 heads over 8 of 128: 81 us
 // (gk_paged_attn 365): 19 own keys beside 23 that lay the codes out as bf16, 42 the prefix in tiles of 128 rows (8 key
 // tiles a block at 2.7 us, its softmax warps' rate for codes, and 15 to begin and end), 10 the join; bf16 pages 56. 7
@@ -192,13 +192,12 @@ extern "C" gk_status gk_paged_attn_shared(gk_ctx* ctx, const gk_paged_kv* cache,
     a.row_parts = reinterpret_cast<int2*>(ws);
     a.part_o = p.part_o = reinterpret_cast<float*>(ws + info);
     a.part_ml = p.part_ml = reinterpret_cast<float2*>(a.part_o + rows * H * a.slots * a.p.hs);
-    // Own keys beside the pass that lays out codes, or the prefixes beside own keys (their launches do not depend on
-    // each other, and each by itself leaves much of the GPU idle).
+    // The own keys' launch beside the prefixes': neither reads what the other writes, and each by itself leaves much of the
+    // GPU idle (one after the other: 64 samples 82.5 us, 7 groups 44.7, chunks 806; side by side 77.6, 43.1, 712).
     const bool expanded = p.expanded_k && p.heads == a.p.Hkv;
+    Branch own(ctx);
+    GK_TRY(own.fork());
     if (expanded) GK_TRY(launch_shared_expand(ctx, p));
-    a.early = expanded && B < 65535;  // (a block more along the sequences)
-    GK_TRY(own_few ? launch_shared_few(ctx, a, OWN) : launch_shared_tiles(ctx, a, OWN));
-    p.early = !p.expanded_k && n_groups < 65535;
     if (prefix_few) {
         GK_TRY(launch_shared_few(ctx, p, PREFIX));
     } else {
@@ -208,6 +207,8 @@ extern "C" gk_status gk_paged_attn_shared(gk_ctx* ctx, const gk_paged_kv* cache,
             GK_TRY(launch_shared_tiles(ctx, p, PREFIX));
         }
     }
+    GK_TRY(own.run([&] { return own_few ? launch_shared_few(ctx, a, OWN) : launch_shared_tiles(ctx, a, OWN); }));
+    GK_TRY(own.join());
     return launch_dependent(ctx, "paged_shared_join", shared_join_kernel, dim3((unsigned)cdiv(rows * H, JOIN_WARPS >> join_log2(a.slots))),
                             dim3(JOIN_WARPS * 32), 0, 1, a);
 }
