@@ -24,10 +24,10 @@
 // Registers: 512 threads at 128; the softmax warpgroups take 184 each, the copying one 96, the MMA warp's
 // 48 (where the copying one unpacks codes: 176, 104, 48).
 // All mbarrier waits are bounded (timeout -> GK_ERR_TIMEOUT in the error word).
-// Measured: two chunks of up to 2048 tokens behind 16384 keys, 32 heads over 8 of 128: bf16 pages 494 us, 1.07
+// Measured: two chunks of up to 2048 tokens behind 16384 keys, 32 heads over 8 of 128: bf16 pages 498 us, 1.06
 // PFLOP/s (0.55 of a dense product); 8-bit ones 670 us with the pass that expands them (1980 unpacked on the way):
 // the softmax warps bound both, by a thread's 128 exponentials, maxima and packing a tile, for 8 bits by two more
-// products a score. Three chunks of up to 1000 over 8100 keys, 12 heads of 64: 85 us (half the products a tile for
+// products a score. Three chunks of up to 1000 over 8100 keys, 12 heads of 64: 86 us (half the products a tile for
 // the same softmax). Key tiles that two groups of blocks read side by side come from L2.
 #include "paged_attn_tiles.cuh"
 

@@ -365,7 +365,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                         for (int i = 0; i < 4 * L::HALVES; ++i) {
                             const int r = i / L::HALVES * 4 + lane / 8, c = (i % L::HALVES) * 8 + lane % 8;
                             uint4 x = make_uint4(0, 0, 0, 0);
-                            if (!none && grp * 16 + r < left && (PART != OWN || it.k_begin + j * KT + grp * 16 + r >= it.from) && c * 8 < hs) x = __ldg(reinterpret_cast<const uint4*>(src + r * row_bytes + c * 16));
+                            if (!none && grp * 16 + r < left && c * 8 < hs) x = __ldg(reinterpret_cast<const uint4*>(src + r * row_bytes + c * 16));
+                            if constexpr (PART == OWN)  // (in the load's condition it costs whole sequences' kernel registers: chunks 0.6% longer)
+                                if (it.k_begin + j * KT + grp * 16 + r < it.from) x = make_uint4(0, 0, 0, 0);
                             odd |= drop_odd2(x.x) | drop_odd2(x.y) | drop_odd2(x.z) | drop_odd2(x.w);
                             *reinterpret_cast<uint4*>(tile + (c >> 3) * HALF + swizzled(grp * 16 + r, c & 7)) = x;
                         }
