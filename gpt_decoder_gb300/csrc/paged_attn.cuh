@@ -28,6 +28,7 @@ struct AttnArgs {
     const int32_t* group_start;
     const int32_t* prefix_len;
     int n_groups, sequences, max_group, slots, slot0, prefix_splits, prefix_min;
+    bool fine;        // PREFIX in tiles: weights as two bf16 parts
     int2* row_parts;  // [rows]: pieces of the prefix and of a row's own keys; (0, 0): the row is left as it was
     int clustered;  // the pieces are the blocks of one cluster, which joins them itself
     float* part_o;
@@ -137,9 +138,11 @@ gk_status launch_attn_join(gk_ctx* ctx, const AttnArgs& a);
 gk_status launch_attn_few(gk_ctx* ctx, const AttnArgs& a);
 // Any number of rows, for heads head0 .. head0 + heads - 1, in tiles of 128 on the tensor cores (tcgen05).
 gk_status launch_attn_tiles(gk_ctx* ctx, const AttnArgs& a);
-// The same for the prefixes of groups (PREFIX) or what follows them (OWN), which leave parts.
+// The same for the prefixes of groups (PREFIX) or what follows them (OWN), which leave parts; prefixes in tiles with
+// weights of 16 bits where a.fine.
 gk_status launch_shared_few(gk_ctx* ctx, const AttnArgs& a, int part);
 gk_status launch_shared_tiles(gk_ctx* ctx, const AttnArgs& a, int part);
+gk_status launch_shared_fine(gk_ctx* ctx, const AttnArgs& a);
 // 8-bit codes of the prefixes as bf16, before the tiles that take them.
 gk_status launch_shared_expand(gk_ctx* ctx, const AttnArgs& a);
 

@@ -78,13 +78,16 @@ struct Item {
 enum { PAGES16, PAGES8, EXPANDED };
 constexpr uint32_t ODD_SCALES = 1u << 31;  // beside a tile's refused groups: some value's scale is not finite
 
-template <int HSP, int FROM, int PART>
+// FINE: weights as two bf16 parts (16 significant bits), the lower one's product after the other's. S waits for both then
+// (P's two parts fill the columns of its scores), as with heads of 128 without.
+template <int HSP, int FROM, int PART, bool FINE>
 __global__ void __launch_bounds__(THREADS, 1)
     attn_tiles_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
     constexpr bool Q8 = FROM != PAGES16;
     using L = Layout<HSP>;
-    constexpr bool EARLY = HSP == 64;  // the next S before P V
+    constexpr bool EARLY = HSP == 64 && !FINE;  // the next S before P V
     constexpr uint32_t P_AT = EARLY ? 384 : 0, P_STEP = EARLY ? 64 : 128;  // tensor memory columns of P_g
+    constexpr uint32_t P_LOW = 64;                                        // FINE: its lower part's, from there (over S too)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sQ = smem;           // [2 tiles][halves]
@@ -239,6 +242,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                         for (int kk = 0; kk < KT / 16; ++kk)
                             umma_bf16_ts(tmem + 256 + g * HSP, tmem + P_AT + g * P_STEP + kk * 8, desc_add(v_d, stage * L::TILE + kk * 2048),
                                          id_o, (j > 0 || kk > 0) ? 1u : 0u);
+                        if constexpr (FINE)
+#pragma unroll
+                            for (int kk = 0; kk < KT / 16; ++kk)
+                                umma_bf16_ts(tmem + 256 + g * HSP, tmem + P_AT + g * P_STEP + P_LOW + kk * 8, desc_add(v_d, stage * L::TILE + kk * 2048),
+                                             id_o, 1u);
                         if (EARLY) umma_commit(&bar_pv[g]);
                         if (j == it.tiles(g) - 1) umma_commit(&bar_o[g]);
                     }
@@ -543,6 +551,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t pw[16];
+                    [[maybe_unused]] uint32_t low[FINE ? 16 : 1];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         uint32_t* w = &sv[c][4 * e];
@@ -566,8 +575,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                         pw[2 * e] = pack2(p[0], p[1]);
                         pw[2 * e + 1] = pack2(p[2], p[3]);
+                        if constexpr (FINE)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)
+                                low[2 * e + x] = pack2(p[2 * x] - __uint_as_float(pw[2 * e + x] << 16), p[2 * x + 1] - __uint_as_float(pw[2 * e + x] & 0xffff0000u));
                     }
                     tmem_st16(lane_addr + P_AT + g * P_STEP + c * 16, pw);
+                    if constexpr (FINE) tmem_st16(lane_addr + P_AT + g * P_STEP + P_LOW + c * 16, low);
                 }
             };
             if (Q8 && (bad & ODD_SCALES)) weights(std::true_type{});
@@ -690,15 +704,15 @@ __global__ void __launch_bounds__(256) expand_kernel(const AttnArgs a, __nv_bflo
     }
 }
 
-template <int HSP, int FROM, int PART>
+template <int HSP, int FROM, int PART, bool FINE = false>
 gk_status tiles(gk_ctx* ctx, const AttnArgs& a, const __nv_bfloat16* k, const __nv_bfloat16* v, int64_t rows, int box) {
-    GK_TRY((allow_shared<attn_tiles_kernel<HSP, FROM, PART>>(ctx, "gk_paged_attn", Layout<HSP>::BYTES)));
+    GK_TRY((allow_shared<attn_tiles_kernel<HSP, FROM, PART, FINE>>(ctx, "gk_paged_attn", Layout<HSP>::BYTES)));
     CUtensorMap mk{}, mv{};
     if (FROM != PAGES8)
         GK_REQUIRE(ctx, make_map(&mk, k, a.p.hs, rows, a.p.hs, box) && make_map(&mv, v, a.p.hs, rows, a.p.hs, box), GK_ERR_CUDA,
                    "gk_paged_attn: tensor map");
     const int64_t pairs = cdiv((int64_t)a.max_q * a.G, 2 * QT);
-    return launch_dependent(ctx, "paged_attn_tiles", attn_tiles_kernel<HSP, FROM, PART>,
+    return launch_dependent(ctx, "paged_attn_tiles", attn_tiles_kernel<HSP, FROM, PART, FINE>,
                             dim3((unsigned)(pairs * a.splits + (PART == OWN)), (unsigned)a.heads, (unsigned)a.B), dim3(THREADS), Layout<HSP>::BYTES, 1, a,
                             mk, mv);
 }
@@ -709,21 +723,21 @@ gk_status launch_expand(gk_ctx* ctx, const AttnArgs& a) {
                             dim3(256), 0, 1, a, a.expanded_k, a.expanded_v);
 }
 
-template <int PART>
+template <int PART, bool FINE = false>
 gk_status launch_tiles(gk_ctx* ctx, const AttnArgs& a) {
     const bool small = a.p.hs <= 64;
     if constexpr (PART != OWN)
     if (a.expanded_k) {
         const int64_t rows = a.expanded_rows;
         if constexpr (PART == WHOLE) GK_TRY(launch_expand<PART>(ctx, a));  // (prefixes: launched before)
-        return small ? tiles<64, EXPANDED, PART>(ctx, a, a.expanded_k, a.expanded_v, rows, KT)
-                     : tiles<128, EXPANDED, PART>(ctx, a, a.expanded_k, a.expanded_v, rows, KT);
+        return small ? tiles<64, EXPANDED, PART, FINE>(ctx, a, a.expanded_k, a.expanded_v, rows, KT)
+                     : tiles<128, EXPANDED, PART, FINE>(ctx, a, a.expanded_k, a.expanded_v, rows, KT);
     }
-    if (a.p.k_scale) return small ? tiles<64, PAGES8, PART>(ctx, a, nullptr, nullptr, 0, 0) : tiles<128, PAGES8, PART>(ctx, a, nullptr, nullptr, 0, 0);
+    if (a.p.k_scale) return small ? tiles<64, PAGES8, PART, FINE>(ctx, a, nullptr, nullptr, 0, 0) : tiles<128, PAGES8, PART, FINE>(ctx, a, nullptr, nullptr, 0, 0);
     const int64_t rows = (a.p.n_pages * a.p.Hkv) << a.p.page_log2;
     const __nv_bfloat16 *k = static_cast<const __nv_bfloat16*>(a.p.k), *v = static_cast<const __nv_bfloat16*>(a.p.v);
     const int box = std::min(KT, 1 << a.p.page_log2);
-    return small ? tiles<64, PAGES16, PART>(ctx, a, k, v, rows, box) : tiles<128, PAGES16, PART>(ctx, a, k, v, rows, box);
+    return small ? tiles<64, PAGES16, PART, FINE>(ctx, a, k, v, rows, box) : tiles<128, PAGES16, PART, FINE>(ctx, a, k, v, rows, box);
 }
 
 }  // namespace

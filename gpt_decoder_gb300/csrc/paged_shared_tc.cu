@@ -4,7 +4,8 @@
 namespace gk {
 
 gk_status launch_shared_tiles(gk_ctx* ctx, const AttnArgs& a, int part) {
-    return part == PREFIX ? launch_tiles<PREFIX>(ctx, a) : launch_tiles<OWN>(ctx, a);
+    if (part == PREFIX) return a.fine ? launch_shared_fine(ctx, a) : launch_tiles<PREFIX>(ctx, a);
+    return launch_tiles<OWN>(ctx, a);
 }
 
 gk_status launch_shared_expand(gk_ctx* ctx, const AttnArgs& a) { return launch_expand<PREFIX>(ctx, a); }

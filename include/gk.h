@@ -490,6 +490,7 @@ gk_status gk_paged_attn(gk_ctx* ctx, const gk_paged_kv* cache, int dtype, const 
  *   sequence's own, with a copy of its tokens.) Which of these rows the prefix is looked up in is open. A sequence that
  *   is in no group shares nothing, and neither does one whose new rows do not all lie behind the prefix (kv_len[b] - n <
  *   prefix_len[g], padding rows among them): its keys are read for it alone.
+ *   Weights have as many bits as gk_paged_attn gives them, by max_q and not by a group's rows.
  *   n_groups    1 .. 65535.
  *   max_group_q at least every group's number of rows (host, as max_q). A group with more, or with sequences past B,
  *               records GK_ERR_INDEX and its rows are left as they were; so does a prefix_len past the table, the part

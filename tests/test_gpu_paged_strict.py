@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 from oracle import serving
-from tests.test_gpu_paged_more import shared_cache
+from tests.test_gpu_paged_more import attend_shared, shared_cache, shared_ref
 from tests.test_gpu_serving import Dev, dev, starts
 
 pytestmark = pytest.mark.gpu
@@ -88,3 +88,66 @@ def test_shared_sees_what_was_launched_before_and_keeps_it_from_what_follows(S, 
             assert all(t.equal(a, b) for a, b in zip(taken(), want))
         gk.gk_sync(ctx)
     ctx.close()
+
+
+# ----------------------------------------------------------------------------------------- rounding
+def few_heavy_keys(rng, S, n, H, Hkv, hs, page, q8, prefix=2100, tail=6):
+    """Sequences behind one prefix in which three keys of it and one own one share all of the weight, their values near 1 and
+    -1: sums cancel, and what a weight was rounded to shows. (cache, rows, new tokens, group_start, prefix_len)"""
+    c, ns, gs, pl = shared_cache(rng, [(prefix, [(tail + n, n)] * S)], Hkv, hs, page, False)
+    k = rng.standard_normal(c.k.shape).astype(np.float32) * np.float32(0.3)
+    k[..., 0] = -24
+    v = rng.standard_normal(c.v.shape).astype(np.float32)
+    at = [c.place(0, j) for j in (17, 1200, prefix - 130)] + [c.place(b, prefix + 3) for b in range(S)]
+    pg, rw = (np.array(x) for x in zip(*at))
+    k[pg, :, rw] = rng.standard_normal((len(at), Hkv, hs))
+    k[pg, :, rw, 0] = 4
+    v[pg, :, rw] = rng.choice([-1, 1], (len(at), Hkv, hs)) * rng.uniform(0.9, 1.1, (len(at), Hkv, hs))
+    if q8:
+        (kc, ks), (vc, vs) = serving.quantise(k), serving.quantise(v)
+        c = serving.Pages(kc, vc, ks, vs, c.table, c.kv_len)
+    else:
+        c = serving.Pages(serving.bf16(k), serving.bf16(v), None, None, c.table, c.kv_len)
+    # (a page in which the prefix ends is each sequence's own: the same tokens)
+    if prefix % page:
+        for x in (c.k, c.v, c.k_scale, c.v_scale):
+            if x is not None:
+                x[c.table[:, prefix // page], :, : prefix % page] = x[c.table[0, prefix // page], :, : prefix % page]
+    q = rng.standard_normal((sum(ns), H, hs)) * 0.5
+    q[..., 0] = 16
+    return c, serving.bf16(q), ns, gs, pl
+
+
+# Beside y's own rounding (half a step of bf16: 2^-8 |y|) a weight of 16 bits may be off by 2^-17 relative, and by what its
+# float32 score is: a sum of hs products, each addition cut by a step of 2^-23 of a running sum of at most scale sum |q||k| <
+# 9.5 here, 128 2^-23 9.5 = 2^-12.7; the same again in the sum of weights that divides. Together below 2^-11.5 of the spread
+# sum w |v|. (Weights rounded to bf16 are off by up to 2^-8 each.)
+FINE = 2.0 ** -11.5
+
+
+@pytest.mark.parametrize("S,n,H,Hkv,hs,page,q8,ws", [
+    (64, 1, 8, 2, 128, 64, True, 64),  # 256 rows, codes laid out as bf16 first
+    (64, 1, 8, 2, 128, 64, True, 2),  # no room for that: unpacked on the way
+    (40, 1, 4, 2, 64, 16, True, 64),
+    (130, 1, 4, 1, 64, 32, True, 64),  # more than 512 rows
+    (40, 1, 2, 2, 64, 64, False, 64),
+    (36, 3, 4, 2, 128, 128, False, 64),
+    (9, 8, 4, 1, 96, 256, False, 64),
+    (10, 16, 4, 1, 80, 16, True, 64),
+    (5, 1, 4, 1, 64, 64, True, 64),  # few rows in all
+])
+def test_shared_weights_of_few_rows_have_16_bits(S, n, H, Hkv, hs, page, q8, ws):
+    """As many rows as a sequence may have (64 a key / value head over 8-bit pages, 32 over bf16), in groups of many more."""
+    from gpt_decoder_gb300 import gk
+
+    assert n * H // Hkv <= (64 if q8 else 32)
+    rng = np.random.default_rng(4100 + S + hs)
+    c, q, ns, gs, pl = few_heavy_keys(rng, S, n, H, Hkv, hs, page, q8)
+    scale = hs ** -0.5
+    y_ref, lse_ref, spread = shared_ref(c, q, ns, gs, pl, scale)
+    ctx = gk.Ctx(_t().cuda.current_stream().cuda_stream, workspace_bytes=ws << 20)
+    y, lse = attend_shared(ctx, c, q, ns, gs, pl, scale)
+    ctx.close()
+    off = np.abs(y - y_ref) - 2.0 ** -8 * np.abs(y_ref)
+    assert off.max() <= FINE * spread.max() and (off <= FINE * spread).all(), (off / spread).max()
+    assert np.abs(lse - lse_ref).max() < 2.0 ** -11.5
