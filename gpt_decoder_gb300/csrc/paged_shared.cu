@@ -165,25 +165,30 @@ extern "C" gk_status gk_paged_attn_shared(gk_ctx* ctx, const gk_paged_kv* cache,
     p.fine = own_few && !prefix_few;
     p.B = n_groups;
     p.max_q = a.max_group;
+    int64_t prefix_splits, own_splits;
+    const int64_t pairs = prefix_few ? 1 : cdiv(group_rows, 256);  // blocks a prefix and head
+    split_prefixes(ctx, prefix_few, n_groups * a.p.Hkv * pairs, a.p.capacity, &prefix_splits, &p.min_split);
+    split_own(ctx, own_few, (int64_t)B * a.p.Hkv * (own_few ? 1 : cdiv(own_rows, 256)), a.p.capacity, &own_splits, &a.min_split);
+    if (room < info + 2 * per) return gk_paged_attn(ctx, cache, dtype, q, ldq, y, ldy, lse, q_start, B, H, rows, max_q, scale);
     if (!prefix_few && a.p.k_scale && (a.p.hs > 64 || group_rows > 512)) {
-        // 8-bit codes laid out as bf16 first, as in gk_paged_attn: of the prefixes, all heads or a few at a time
+        // 8-bit codes laid out as bf16 first, as in gk_paged_attn: of the prefixes, all heads or a few at a time, in what the
+        // rows' parts leave of the workspace. (64 samples behind 15300 keys, 8 heads of 128: 81 us with 96 MB; 64 MB hold 21
+        // parts of the rows but not the codes beside them, which are then unpacked on the way: 96 us, each sequence alone 338.)
+        const int64_t parts = info + std::min<int64_t>(512, prefix_splits + own_splits) * per, left = std::max<int64_t>(0, (int64_t)room - parts);
         const int64_t er = (int64_t)n_groups * cdiv(a.p.capacity, 128) * 128, bytes = er * a.p.hs * 2;  // of a head
-        const int64_t fit = (int64_t)(room / 2) >= bytes * a.p.Hkv ? a.p.Hkv : (int64_t)(room / 8 * 3) / bytes;
+        const int64_t fit = std::min<int64_t>(a.p.Hkv, left / (2 * bytes));
         const int64_t turns = fit ? cdiv(a.p.Hkv, fit) : 0, heads = fit ? cdiv(a.p.Hkv, turns) : 0;
-        if (fit && er * heads < (1ll << 31) && (turns == 1 || 2 * heads * n_groups * cdiv(group_rows, 256) >= ctx->num_sms)) {
+        if (fit && er * heads < (1ll << 31) && (turns == 1 || 2 * heads * n_groups * pairs >= ctx->num_sms)) {
             p.heads = (int)heads;
             p.expanded_k = reinterpret_cast<__nv_bfloat16*>(ws);
             p.expanded_v = reinterpret_cast<__nv_bfloat16*>(ws + bytes * heads);
             p.expanded_rows = er * heads;
             ws += 2 * bytes * heads;
             room -= 2 * (size_t)(bytes * heads);
+            split_prefixes(ctx, prefix_few, n_groups * heads * pairs, a.p.capacity, &prefix_splits, &p.min_split);
         }
     }
-    int64_t prefix_splits, own_splits;
-    split_prefixes(ctx, prefix_few, (int64_t)n_groups * p.heads * (prefix_few ? 1 : cdiv(group_rows, 256)), a.p.capacity, &prefix_splits, &p.min_split);
-    split_own(ctx, own_few, (int64_t)B * a.p.Hkv * (own_few ? 1 : cdiv(own_rows, 256)), a.p.capacity, &own_splits, &a.min_split);
-    const int64_t slots = room < info ? 0 : std::min<int64_t>(512, (int64_t)((room - info) / per));
-    if (slots < 2) return gk_paged_attn(ctx, cache, dtype, q, ldq, y, ldy, lse, q_start, B, H, rows, max_q, scale);
+    const int64_t slots = std::min<int64_t>(512, (int64_t)((room - info) / per));
     prefix_splits = std::min(prefix_splits, std::max<int64_t>(1, slots * prefix_splits / (prefix_splits + own_splits)));
     own_splits = std::min(own_splits, slots - prefix_splits);
     p.splits = (int)prefix_splits;

@@ -496,9 +496,11 @@ gk_status gk_paged_attn(gk_ctx* ctx, const gk_paged_kv* cache, int dtype, const 
  *               records GK_ERR_INDEX and its rows are left as they were; so does a prefix_len past the table, the part
  *               of it that is there being attended.
  * Infinities, NaN and refused pages are as with gk_paged_attn. Uses the context's workspace for the parts of a row's
- * keys, (hs * 4 + 8) * H bytes a row and part, two parts at least. Where it has no room for them, the table has room for
+ * keys, (hs * 4 + 8) * H bytes a row and part, and 8 bytes a row; two parts at least. Prefixes of
+ * 8-bit pages are fastest where their codes as bf16 have room beside the parts: 4 * n_groups * max_pages * page_size * Hkv *
+ * hs bytes (max_pages * page_size rounded up to 128). Where there is no room for two parts, the table has room for
  * fewer than 2048 positions (max_pages * page_size) or there are more groups than half the sequences, the call
- * computes gk_paged_attn, which is faster there, and does not look at the groups. */
+ * computes gk_paged_attn and does not look at the groups. */
 gk_status gk_paged_attn_shared(gk_ctx* ctx, const gk_paged_kv* cache, int dtype, const void* q, int64_t ldq,
                                void* y, int64_t ldy, float* lse, const int32_t* q_start, int B,
                                const int32_t* group_start, const int32_t* prefix_len, int n_groups, int H,

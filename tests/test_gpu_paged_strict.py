@@ -5,7 +5,7 @@ import pytest
 
 from oracle import serving
 from tests.test_gpu_paged_more import attend_shared, shared_cache, shared_ref
-from tests.test_gpu_serving import Dev, dev, starts
+from tests.test_gpu_serving import Dev, check_attention, dev, starts
 
 pytestmark = pytest.mark.gpu
 
@@ -151,3 +151,24 @@ def test_shared_weights_of_few_rows_have_16_bits(S, n, H, Hkv, hs, page, q8, ws)
     off = np.abs(y - y_ref) - 2.0 ** -8 * np.abs(y_ref)
     assert off.max() <= FINE * spread.max() and (off <= FINE * spread).all(), (off / spread).max()
     assert np.abs(lse - lse_ref).max() < 2.0 ** -11.5
+
+
+# ----------------------------------------------------------------------------------------- workspace
+@pytest.mark.parametrize("width,mib", [(16384, 64), (16000, 64), (15008, 64), (14000, 64), (65536, 256), (16384, 96), (2048, 3)])
+def test_shared_8_bit_prefixes_leave_room_for_the_parts(width, mib):
+    """One group of 64 samples, 32 heads over 8 of 128, behind 8-bit pages, in workspaces that the prefix's codes as bf16 would
+    take whole (64 MiB: 16384 positions), nearly, or that hold two parts of every row and no codes: the shared way is taken, as an
+    impossible group shows, which gk_paged_attn would not look at."""
+    from gpt_decoder_gb300 import gk
+
+    rng = np.random.default_rng(4200)
+    H, Hkv, hs, page = 32, 8, 128, 16
+    c, ns, gs, pl = shared_cache(rng, [(190, [(9, 1)] * 64)], Hkv, hs, page, True)
+    c.table = np.pad(c.table[:, : 2048 // page], ((0, 0), (0, width // page - 2048 // page)), constant_values=-1)
+    assert (64 * H * (hs * 4 + 8)) * 2 + 64 * 8 <= mib << 20
+    q = serving.bf16(rng.standard_normal((64, H, hs)) * 2)
+    ctx = gk.Ctx(_t().cuda.current_stream().cuda_stream, workspace_bytes=mib << 20)
+    check_attention(*attend_shared(ctx, c, q, ns, gs, pl, 0.088), shared_ref(c, q, ns, gs, pl, 0.088))
+    y, lse = attend_shared(ctx, c, q, ns, gs, pl, 0.088, max_group=63, fails=True)
+    assert (y == 3).all() and (lse == 3).all()
+    ctx.close()
