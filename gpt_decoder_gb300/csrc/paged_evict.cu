@@ -13,6 +13,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <initializer_list>
 
 #include "paged.cuh"
 
@@ -302,13 +303,19 @@ extern "C" gk_status gk_paged_evict(gk_ctx* ctx, const gk_paged_kv* cache, const
     GK_TRY(check_pages(ctx, "gk_paged_evict", &t, new_len, B, 0, &a.to));
     GK_REQUIRE(ctx, to->dtype == cache->dtype && to->Hkv == cache->Hkv && to->page_size == cache->page_size && to->hs == cache->hs,
                GK_ERR_ARG, "gk_paged_evict: the two caches differ");
-    GK_REQUIRE(ctx, cache->k != to->k || (cache->v == to->v && cache->k_scale == to->k_scale && cache->v_scale == to->v_scale && mass == to_mass),
-               GK_ERR_ARG, "gk_paged_evict: one pool has one set of arrays");
+    // (an array of both beside one that is not: a page id would name other places in the one than in the other, and what is
+    // read of the shared one may be written)
+    const bool same = cache->k == to->k;
+    GK_REQUIRE(ctx, (cache->v == to->v) == same && (mass == to_mass) == same &&
+               (!a.from.k_scale || ((cache->k_scale == to->k_scale) == same && (cache->v_scale == to->v_scale) == same)),
+               GK_ERR_ARG, "gk_paged_evict: one pool has one set of arrays, and two have two");
     GK_REQUIRE(ctx, budget >= 1 && budget <= 1 << 30 && recent >= 0 && recent <= budget, GK_ERR_ARG, "gk_paged_evict: budget %d, recent %d",
                budget, recent);
     GK_REQUIRE(ctx, aligned16(mass) && aligned16(to_mass), GK_ERR_ALIGN, "gk_paged_evict: mass must be 16-byte aligned");
-    const uintptr_t x = (uintptr_t)new_len, y = (uintptr_t)cache->kv_len, len = (uintptr_t)B * sizeof(int32_t);
-    GK_REQUIRE(ctx, x + len <= y || y + len <= x, GK_ERR_ARG, "gk_paged_evict: new_len overlaps the old lengths");
+    const uintptr_t x = (uintptr_t)new_len, len = (uintptr_t)B * sizeof(int32_t);
+    for (const int32_t* read : {cache->kv_len, first})
+        GK_REQUIRE(ctx, !read || x + len <= (uintptr_t)read || (uintptr_t)read + len <= x, GK_ERR_ARG,
+                   "gk_paged_evict: new_len overlaps the old lengths or first");
     a.mass = mass;
     a.to_mass = to_mass;
     a.first = first;

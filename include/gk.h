@@ -535,12 +535,12 @@ gk_status gk_paged_mass(gk_ctx* ctx, const gk_paged_kv* cache, int dtype, const 
  * The tokens of one position differ by head afterwards; attention needs no more than their order.
  *   cache, mass  the sequences (kv_len read from the device) and their tokens' mass, as for gk_paged_mass. A NaN
  *                counts as the least.
- *   to, to_mass  where they go: dtype, Hkv, page_size and hs as of cache; other pages of the same arrays (with mass ==
- *                to_mass, else GK_ERR_ARG), or other arrays. to->kv_len is not read, and may be new_len. Rows behind a
+ *   to, to_mass  where they go: dtype, Hkv, page_size and hs as of cache; other pages of the same arrays (mass == to_mass
+ *                among them), or other arrays, all of them (GK_ERR_ARG where some are the same). to->kv_len is not read, and may be new_len. Rows behind a
  *                sequence's new length are left as they were.
  *   first        device int32 [B] or NULL (0); held to 0 .. kv_len[b].
  *   budget       1 .. 2^30; recent 0 .. budget.
- *   new_len      device int32 [B];  kept  device int32 [B][Hkv][budget]. new_len must not overlap cache->kv_len.
+ *   new_len      device int32 [B];  kept  device int32 [B][Hkv][budget]. new_len must not overlap cache->kv_len or first.
  * A page that is written must not be one that the call reads. The same page may stand in both tables only at the same
  * place, where all its positions are below first[b], or in sequences that keep all their tokens: what stays in its row
  * is not moved. A position without a page that exists records GK_ERR_INDEX: in cache its mass counts as the least (and if

@@ -5,7 +5,8 @@ import pytest
 
 from oracle import serving
 from tests.test_gpu_paged_more import attend_shared, shared_cache, shared_ref
-from tests.test_gpu_serving import Dev, check_attention, dev, starts
+from tests.test_gpu_serving import Dev, check_attention, dev, refused, starts
+from tests.test_oracle_serving import cache
 
 pytestmark = pytest.mark.gpu
 
@@ -171,4 +172,34 @@ def test_shared_8_bit_prefixes_leave_room_for_the_parts(width, mib):
     check_attention(*attend_shared(ctx, c, q, ns, gs, pl, 0.088), shared_ref(c, q, ns, gs, pl, 0.088))
     y, lse = attend_shared(ctx, c, q, ns, gs, pl, 0.088, max_group=63, fails=True)
     assert (y == 3).all() and (lse == 3).all()
+    ctx.close()
+
+
+# ------------------------------------------------------------------------------------------ refusals
+def test_evict_refuses_pools_that_share_some_arrays():
+    """Two pools with one array of values, of steps or of masses would be read and written at unlike places; new_len over first
+    would change what the call reads."""
+    from gpt_decoder_gb300 import gk
+
+    t = _t()
+    ctx = gk.Ctx(t.cuda.current_stream().cuda_stream, workspace_bytes=0)
+    for q8 in (False, True):
+        c, to = (cache(np.random.default_rng(i), [20], 2, 32, 16, q8) for i in (1, 2))
+        a, b = Dev(c, poison=False), Dev(to, poison=False)
+        assert a.k.shape == b.k.shape
+        ma, mb = (t.full(a.k.shape[:3], 4.0, device="cuda") for _ in range(2))
+        new, kept = t.zeros(1, dtype=t.int32, device="cuda"), t.zeros(1, 2, 8, dtype=t.int32, device="cuda")
+        before = [x.clone() for x in (b.k, b.v, ma, mb)]
+
+        def call(k=b.k, v=b.v, ks=b.ks, vs=b.vs, m=mb, table=b.table, first=None):
+            gk.gk_paged_evict(ctx, a.h, ma, gk.PagedKv(k, v, ks, vs, table, new), m, first, 8, 2, new, kept, 1)
+
+        bad = [dict(m=ma), dict(v=a.v), dict(k=a.k), dict(k=a.k, v=a.v, ks=a.ks, vs=a.vs), dict(v=a.v, m=ma), dict(first=new)]
+        for args in bad + ([dict(ks=a.ks), dict(vs=a.vs), dict(k=a.k, v=a.v, m=ma)] if q8 else []):
+            refused(gk.GK_ERR_ARG, lambda: call(**args))
+        gk.gk_sync(ctx)
+        assert all(t.equal(x, y) for x, y in zip((b.k, b.v, ma, mb), before)) and (new == 0).all()
+        call()
+        gk.gk_sync(ctx)
+        assert new.tolist() == [8]
     ctx.close()
