@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 from oracle import serving
-from tests.test_gpu_paged_more import attend_shared, shared_cache, shared_ref
+from tests.test_gpu_paged_more import attend_shared, shared_cache, shared_ref, to_pages, weigh
 from tests.test_gpu_serving import Dev, check_attention, dev, refused, starts
 from tests.test_oracle_serving import cache
 
@@ -173,6 +173,69 @@ def test_shared_8_bit_prefixes_leave_room_for_the_parts(width, mib):
     y, lse = attend_shared(ctx, c, q, ns, gs, pl, 0.088, max_group=63, fails=True)
     assert (y == 3).all() and (lse == 3).all()
     ctx.close()
+
+
+# ---------------------------------------------------------------------------------------------- mass
+# With scores near zero a weight is 2^(-l) alone, l the row's log sum in powers of two, and what is lost on the way from lse to
+# the weight shows. In tiles it goes through a product, of 1 / f and -l in three bf16 parts each (a part rounds by 2^-9, so
+# three leave 2^-27): its one step may cut the sum twice by a step of float32 (2 2^-23 |l|), and lse log2(e), 1 / f, the products of
+# parts that are left out and the result times f each round by at most 2^-24 |l|: |l| 2^-21 in all, as the exponential's argument, so
+# times ln 2 relative to the weight. The exponential itself: 2^-22. Scores: sums of hs products with scale sum |q||k| < 2^-4.9 (asserted),
+# hs + 16 cuts of 2^-23 of that: below 2^-20.7. A key's sum over its N rows and heads: at most min(N, 48) additions in a chain (a
+# thread has four sums of a tile's 128 rows, then joins them, and there are three pairs of tiles at most): 2^-24 each.
+# A log sum of two parts would be off by up to 2^-18 |l|; one whose step comes first in the product is cut hs / 16 times more, always to the
+# same side: by |l| 2^-24 in the mean each time, which the sum over all keys shows (there the chains' roundings average out).
+def mass_and_bounds(c, q, lse, n, scale):
+    """{place: (mass, bound)} in 64 bits, and the sums over all keys of both without the chains' roundings."""
+    qs, G, out, total = starts(n), q.shape[1] // c.Hkv, {}, np.zeros(2)
+    for b in range(len(n)):
+        kv = int(c.kv_len[b])
+        pos = np.arange(kv)
+        pg, rw = (np.array(x) for x in zip(*(c.place(b, j) for j in range(kv))))
+        k = np.stack([c.vector("k", p, r) for p, r in zip(pg, rw)])  # [kv, Hkv, hs]
+        rows = slice(qs[b], qs[b + 1])
+        seen = pos[None] <= (kv - n[b] + np.arange(n[b]))[:, None]
+        for hk in range(c.Hkv):
+            heads = slice(hk * G, hk * G + G)
+            z = scale * np.einsum("ihd,jd->ihj", q[rows, heads].astype(np.float64), k[:, hk])
+            l = lse[rows, heads].astype(np.float64)[..., None]
+            size = scale * np.einsum("ihd,jd->ihj", np.abs(q[rows, heads]).astype(np.float64), np.abs(k[:, hk]))
+            assert size.max() < 2.0 ** -4.9
+            w = np.exp(z - l) * seen[:, None]
+            bound = w * (np.abs(l) * 2.0 ** -21 + 2.0 ** -22 + 2.0 ** -20.7)  # (|l| log2(e) ln(2) = |lse|)
+            m, e = w.sum((0, 1)), bound.sum((0, 1))
+            total += m.sum(), (w * (np.abs(l) * 2.0 ** -22 + 2.0 ** -22 + 2.0 ** -20.7)).sum()
+            chain = np.minimum(seen.sum(0) * G, 48) * 2.0 ** -24
+            for j in range(kv):
+                out[pg[j], hk, rw[j]] = m[j], e[j] + chain[j] * m[j]
+    return out, total
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("kv_len,n,H,Hkv,hs,page", [
+    ([300, 700, 90, 1500], [70, 90, 66, 80], 4, 4, 64, 16),
+    ([2000, 400, 130], [128, 100, 129], 3, 3, 128, 64),
+    ([600, 1800], [33, 40], 8, 4, 96, 32),
+    ([900, 128], [30, 20], 4, 1, 128, 128),
+    ([500, 90, 1700], [1, 3, 2], 8, 4, 64, 32),  # few rows: scores in registers
+    ([500, 90, 1700], [16, 9, 12], 8, 2, 128, 64),
+])
+def test_mass_keeps_float32_of_the_log_sums(gkctx, kv_len, n, H, Hkv, hs, page, q8):
+    rng = np.random.default_rng(4300 + hs + len(n))
+    c = cache(rng, kv_len, Hkv, hs, page, q8)
+    q = serving.bf16(rng.standard_normal((sum(n), H, hs)) * 2.0 ** -9)
+    scale = hs ** -0.5
+    # log sums as attention leaves them, and others that spread over more sizes
+    lse = serving.paged_attn(c, q, starts(n), scale)[1]
+    for ls in (lse, lse + rng.uniform(-1, 6, lse.shape)):
+        ls = ls.astype(np.float32)
+        got = weigh(gkctx, c, q, ls, n, scale)
+        want, total = mass_and_bounds(c, q, ls, n, scale)
+        at = tuple(np.array(x) for x in zip(*want))
+        m, e = (np.array(x) for x in zip(*want.values()))
+        off = np.abs(got[at] - m)
+        assert (off <= e).all(), (float((off / e).max()), int((off > e).sum()), len(e))
+        assert abs(got[at].astype(np.float64).sum() - total[0]) <= total[1], (got[at].astype(np.float64).sum() - total[0]) / total[1]
 
 
 # ------------------------------------------------------------------------------------------ refusals
