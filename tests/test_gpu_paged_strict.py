@@ -238,6 +238,29 @@ def test_mass_keeps_float32_of_the_log_sums(gkctx, kv_len, n, H, Hkv, hs, page, 
         assert abs(got[at].astype(np.float64).sum() - total[0]) <= total[1], (got[at].astype(np.float64).sum() - total[0]) / total[1]
 
 
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("kv_len,n,H,Hkv,hs,first", [([300, 130], [1, 4], 4, 2, 64, [7, 0]), ([700, 260], [100, 65], 2, 2, 128, [0, 129]),
+                                                     ([400], [70], 3, 1, 80, None)])
+def test_mass_in_place_gives_the_bits_of_another_array(gkctx, kv_len, n, H, Hkv, hs, first, q8):
+    """At every weighed key, and nothing else is touched."""
+    rng = np.random.default_rng(4400 + hs)
+    c = cache(rng, kv_len, Hkv, hs, 16, q8)
+    q = serving.bf16(rng.standard_normal((sum(n), H, hs)) * 2)
+    scale = hs ** -0.5
+    lse = serving.paged_attn(c, q, starts(n), scale)[1].astype(np.float32)
+    first = None if first is None else np.array(first, np.int32)
+    weighed = np.zeros(c.k.shape[:3], bool)
+    for at in serving.paged_mass(c, q, lse, starts(n), scale, first=first):
+        weighed[at] = True
+    assert weighed.any() and not weighed.all()
+    old = rng.uniform(0, 2, weighed.shape).astype(np.float32)
+    apart = weigh(gkctx, c, q, lse, n, scale, old=dev(old), decay=0.75, first=first, mass=dev(np.full(old.shape, 5, np.float32)))
+    mass = dev(old)
+    in_place = weigh(gkctx, c, q, lse, n, scale, old=mass, decay=0.75, first=first, mass=mass)
+    assert np.array_equal(in_place[weighed], apart[weighed]) and (in_place[weighed] != old[weighed]).all()
+    assert np.array_equal(in_place[~weighed], old[~weighed]) and (apart[~weighed] == 5).all()
+
+
 # ------------------------------------------------------------------------------------------ refusals
 def test_evict_refuses_pools_that_share_some_arrays():
     """Two pools with one array of values, of steps or of masses would be read and written at unlike places; new_len over first
