@@ -261,6 +261,74 @@ def test_mass_in_place_gives_the_bits_of_another_array(gkctx, kv_len, n, H, Hkv,
     assert np.array_equal(in_place[~weighed], old[~weighed]) and (apart[~weighed] == 5).all()
 
 
+@pytest.mark.parametrize("n,H,Hkv,hs,q8", [(1, 4, 2, 64, True), (1, 8, 2, 128, False), (90, 4, 2, 128, True), (200, 2, 2, 64, False)])
+def test_mass_and_evict_replayed_on_other_lengths(n, H, Hkv, hs, q8):
+    """A captured call against an eager one, all outputs (scales among them) after each replay: lengths, page tables, `first` and
+    inputs change between them, and the last of them is not what was captured either."""
+    from gpt_decoder_gb300 import gk
+
+    t = _t()
+    rng = np.random.default_rng(4500 + n + hs)
+    c = cache(rng, [1500, 900], Hkv, hs, 64, q8)
+    to = to_pages(rng, c, [300, 300], False)
+    w, qs = H * hs, dev(starts([n, n]))
+    d, td = Dev(c, poison=False), Dev(to, poison=False)
+    q = dev(serving.bf16(rng.standard_normal((2 * n, w))), t.bfloat16)
+    lse, first = t.zeros(2 * n, H, device="cuda"), dev(np.array([20, 0], np.int32))
+
+    class Out:
+        def __init__(self):
+            self.mass, self.to_mass = t.zeros(c.k.shape[:3], device="cuda"), t.zeros(to.k.shape[:3], device="cuda")
+            self.k, self.v = (t.zeros_like(x) for x in (td.k, td.v))
+            self.ks, self.vs = (None if x is None else t.zeros_like(x) for x in (td.ks, td.vs))
+            self.new, self.kept = t.zeros(2, dtype=t.int32, device="cuda"), t.zeros(2, Hkv, 280, dtype=t.int32, device="cuda")
+            self.h = gk.PagedKv(self.k, self.v, self.ks, self.vs, td.table, self.new)
+
+        def all(self):
+            return [x for x in (self.mass, self.to_mass, self.k, self.v, self.ks, self.vs, self.new, self.kept) if x is not None]
+
+    def call(ctx, o):
+        y = spare
+        gk.gk_paged_attn(ctx, d.h, gk.GK_BF16, q, w, y, w, lse, qs, 2, H, 2 * n, n, 0.125)
+        gk.gk_paged_mass(ctx, d.h, gk.GK_BF16, q, w, lse, None, 1.0, o.mass, first, qs, 2, H, 2 * n, n, 0.125)
+        gk.gk_paged_evict(ctx, d.h, o.mass, o.h, o.to_mass, first, 280, 30, o.new, o.kept, 2)
+
+    spare = t.zeros(2 * n, w, dtype=t.bfloat16, device="cuda")
+    side = t.cuda.Stream()
+    ctx, o = gk.Ctx(side, workspace_bytes=16 << 20), Out()
+    eager = gk.Ctx(t.cuda.current_stream().cuda_stream, workspace_bytes=16 << 20)
+    t.cuda.synchronize()
+    g = t.cuda.CUDAGraph()
+    with t.cuda.graph(g, stream=side):
+        call(ctx, o)
+    turned = c.table[:, ::-1].copy()
+    turned[1, :] = np.where(c.table[1] < 0, -1, c.table[1])
+    for lens, firsts, table in (([n, n + 3], [0, 1], c.table), ([700, 900], [20, 0], c.table), ([n + 1300, 280], [9, 130], turned), ([1499, 281], [3, 7], c.table)):
+        d.kv_len.copy_(dev(np.array(lens, np.int32)))
+        first.copy_(dev(np.array(firsts, np.int32)))
+        d.table.copy_(dev(table))
+        q.copy_(dev(serving.bf16(rng.standard_normal((2 * n, w))), t.bfloat16))
+        for x in o.all():
+            x.zero_()
+        t.cuda.synchronize()
+        g.replay()
+        t.cuda.synchronize()
+        want = Out()
+        call(eager, want)
+        gk.gk_sync(eager)
+        assert all(t.equal(a, b) for a, b in zip(o.all(), want.all())) and o.mass.abs().sum() > 0
+        # and those against the oracle: the lengths that the call saw are these
+        now = serving.Pages(c.k, c.v, c.k_scale, c.v_scale, table, np.array(lens, np.int32))
+        blank = serving.Pages(*(None if x is None else np.zeros_like(x) for x in (to.k, to.v, to.k_scale, to.v_scale)), to.table, to.kv_len)
+        mass = o.mass.cpu().numpy()
+        new_len, kept = serving.paged_evict(now, mass, blank, np.zeros(to.k.shape[:3], np.float32), np.array(firsts, np.int32), 280, 30)
+        assert np.array_equal(o.new.cpu().numpy(), new_len) and np.array_equal(o.kept.cpu().numpy(), kept)
+        assert np.array_equal(o.k.float().cpu().numpy(), blank.k.astype(np.float32))
+    gk.gk_sync(ctx)
+    ctx.close()
+    eager.close()
+
+
 # ------------------------------------------------------------------------------------------ refusals
 def test_evict_refuses_pools_that_share_some_arrays():
     """Two pools with one array of values, of steps or of masses would be read and written at unlike places; new_len over first
