@@ -3,13 +3,15 @@
 // a KV cache" (the cache that grows by a row a token; here it is held to a size).
 //
 // Two launches. Select: a cluster of blocks per sequence and key / value head holds the head's masses in shared memory, as
-// integers that order like them, and finds the n-th largest by its bits: three digits of 11, 11 and 10 bits, for each a
-// histogram of what still matches, summed over the cluster through distributed shared memory. Then each warp counts what
-// stays of its stretch of positions and walks it, so the positions come out in order without a sort: keys above the
-// n-th, and the first of those equal to it. Move: those rows, with scales and mass, a tile of tokens a block.
+// integers that order like them (a table wider than its blocks can hold, 49152 positions each and up to eight blocks where
+// sequences are few, has them read again each time), and finds the n-th largest by its bits: three digits of 11, 11 and
+// 10 bits, for each a histogram of what still matches, summed over the cluster through distributed shared memory. Then each
+// warp counts what stays of its stretch of positions and walks it, so the positions come out in order without a sort: keys
+// above the n-th, and the first of those equal to it. Move: those rows, with scales and mass, a tile of tokens a block.
 // The bytes of what moves bound it where there are many: 48 sequences of up to 8191 tokens to 2064, 8 heads of 128, bf16:
-// 127 us, 5.9 TB/s (0.89 of a copy), the selection 15 of them; 3 of up to 65536 to 8256 52 us, 19 the selection (a chain:
-// page ids, masses, three digits at about 2.5 us, the walk). One of 1100 to 516, 12 heads of 64: 8.8 us, two launches.
+// 128 us, 5.9 TB/s (0.89 of a copy), the selection 15 of them; 3 of up to 65536 to 8256 52 us, 19 the selection (a chain:
+// page ids, masses, three digits at about 2.5 us, the walk). One of 1100 to 516, 12 heads of 64: 9.1 us, two launches. Clusters
+// and shared memory go by the table's width: with tables of 65536 positions the 48 take 136 us, the one 17.
 #include <math.h>
 
 #include <algorithm>
@@ -336,6 +338,10 @@ extern "C" gk_status gk_paged_evict(gk_ctx* ctx, const gk_paged_kv* cache, const
     } else {
         GK_TRY(launch_dependent(ctx, "paged_evict_select", evict_select_kernel<false>, grid, dim3(SELECT), 0, blocks, a, each));
     }
-    const int64_t tiles = cdiv(std::min(budget, a.from.capacity), TOKENS);
+    // A block a tile of the budget. The first tokens move too, and only the device knows their number: where a table has room
+    // for more of them than for a few budgets, eight blocks an SM (first 8192 and a budget of 256, 8 sequences, 8 heads of 128:
+    // 58 us, 145 with the budget's blocks alone; one sequence of 1100 with a budget of 512 would take 9.3 instead of 9.1).
+    int64_t tiles = cdiv(std::min(budget, a.from.capacity), TOKENS);
+    if (first && a.from.capacity / 4 > budget) tiles = std::max(tiles, std::min(cdiv(a.from.capacity, TOKENS), cdiv(8 * (int64_t)ctx->num_sms, (int64_t)a.from.Hkv * B)));
     return launch_dependent(ctx, "paged_evict_move", evict_move_kernel, dim3((unsigned)tiles, (unsigned)a.from.Hkv, (unsigned)B), dim3(MOVE), 0, 1, a);
 }

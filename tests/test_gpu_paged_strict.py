@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 from oracle import serving
-from tests.test_gpu_paged_more import attend_shared, shared_cache, shared_ref, to_pages, weigh
+from tests.test_gpu_paged_more import attend_shared, check_evict, evict, shared_cache, shared_ref, to_pages, weigh
 from tests.test_gpu_serving import Dev, check_attention, dev, refused, starts
 from tests.test_oracle_serving import cache
 
@@ -327,6 +327,23 @@ def test_mass_and_evict_replayed_on_other_lengths(n, H, Hkv, hs, q8):
     gk.gk_sync(ctx)
     ctx.close()
     eager.close()
+
+
+# ---------------------------------------------------------------------------------------------- eviction
+@pytest.mark.parametrize("one_pool", [False, True])
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("kv_len,first,budget,recent,Hkv,hs,page", [([9000, 300], [8500, 64], 16, 4, 2, 64, 64), ([4100] * 20, [4000] * 20, 1, 0, 4, 16, 16),
+                                                                    ([20000], [19999], 64, 32, 1, 32, 256)])
+def test_evict_of_first_tokens_far_above_the_budget(gkctx, kv_len, first, budget, recent, Hkv, hs, page, q8, one_pool):
+    """Every one of the first tokens moves, whatever the number of blocks that the budget gives."""
+    rng = np.random.default_rng(4600 + budget)
+    c = cache(rng, kv_len, Hkv, hs, page, q8)
+    first = np.array(first, np.int32)
+    to = to_pages(rng, c, np.minimum(kv_len, first + budget), one_pool)
+    mass = np.exp(rng.standard_normal(c.k.shape[:3]) * 3).astype(np.float32)
+    to_mass = mass if one_pool else np.full(to.k.shape[:3], 3, np.float32)
+    got = evict(gkctx, c, mass, to, to_mass, first, budget, recent)
+    check_evict(got, c, mass, to, to_mass, first, budget, recent)
 
 
 # ------------------------------------------------------------------------------------------ refusals
