@@ -167,7 +167,7 @@ extern "C" gk_status gk_paged_attn_shared(gk_ctx* ctx, const gk_paged_kv* cache,
     p.max_q = a.max_group;
     int64_t prefix_splits, own_splits;
     const int64_t pairs = prefix_few ? 1 : cdiv(group_rows, 256);  // blocks a prefix and head
-    split_prefixes(ctx, prefix_few, n_groups * a.p.Hkv * pairs, a.p.capacity, &prefix_splits, &p.min_split);
+    split_prefixes(ctx, prefix_few, (int64_t)n_groups * a.p.Hkv * pairs, a.p.capacity, &prefix_splits, &p.min_split);
     split_own(ctx, own_few, (int64_t)B * a.p.Hkv * (own_few ? 1 : cdiv(own_rows, 256)), a.p.capacity, &own_splits, &a.min_split);
     if (room < info + 2 * per) return gk_paged_attn(ctx, cache, dtype, q, ldq, y, ldy, lse, q_start, B, H, rows, max_q, scale);
     if (!prefix_few && a.p.k_scale && (a.p.hs > 64 || group_rows > 512)) {
