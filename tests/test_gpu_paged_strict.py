@@ -346,6 +346,22 @@ def test_evict_of_first_tokens_far_above_the_budget(gkctx, kv_len, first, budget
     check_evict(got, c, mass, to, to_mass, first, budget, recent)
 
 
+@pytest.mark.parametrize("B,Hkv,width", [(1, 2, 390000), (160, 4, 48896), (2, 3, 16400)])
+def test_evict_of_tables_as_wide_as_the_blocks_hold(gkctx, B, Hkv, width):
+    """Close under what a block's shared memory has room for, in clusters of eight and alone."""
+    rng = np.random.default_rng(4700 + B)
+    page = 16
+    lens = [int(x) for x in rng.integers(100, 900, B)]
+    lens[0] = 9000
+    c = cache(rng, lens, Hkv, 16, page, False)
+    c.table = np.pad(c.table, ((0, 0), (0, width // page - c.table.shape[1])), constant_values=-1)
+    to = to_pages(rng, c, np.minimum(lens, 90), False)
+    mass = np.exp(rng.standard_normal(c.k.shape[:3]) * 3).astype(np.float32)
+    to_mass = np.full(to.k.shape[:3], 3, np.float32)
+    got = evict(gkctx, c, mass, to, to_mass, None, 90, 20)
+    check_evict(got, c, mass, to, to_mass, None, 90, 20)
+
+
 # ------------------------------------------------------------------------------------------ refusals
 def test_evict_refuses_pools_that_share_some_arrays():
     """Two pools with one array of values, of steps or of masses would be read and written at unlike places; new_len over first
