@@ -9,12 +9,13 @@
 // bytes are read once instead of S times, and the rows that meet a key are S times as many, which is what the tensor
 // cores need. Then each sequence attends to its own keys. Both are the kernels of gk_paged_attn, launched beside each
 // other (Branch, launch.cuh).
-// Measured: a token of 64 sequences behind 16384 shared 8-bit keys and up to 1024 own ones, 32 heads over 8 of 128: 81 us
-// (gk_paged_attn 365): 19 own keys beside 23 that lay the codes out as bf16, 42 the prefix in tiles of 128 rows (8 key
-// tiles a block at 2.7 us, its softmax warps' rate for codes, and 15 to begin and end), 10 the join; bf16 pages 56. 7
-// groups of up to 16 sequences behind up to 8100 keys, 12 heads of 64, bf16: 41 us, 3.1 TB/s (122): blocks of few tiles, a
-// third of their time the loads that lead to the first key. Chunks of 256 behind 16384 keys, 12 sequences a group: 782
-// (787): the tensor cores' part bounds both.
+// Measured: a token of 64 sequences behind 16384 shared 8-bit keys and up to 1024 own ones, 32 heads over 8 of 128: 82 us
+// (gk_paged_attn 361): 23 to lay the codes out as bf16, beside the own keys, 49 the prefix in tiles of 128 rows (8 key tiles a
+// block at its softmax warps' rate for codes and weights in two parts, and 15 to begin and end), 10 the join; bf16 pages 63
+// (539). 7 groups of up to 16 sequences behind up to 8100 keys, 12 heads of 64, bf16: 43 us, 3.0 TB/s (121): blocks of few
+// tiles, a third of their time the loads that lead to the first key; 8 bits 33 (119). Chunks of 256 behind 16384 keys, 12
+// sequences a group: 717 (784), as own keys fill the SMs that the prefixes' last wave leaves; the tensor cores' part bounds
+// both. 8 bits, 256 MB of workspace: 1049 (3431, whose codes have no room as bf16).
 #include <math.h>
 
 #include <algorithm>
@@ -104,8 +105,8 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) shared_join_kernel(const Attn
 bool is_few(const AttnArgs& a, int64_t rows) { return rows <= (a.p.k_scale ? 64 : 32); }
 
 // Pieces of the prefixes' `units` (groups, heads, pairs of row tiles). Few rows: four or sixteen blocks an SM, as
-// for gk_paged_attn, but pieces of 512 where there are some groups (7 of up to 8100 keys, 12 heads of 64: 44.5 us against
-// 50 with pieces of 256). Tiles: one wave, pieces of 256 at least.
+// for gk_paged_attn, but pieces of 512 where there are some groups (7 of up to 8100 keys, 12 heads of 64: 43.1 us against
+// 47.7 with pieces of 256). Tiles: one wave, pieces of 256 at least.
 void split_prefixes(gk_ctx* ctx, bool few, int64_t units, int capacity, int64_t* splits, int* least) {
     const bool alone = units < ctx->num_sms / 2;
     *least = !few ? 256 : alone ? 128 : 512;
@@ -113,7 +114,7 @@ void split_prefixes(gk_ctx* ctx, bool few, int64_t units, int capacity, int64_t*
     *splits = std::max<int64_t>(1, std::min(*splits, cdiv(capacity, *least)));
 }
 // And of what follows them: mostly short, so pieces of 256 and two of them at most once they fill the GPU (64 sequences of
-// up to 1024 own keys, 8 heads: two pieces 85.3 us in all, five 87.2, five of 1024 93.7; 54 sequences 49.1, 50.2, 49.2).
+// up to 1024 own keys, 8 heads: two pieces 82.2 us in all, five 86.0, five of 1024 91.1; 54 sequences 43.1, 44.8, 48.0).
 void split_own(gk_ctx* ctx, bool few, int64_t units, int capacity, int64_t* splits, int* least) {
     *least = few ? (units < ctx->num_sms / 2 ? 128 : 256) : 1024;
     *splits = few ? std::max<int64_t>(2, cdiv(4 * (int64_t)ctx->num_sms, units)) : cdiv((int64_t)ctx->num_sms, units);
@@ -141,11 +142,13 @@ extern "C" gk_status gk_paged_attn_shared(gk_ctx* ctx, const gk_paged_kv* cache,
     GK_REQUIRE(ctx, std::min<int64_t>(max_group_q, rows) * a.G < (1ll << 30), GK_ERR_UNSUPPORTED,
                "gk_paged_attn_shared: groups of %d rows of %d heads a key / value head", max_group_q, a.G);
     if (rows == 0) return GK_OK;
-    // Sharing costs two launches more and a join, and wins from prefixes of about 2000 positions and two sequences a group on
-    // (a token of 16 / 64 sequences, 12 heads of 64, prefixes of 250 / 1000 / 4000 / 16000: 10.5 / 12.6 / 14.8 / 24 us
-    // against 7 / 18 / 35 / 95 for each alone, and 19 / 27 / 29 / 45 against 14 / 36 / 96 / 324; 32 heads over 8 of 128,
-    // 64 sequences: 33 / 43 / 47 / 50 against 19 / 48 / 142 / 518; 2 sequences of 4000 / 16000: 12 / 17 against 12 / 20).
-    // The lengths are on the device; the table's width bounds them.
+    // Sharing costs two launches, a branch and a join, and wins from about 1000 positions on for a token of many sequences, from
+    // more for wide heads and for chunks. Tables of 4096 positions, prefixes of 250 / 1000 / 2000 / 3900, a token of one group
+    // (against each sequence alone): 12 heads of 64, bf16, 16 sequences 12.5 / 12.5 / 13.6 / 15.9 us (11 / 21 / 22 / 37), 64 of
+    // them 17 / 18 / 21 / 25 (19 / 38 / 55 / 93); 32 heads over 8 of 128, 8 bits, 16 of them 21 / 21 / 21 / 24 (13 / 19 / 26 / 39),
+    // 64 39 / 40 / 42 / 44 (20 / 42 / 63 / 101); 2 sequences 11 to 13.5 (6 to 10), which win from 16000 on (16.6 against 20). 16
+    // chunks of 256 behind 1000, 32 heads over 8 of 128, bf16: 193 (100), 8 bits 211 (133); behind 8000 494 (942). The lengths are
+    // on the device; the table's width bounds them, and one border stands for all of these.
     if (a.p.capacity < 2048 || 2 * (int64_t)n_groups > B) return gk_paged_attn(ctx, cache, dtype, q, ldq, y, ldy, lse, q_start, B, H, rows, max_q, scale);
     a.group_start = group_start;
     a.prefix_len = prefix_len;
@@ -201,7 +204,8 @@ extern "C" gk_status gk_paged_attn_shared(gk_ctx* ctx, const gk_paged_kv* cache,
     a.part_o = p.part_o = reinterpret_cast<float*>(ws + info);
     a.part_ml = p.part_ml = reinterpret_cast<float2*>(a.part_o + rows * H * a.slots * a.p.hs);
     // The own keys' launch beside the prefixes': neither reads what the other writes, and each by itself leaves much of the
-    // GPU idle (one after the other: 64 samples 82.5 us, 7 groups 44.7, chunks 806; side by side 77.6, 43.1, 712).
+    // GPU idle (one after the other: 64 samples, then with weights of one part, 82.5 us, 7 groups 44.7, chunks 806; side by
+    // side 77.6, 43.1, 714).
     const bool expanded = p.expanded_k && p.heads == a.p.Hkv;
     Branch own(ctx);
     GK_TRY(own.fork());
