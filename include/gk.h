@@ -68,9 +68,10 @@ typedef struct gk_ctx gk_ctx;
 /* ------------------------------------------------------------------------------ context */
 
 /* Create a context bound to `cuda_stream` (a cudaStream_t; NULL = the legacy default
- * stream) on the current device. It allocates a device error word and `workspace_bytes`
- * of device scratch used by the calls that need scratch (each says how much). Returns
- * GK_ERR_CUDA if an allocation fails. Not thread-safe: one context per host thread. */
+ * stream) on the current device. It allocates a device error word, `workspace_bytes`
+ * of device scratch used by the calls that need scratch (each says how much), and a stream of its own for
+ * what a call launches beside the work on `cuda_stream` (all of it lies between what was on that stream
+ * before the call and what comes after). Returns GK_ERR_CUDA if an allocation fails. Not thread-safe: one context per host thread. */
 gk_status gk_ctx_create(gk_ctx** out, void* cuda_stream, size_t workspace_bytes);
 void gk_ctx_destroy(gk_ctx* ctx);
 /* Rebind the stream (e.g. to the stream a graph capture runs on). */

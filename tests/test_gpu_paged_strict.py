@@ -87,6 +87,10 @@ def test_shared_sees_what_was_launched_before_and_keeps_it_from_what_follows(S, 
             g.replay()
             t.cuda.synchronize()
             assert all(t.equal(a, b) for a, b in zip(taken(), want))
+        with t.cuda.stream(stream):  # and not captured again, by the context that was
+            run(ctx, lambda: None)
+        t.cuda.synchronize()
+        assert all(t.equal(a, b) for a, b in zip(taken(), want))
         gk.gk_sync(ctx)
     ctx.close()
 
